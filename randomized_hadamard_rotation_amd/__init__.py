@@ -378,3 +378,12 @@ def rhtq_stream_floor(x, packed, scales, stream=None):
                                  ctypes.c_void_p(st.cuda_stream)), "rhtq_stream_floor")
     _keep_for(st, other, xc if xc is not x else None)
     return packed, scales
+
+
+try:   # the serving calls are typed by torch; without torch the host helpers above still work
+    from .serving import (EXPORTED_SERVING, RhtqCache, rhtq_cache_append, rhtq_cache_new, rhtq_cache_read,  # noqa: F401
+                          rhtq_matvec, rhtq_paged_attention, rhtq_pages_compact, rhtq_pages_copy, rhtq_pages_fork,
+                          rhtq_pages_free, rhtq_pages_reserve, rhtq_pages_trim, rhtq_serving_version)
+except ImportError as _e:
+    if _e.name != "torch":
+        raise

@@ -1,0 +1,414 @@
+"""What uses 4-bit rows when a model answers: products with quantised weights and a paged 4-bit key-value cache.
+
+The functions carry the names of the C entry points in include/serving/rhtq_serving.h and, like the others, only
+marshal arguments: torch provides device memory and the current HIP stream, every step runs in the library's
+kernels, and nothing is read back to the host.  They are exported by the package itself.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import NamedTuple
+
+import torch
+
+from . import (_DEFAULT_GROUP, _DEFAULT_SCALE, _FMT, _SCALE, RHTQ_IN_BF16, RHTQ_IN_F16, RHTQ_IN_F32, RHTQ_SCALE_F16,
+               RHTQ_SCALE_F32, _check, _expect, _keep_for, _resolve_stream, _same_device, _scale_torch_dtype,
+               _signs_tensor, lib, scale_shape)
+
+EXPORTED_SERVING = ["rhtq_serving_version", "rhtq_matvec_workspace", "rhtq_matvec", "rhtq_cache_append", "rhtq_cache_read",
+                    "rhtq_paged_attention_workspace", "rhtq_paged_attention", "rhtq_pages_workspace", "rhtq_pages_reserve",
+                    "rhtq_pages_free", "rhtq_pages_trim", "rhtq_pages_fork", "rhtq_pages_copy", "rhtq_pages_compact"]
+
+_IN = {torch.bfloat16: RHTQ_IN_BF16, torch.float16: RHTQ_IN_F16, torch.float32: RHTQ_IN_F32}
+_SCALE_OF = {torch.float32: RHTQ_SCALE_F32, torch.float16: RHTQ_SCALE_F16}
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("layers", ctypes.c_int32), ("pages", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("page", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("scale_dtype", ctypes.c_int32)]
+
+
+def _declare():
+    vp, i32, i64, ci, fl = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+    cache = ctypes.POINTER(_CacheStruct)
+    args = {
+        "rhtq_serving_version": (ci, []),
+        "rhtq_matvec_workspace": (i64, [i64, i32]),
+        "rhtq_matvec": (ci, [vp, ci, i64, i32, i32, vp, ci, vp, vp, vp, i64, ci, i32, ci, vp, ci, vp, i64, vp]),
+        "rhtq_cache_append": (ci, [cache, vp, vp, ci, i64, i64, i64, i64, i64, vp, i32, vp, vp, i32, vp, vp, vp]),
+        "rhtq_cache_read": (ci, [cache, vp, vp, ci, i64, vp, i32, vp, vp, i32, vp, vp, vp]),
+        "rhtq_paged_attention_workspace": (i64, [i32] * 8),
+        "rhtq_paged_attention": (ci, [vp, ci, i32, i32, i64, i64, cache, vp, i32, vp, vp, vp, fl, i32, i32, vp, vp, i64, vp]),
+        "rhtq_pages_workspace": (i64, [i32, i32, i32]),
+        "rhtq_pages_reserve": (ci, [vp, i32, vp, i32, vp, i32, i32, vp, vp, vp, i64, vp]),
+        "rhtq_pages_free": (ci, [vp, i32, vp, i32, vp, i32, vp, i32, vp]),
+        "rhtq_pages_trim": (ci, [vp, i32, vp, i32, vp, i32, i32, i32, i32, vp]),
+        "rhtq_pages_fork": (ci, [cache, vp, i32, vp, i32, vp, vp, vp, i32, vp, vp, i64, vp]),
+        "rhtq_pages_copy": (ci, [cache, vp, vp, i32, vp]),
+        "rhtq_pages_compact": (ci, [cache, vp, i32, i32, vp, vp, vp, i64, vp]),
+    }
+    for name, (res, types) in args.items():
+        f = getattr(lib, name)
+        f.restype, f.argtypes = res, types
+
+
+_declare()
+
+
+class RhtqCache(NamedTuple):
+    """One layer's paged cache, or with a leading axis every layer's: codes uint8 [.., pages, kv_heads, page, head_dim/2], scales
+    float16 or float32 [.., pages, kv_heads, page].  Page calls take every layer at once; append, read and attention one."""
+    k_codes: torch.Tensor
+    k_scales: torch.Tensor
+    v_codes: torch.Tensor
+    v_scales: torch.Tensor
+
+    def layer(self, i: int) -> "RhtqCache":
+        return RhtqCache(*(t[i] for t in self))
+
+
+def rhtq_cache_new(pages: int, kv_heads: int, page: int, head_dim: int, scale_dtype: str = "f16", layers: int | None = None,
+                   device="cuda") -> RhtqCache:
+    """A cache of zero rows, with a leading axis if `layers` is given."""
+    if scale_dtype not in ("f16", "f32"):
+        raise ValueError("scale_dtype must be 'f16' or 'f32'")
+    if head_dim not in (64, 128, 256):
+        raise ValueError("head_dim must be 64, 128 or 256")
+    if page < 16 or page > 256 or page & (page - 1):
+        raise ValueError("page must be a power of two from 16 to 256")
+    shape = (() if layers is None else (layers,)) + (pages, kv_heads, page)
+    sdt = _scale_torch_dtype(scale_dtype)
+    return RhtqCache(*(torch.zeros(s, dtype=d, device=device) for s, d in
+                       2 * (((*shape, head_dim // 2), torch.uint8), (shape, sdt))))
+
+
+def _cache_struct(cache, layered):
+    """The C struct of a cache whose four tensors agree; with `layered`, a leading axis is taken."""
+    k, ks, v, vs = cache
+    dims = k.dim()
+    if dims != 4 and not (layered and dims == 5):
+        raise ValueError("k_codes must be [pages][kv_heads][page][head_dim/2]" + (", with layers in front or not" if layered else ""))
+    if k.dtype != torch.uint8:
+        raise ValueError(f"k_codes: dtype {k.dtype}, expected torch.uint8")
+    if ks.dtype not in _SCALE_OF:
+        raise ValueError(f"k_scales: dtype {ks.dtype}, expected float16 or float32")
+    shape = k.shape
+    _expect(k, "k_codes", torch.uint8, shape)
+    _expect(ks, "k_scales", ks.dtype, shape[:-1])
+    _expect(v, "v_codes", torch.uint8, shape)
+    _expect(vs, "v_scales", ks.dtype, shape[:-1])
+    return _CacheStruct(k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(), shape[0] if dims == 5 else 1, shape[-4],
+                        shape[-3], shape[-2], 2 * shape[-1], _SCALE_OF[ks.dtype])
+
+
+def _int32(t, name, shape):
+    _expect(t, name, torch.int32, shape)
+
+
+def _cache_signs(signs, dim, device):
+    return None if signs is None else _signs_tensor(signs, dim, device)
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def rhtq_serving_version() -> int:
+    return lib.rhtq_serving_version()
+
+
+def rhtq_matvec(packed, scales, x, signs=None, fmt: str = "int4", group: int = 0, scale_dtype: str | None = None,
+                tensor_scale=None, rotated: bool = False, block=None, out=None, out_dtype=None, stream=None):
+    """y [tokens][rows] = x [tokens][n] times the transpose of the matrix that rhtq_inverse(packed, scales, n, signs, ...) gives:
+    rows quantised by rhtq_forward are weights, used as they lie.  x is bfloat16, float16 or float32; y has its type unless `out`
+    or out_dtype says otherwise.  rotated = True: x is rhtq_rotate(x, signs) already (one rotation serves several weights).
+    fmt, group, scale_dtype, tensor_scale and block as in rhtq_forward."""
+    if fmt not in _FMT:
+        raise ValueError(f"unknown fmt {fmt!r}")
+    if x.dim() != 2 or packed.dim() != 2:
+        raise ValueError("x must be 2-D [tokens][n] and packed 2-D [rows][n/2]")
+    if x.dtype not in _IN:
+        raise ValueError("x must be bfloat16, float16 or float32")
+    tokens, n = x.shape
+    rows = packed.shape[0]
+    if scale_dtype is None:
+        scale_dtype = _DEFAULT_SCALE[fmt]
+    if group == 0:
+        group = _DEFAULT_GROUP.get(fmt, 0)
+    if packed.dtype != torch.uint8 or packed.shape[1] * 2 != n:
+        raise ValueError(f"packed: {packed.dtype} {tuple(packed.shape)}, expected uint8 {(rows, n // 2)}")
+    sshape = scale_shape(rows, n, fmt, group)
+    sdt = _scale_torch_dtype(scale_dtype)
+    if scales.dtype != sdt or tuple(scales.shape) != sshape:
+        raise ValueError(f"scales: {scales.dtype} {tuple(scales.shape)}, expected {sdt} {sshape}")
+    if fmt == "nvfp4":
+        if tensor_scale is None:
+            raise ValueError("NVFP4 needs its tensor_scale")
+        if tensor_scale.dtype != torch.float32 or tensor_scale.numel() != 1:
+            raise ValueError("tensor_scale must be one float32")
+    else:
+        tensor_scale = None
+    if out_dtype is None:
+        out_dtype = x.dtype if out is None else out.dtype
+    if out_dtype not in _IN:
+        raise ValueError("out_dtype must be bfloat16, float16 or float32")
+    if out is not None:
+        _expect(out, "out", out_dtype, (tokens, rows))
+    dev = x.device
+    _same_device(dev, x=x, packed=packed, scales=scales, tensor_scale=tensor_scale, out=out)
+    xc, pc, sc = x.contiguous(), packed.contiguous(), scales.contiguous()
+    s = None if rotated else _signs_tensor(signs, n, dev)
+    with torch.cuda.device(dev):
+        st, other = _resolve_stream(stream)
+        own = out is None
+        if own:
+            out = torch.empty((tokens, rows), dtype=out_dtype, device=dev)
+        need = lib.rhtq_matvec_workspace(tokens, n)
+        work = torch.empty(need, dtype=torch.uint8, device=dev)
+        _check(lib.rhtq_matvec(xc.data_ptr(), _IN[x.dtype], tokens, n, n if block is None else block, _p(s), int(rotated),
+                               pc.data_ptr(), sc.data_ptr(), _p(tensor_scale), rows, _FMT[fmt], group, _SCALE[scale_dtype],
+                               out.data_ptr(), _IN[out_dtype], work.data_ptr(), need, st.cuda_stream), "rhtq_matvec")
+        _keep_for(st, other, xc if xc is not x else None, pc if pc is not packed else None, sc if sc is not scales else None, s,
+                  work, out if own else None)
+    return out
+
+
+def _rows_of(cache, table, lengths, starts, tokens):
+    """(struct, seqs, width) of an append or read call after its checks; the device is checked last, by the caller."""
+    c = _cache_struct(cache, False)
+    if table.dim() != 2:
+        raise ValueError("table must be 2-D [seqs][width]")
+    seqs, width = table.shape
+    _int32(table, "table", (seqs, width))
+    _int32(lengths, "lengths", (seqs,))
+    if starts is not None:
+        _int32(starts, "starts", (seqs + 1,))
+    elif tokens != seqs:
+        raise ValueError(f"without starts there is one row for each of {seqs} sequences: got {tokens}")
+    return c, seqs, width
+
+
+def _row_strides(x):
+    """x with rows that start on 16 bytes (a copy where they do not), and its strides in elements."""
+    per16 = 16 // x.element_size()
+    if x.stride(2) != 1 or x.stride(0) % per16 or x.stride(1) % per16 or x.data_ptr() % 16:
+        x = x.contiguous()
+        if x.data_ptr() % 16:
+            x = x.clone()
+    return x
+
+
+def rhtq_cache_append(cache: RhtqCache, k, v, table, lengths, starts=None, k_signs=None, v_signs=None, stream=None):
+    """Rotate, quantise (INT4, one scale a row) and store new keys and values [tokens][kv_heads][head_dim] (bfloat16, float16 or
+    float32; any strides) in the pages that `table` int32 [seqs][width] names.  Rows starts[s] .. starts[s+1]-1 are the last positions
+    of sequence s, up to lengths[s] - 1; starts None: one row for each sequence.  Rows of no sequence, or on no page, are passed over."""
+    if k.dim() != 3 or v.dim() != 3 or k.shape != v.shape:
+        raise ValueError("k and v must be 3-D [tokens][kv_heads][head_dim], alike")
+    if k.dtype not in _IN or v.dtype != k.dtype:
+        raise ValueError("k and v must both be bfloat16, float16 or float32")
+    tokens = k.shape[0]
+    c, seqs, width = _rows_of(cache, table, lengths, starts, tokens)
+    if (c.kv_heads, c.head_dim) != tuple(k.shape[1:]):
+        raise ValueError(f"k: {tuple(k.shape)}, expected {(tokens, c.kv_heads, c.head_dim)}")
+    dev = k.device
+    _same_device(dev, k=k, v=v, k_codes=cache.k_codes, k_scales=cache.k_scales, v_codes=cache.v_codes, v_scales=cache.v_scales,
+                 table=table, lengths=lengths, starts=starts)
+    with torch.cuda.device(dev):
+        ks, vs = _cache_signs(k_signs, c.head_dim, dev), _cache_signs(v_signs, c.head_dim, dev)
+        kc, vc = _row_strides(k), _row_strides(v)
+        st, other = _resolve_stream(stream)
+        _check(lib.rhtq_cache_append(ctypes.byref(c), kc.data_ptr(), vc.data_ptr(), _IN[k.dtype], tokens, kc.stride(0), kc.stride(1),
+                                     vc.stride(0), vc.stride(1), table.data_ptr(), width, lengths.data_ptr(), _p(starts), seqs,
+                                     _p(ks), _p(vs), st.cuda_stream), "rhtq_cache_append")
+        _keep_for(st, other, ks, vs, kc if kc is not k else None, vc if vc is not v else None)
+
+
+def rhtq_cache_read(cache: RhtqCache, table, lengths, starts, tokens: int, k_signs=None, v_signs=None, dtype=torch.bfloat16,
+                    k_out=None, v_out=None, stream=None):
+    """Read rows back, dequantised and with the rotation undone: (k, v) [tokens][kv_heads][head_dim] of `dtype`.  Rows belong to
+    sequences as in rhtq_cache_append: starts from the running sum of lengths reads whole sequences, shorter lengths read earlier rows.
+    Rows of no sequence, or on no page, are zero."""
+    if dtype not in _IN:
+        raise ValueError("dtype must be bfloat16, float16 or float32")
+    if tokens < 0:
+        raise ValueError("tokens must not be negative")
+    c, seqs, width = _rows_of(cache, table, lengths, starts, tokens)
+    shape = (tokens, c.kv_heads, c.head_dim)
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is not None:
+            _expect(t, name, dtype, shape)
+    dev = cache.k_codes.device
+    _same_device(dev, k_codes=cache.k_codes, k_scales=cache.k_scales, v_codes=cache.v_codes, v_scales=cache.v_scales, table=table,
+                 lengths=lengths, starts=starts, k_out=k_out, v_out=v_out)
+    with torch.cuda.device(dev):
+        ks, vs = _cache_signs(k_signs, c.head_dim, dev), _cache_signs(v_signs, c.head_dim, dev)
+        st, other = _resolve_stream(stream)
+        own_k, own_v = k_out is None, v_out is None
+        if own_k:
+            k_out = torch.empty(shape, dtype=dtype, device=dev)
+        if own_v:
+            v_out = torch.empty(shape, dtype=dtype, device=dev)
+        _check(lib.rhtq_cache_read(ctypes.byref(c), k_out.data_ptr(), v_out.data_ptr(), _IN[dtype], tokens, table.data_ptr(), width,
+                                   lengths.data_ptr(), _p(starts), seqs, _p(ks), _p(vs), st.cuda_stream), "rhtq_cache_read")
+        _keep_for(st, other, ks, vs, k_out if own_k else None, v_out if own_v else None)
+    return k_out, v_out
+
+
+def rhtq_paged_attention(q, cache: RhtqCache, table, lengths, k_signs=None, v_signs=None, scale: float | None = None,
+                         window: int = 0, sinks: int = 0, out=None, stream=None):
+    """Attention of one new token per sequence, q [seqs][q_heads][head_dim] (bfloat16 or float16, any strides; q_heads a multiple of the
+    cache's kv_heads), over its cached positions [0, lengths[s]); the token's own row has been appended.  scale: 1/sqrt(head_dim)
+    unless given.  window > 0: only the last `window` positions and the first `sinks` are visible.  A sequence with no visible
+    position gets zeros.  Returns [seqs][q_heads][head_dim] in q's type."""
+    if q.dim() != 3:
+        raise ValueError("q must be 3-D [seqs][q_heads][head_dim]")
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("q must be bfloat16 or float16")
+    c, seqs, width = _rows_of(cache, table, lengths, None, q.shape[0])
+    q_heads, dim = q.shape[1:]
+    if dim != c.head_dim or q_heads < 1 or q_heads % max(c.kv_heads, 1):
+        raise ValueError(f"q: {tuple(q.shape)} does not fit {c.kv_heads} key-value heads of {c.head_dim}")
+    if window < 0 or sinks < 0:
+        raise ValueError("window and sinks must not be negative")
+    if out is not None:
+        _expect(out, "out", q.dtype, q.shape)
+    dev = q.device
+    _same_device(dev, q=q, k_codes=cache.k_codes, k_scales=cache.k_scales, v_codes=cache.v_codes, v_scales=cache.v_scales, table=table,
+                 lengths=lengths, out=out)
+    with torch.cuda.device(dev):
+        ks, vs = _cache_signs(k_signs, dim, dev), _cache_signs(v_signs, dim, dev)
+        qc = _row_strides(q)
+        st, other = _resolve_stream(stream)
+        own = out is None
+        if own:
+            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        need = lib.rhtq_paged_attention_workspace(seqs, q_heads, c.kv_heads, dim, width, c.page, window, sinks)
+        work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        _check(lib.rhtq_paged_attention(qc.data_ptr(), _IN[q.dtype], seqs, q_heads, qc.stride(0), qc.stride(1), ctypes.byref(c),
+                                        table.data_ptr(), width, lengths.data_ptr(), _p(ks), _p(vs),
+                                        1.0 / math.sqrt(dim) if scale is None else scale, window, sinks, out.data_ptr(), _p(work),
+                                        need, st.cuda_stream), "rhtq_paged_attention")
+        _keep_for(st, other, ks, vs, work, qc if qc is not q else None, out if own else None)
+    return out
+
+
+def _paging(table, lengths, refs):
+    if table.dim() != 2 or refs.dim() != 1:
+        raise ValueError("table must be 2-D [seqs][width] and refs 1-D [pages]")
+    _int32(table, "table", table.shape)
+    if lengths is not None:
+        _int32(lengths, "lengths", (table.shape[0],))
+    _int32(refs, "refs", refs.shape)
+    return table.shape
+
+
+def _paged_cache(cache, refs):
+    c = _cache_struct(cache, True)
+    if c.pages != refs.shape[0]:
+        raise ValueError(f"refs has {refs.shape[0]} entries, the cache {c.pages} pages")
+    return c
+
+
+def _index_list(t, name, count=None):
+    if t.dim() != 1:
+        raise ValueError(f"{name} must be 1-D")
+    _int32(t, name, t.shape if count is None else (count,))
+    return t.shape[0]
+
+
+def _work_for(pages, seqs, count, dev):
+    need = lib.rhtq_pages_workspace(pages, seqs, count)
+    return torch.empty(need, dtype=torch.uint8, device=dev), need
+
+
+def rhtq_pages_reserve(table, lengths, refs, add, page: int, stream=None):
+    """Room for add[s] more positions of every sequence: lengths grow, and where `table` int32 [seqs][width] has no page yet the lowest
+    free ones (refs int32 [pages] == 0) are taken.  All or nothing; returns a device int32 [1]: 0 done, otherwise the number of
+    pages missing, or -1 for a negative amount."""
+    seqs, width = _paging(table, lengths, refs)
+    _int32(add, "add", (seqs,))
+    dev = table.device
+    _same_device(dev, table=table, lengths=lengths, refs=refs, add=add)
+    with torch.cuda.device(dev):
+        st, other = _resolve_stream(stream)
+        status = torch.empty(1, dtype=torch.int32, device=dev)
+        work, need = _work_for(refs.shape[0], seqs, 0, dev)
+        _check(lib.rhtq_pages_reserve(table.data_ptr(), width, lengths.data_ptr(), seqs, refs.data_ptr(), refs.shape[0], page,
+                                      add.data_ptr(), status.data_ptr(), work.data_ptr(), need, st.cuda_stream), "rhtq_pages_reserve")
+        _keep_for(st, other, status, work)
+    return status
+
+
+def rhtq_pages_free(table, lengths, refs, seqs, stream=None):
+    """Give up every page of the listed sequences (int32 [count]) and set their lengths to 0."""
+    all_seqs, width = _paging(table, lengths, refs)
+    count = _index_list(seqs, "seqs")
+    dev = table.device
+    _same_device(dev, table=table, lengths=lengths, refs=refs, seqs=seqs)
+    with torch.cuda.device(dev):
+        st, _ = _resolve_stream(stream)
+        _check(lib.rhtq_pages_free(table.data_ptr(), width, lengths.data_ptr(), all_seqs, refs.data_ptr(), refs.shape[0], seqs.data_ptr(),
+                                   count, st.cuda_stream), "rhtq_pages_free")
+
+
+def rhtq_pages_trim(table, lengths, refs, page: int, window: int, sinks: int = 0, stream=None):
+    """Give up the pages that attention with this window and these first positions can never see again."""
+    seqs, width = _paging(table, lengths, refs)
+    dev = table.device
+    _same_device(dev, table=table, lengths=lengths, refs=refs)
+    with torch.cuda.device(dev):
+        st, _ = _resolve_stream(stream)
+        _check(lib.rhtq_pages_trim(table.data_ptr(), width, lengths.data_ptr(), seqs, refs.data_ptr(), refs.shape[0], page, window,
+                                   sinks, st.cuda_stream), "rhtq_pages_trim")
+
+
+def rhtq_pages_fork(cache: RhtqCache, table, lengths, refs, src, dst, stream=None):
+    """Sequences dst (int32 [count], empty ones) become copies of src: full pages are shared, a partly filled last page is copied.
+    All or nothing; returns a device int32 [1]: 0 done, otherwise the number of pages missing, or -1 for an invalid index."""
+    c = _paged_cache(cache, refs)
+    seqs, width = _paging(table, lengths, refs)
+    count = _index_list(src, "src")
+    _index_list(dst, "dst", count)
+    dev = table.device
+    _same_device(dev, table=table, lengths=lengths, refs=refs, src=src, dst=dst, k_codes=cache.k_codes, k_scales=cache.k_scales,
+                 v_codes=cache.v_codes, v_scales=cache.v_scales)
+    with torch.cuda.device(dev):
+        st, other = _resolve_stream(stream)
+        status = torch.empty(1, dtype=torch.int32, device=dev)
+        work, need = _work_for(refs.shape[0], seqs, count, dev)
+        _check(lib.rhtq_pages_fork(ctypes.byref(c), table.data_ptr(), width, lengths.data_ptr(), seqs, refs.data_ptr(), src.data_ptr(),
+                                   dst.data_ptr(), count, status.data_ptr(), work.data_ptr(), need, st.cuda_stream), "rhtq_pages_fork")
+        _keep_for(st, other, status, work)
+    return status
+
+
+def rhtq_pages_copy(cache: RhtqCache, src, dst, stream=None):
+    """Copy whole pages src[i] -> dst[i] (int32 [count]) in every layer; a page may be written once and not read by the same call."""
+    c = _cache_struct(cache, True)
+    count = _index_list(src, "src")
+    _index_list(dst, "dst", count)
+    dev = cache.k_codes.device
+    _same_device(dev, src=src, dst=dst, k_codes=cache.k_codes, k_scales=cache.k_scales, v_codes=cache.v_codes, v_scales=cache.v_scales)
+    with torch.cuda.device(dev):
+        st, _ = _resolve_stream(stream)
+        _check(lib.rhtq_pages_copy(ctypes.byref(c), src.data_ptr(), dst.data_ptr(), count, st.cuda_stream), "rhtq_pages_copy")
+
+
+def rhtq_pages_compact(cache: RhtqCache, table, refs, stream=None):
+    """Move live pages into lower free ones until they fill [0, live); table and refs follow.  Returns live, a device int32 [1]."""
+    c = _paged_cache(cache, refs)
+    seqs, width = _paging(table, None, refs)
+    dev = table.device
+    _same_device(dev, table=table, refs=refs, k_codes=cache.k_codes, k_scales=cache.k_scales, v_codes=cache.v_codes,
+                 v_scales=cache.v_scales)
+    with torch.cuda.device(dev):
+        st, other = _resolve_stream(stream)
+        live = torch.empty(1, dtype=torch.int32, device=dev)
+        work, need = _work_for(refs.shape[0], seqs, 0, dev)
+        _check(lib.rhtq_pages_compact(ctypes.byref(c), table.data_ptr(), width, seqs, refs.data_ptr(), live.data_ptr(), work.data_ptr(),
+                                      need, st.cuda_stream), "rhtq_pages_compact")
+        _keep_for(st, other, live, work)
+    return live
