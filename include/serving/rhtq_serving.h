@@ -37,11 +37,11 @@ int rhtq_serving_version(void);
  *   y_out      [tokens][rows] in out_dtype (RHTQ_IN_BF16, RHTQ_IN_F16 or RHTQ_IN_F32)
  *   workspace  rhtq_matvec_workspace(...) bytes, 16-byte aligned
  * n: a multiple of 32 up to 2^20 (with rotated == 0 also one that rhtq_rotate or its blocked form takes).
- * rows, tokens: any number (0: nothing to do).  Sums are in fp32; x is carried with at least 16 bits below
- * the largest value of each 128-element stretch of its row (22 bits for fp32 output).
+ * rows: any number, tokens up to 2^20 (0: nothing to do).  Sums are in fp32; R x is carried to 22 bits, and to
+ * 2^-35 of the largest value of its row.
  * packed must be 16-byte aligned, x and y_out 16 bytes, scales to their element.
  */
-int64_t rhtq_matvec_workspace(int64_t tokens, int32_t n);
+int64_t rhtq_matvec_workspace(int64_t tokens, int32_t n, int64_t rows);
 int rhtq_matvec(const void* x, int in_dtype, int64_t tokens, int32_t n, int32_t block, const int8_t* signs,
                 int rotated, const uint8_t* packed, const void* scales, const float* tensor_scale, int64_t rows,
                 int fmt, int32_t group, int scale_dtype, void* y_out, int out_dtype, void* workspace,

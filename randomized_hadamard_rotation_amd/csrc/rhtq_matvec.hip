@@ -1,5 +1,20 @@
-// Product of a few rotated rows with 4-bit weights: y[t][r] = sum_k x[t][k] s[r][k / g] c[r][k], fp32 sums.
-// Bounded by the code bytes for up to about 64 rows of x.
+// Product of a few rotated rows with 4-bit weights: y[t][r] = sum_k x[t][k] s[r][k / g] c[r][k].
+//
+// The weights' bytes bound it (rows * n / 2, once), as long as nothing else takes longer than they do; everything here
+// serves that.
+//  - x is laid out once, by prepare_kernel: every row of x is divided by a power of two 2^e so that it lies in [-1, 1], and each
+//    value becomes two halves, hi = fp16(x) and lo = fp16((x - hi) 2^11): 22 bits, more for values near fp16's exponent range's end.
+//    The halves stand in the order in which lanes take them as a matrix operand (below), so they are read as they lie.
+//  - Codes become fp16 exactly: INT4 by setting them into the low mantissa bits of 1024 (two values per instruction, 1.25 instructions
+//    a value in all), E2M1 by the conversion instruction, with the E4M3 scale of a 16-block (product exact: 2 + 4 bits)
+//    or the power of two of a 32-block relative to the largest in its 128 values (exact down to 2^-22 of that one).
+//  - v_mfma_f32_16x16x32_f16 multiplies 16 weight rows by 16 rows of halves (8 tokens, hi and lo); sums are fp32.  INT4 scales multiply
+//    the sum of their group.  y = 2^e (sum_hi + 2^-11 sum_lo).
+//
+// Operand rows m = 4 a + b stand for token 2 a + (b & 1) of a tile of 8, half b >> 1, so that one lane gets both halves of its two tokens.
+// A step covers 128 values of k in 4 products of 32; product i, lane group q = lane / 16, takes the 8 codes of one dword at
+//   4 q + i (groups >= 128, NVFP4, MXFP4: one 16-byte load),  8 (i / 2) + 2 q + i % 2 (groups of 64),  4 i + q (32 and 16)
+// of the row's 16 dwords, so that each product lies inside one scale group (groups of 16: two, the operand masked for each in turn).
 #include "rhtq_internal.h"
 #include "rhtq_serving_device.h"
 #include "rhtq_serving_internal.h"
@@ -7,71 +22,414 @@
 namespace rhtq {
 namespace {
 
-constexpr int kThreads = 256;
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
-__device__ __forceinline__ float e2m1(uint32_t c) {
-  const float m[8] = {0.0f, 0.5f, 1.0f, 1.5f, 2.0f, 3.0f, 4.0f, 6.0f};
-  const float v = m[c & 7];
-  return c & 8 ? -v : v;
+// How the codes are scaled; also what decides the order of k.
+enum Mode { M128, M64, M32, M16, MNV, MMX };
+
+constexpr int kStep = 128;         // values of k in a step
+constexpr int kFrag = 1024;        // bytes of one operand: 64 lanes x 16
+
+// Dword (of 16) of a row's step that product i takes in lane group q.
+template <int MODE>
+__host__ __device__ constexpr int dword_of(int i, int q) {
+  return MODE == M64 ? 8 * (i / 2) + 2 * q + i % 2 : (MODE == M32 || MODE == M16 ? 4 * i + q : 4 * q + i);
+}
+// Value (of 8) of a dword in slot j of the operand: INT4 takes nibbles 16 bits apart in pairs, E2M1 neighbours.
+template <int MODE>
+__host__ __device__ constexpr int value_of(int j) {
+  return MODE == MNV || MODE == MMX ? j : (j >> 1) + 4 * (j & 1);
 }
 
-__device__ __forceinline__ float e4m3(uint32_t b) {
-  const int e = (b >> 3) & 15, m = b & 7;
-  const float v = e == 0 ? ldexpf((float)m, -9) : ldexpf((float)(8 + m), e - 10);
-  return b & 128 ? -v : v;
-}
+// ---- x: halves in operand order -------------------------------------------------------------------------------------------
 
-__device__ __forceinline__ float group_scale(const MatvecArgs& a, int64_t at) {
-  if (a.fmt == RHTQ_FMT_INT4) return load_scale(a.scales, at, a.scale_dtype);
-  const uint32_t b = static_cast<const uint8_t*>(a.scales)[at];
-  if (a.fmt == RHTQ_FMT_NVFP4) return e4m3(b) * a.tensor_scale[0];
-  return b == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(b << 23);
-}
+constexpr int kPrep = 1024;
 
-template <int TX, int TY>
-__global__ __launch_bounds__(kThreads) void matvec_kernel(MatvecArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t r = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
-  const int64_t t = blockIdx.y;
-  if (r >= a.rows) return;
-  const int group = a.group ? a.group : a.n;
-  float acc = 0.0f;
-  for (int k = 8 * lane; k < a.n; k += 512) {
-    float x[8];
-    load_row<TX, 8>(a.x, t * a.n + k, x);
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(a.packed + (r * a.n + k) / 2);
-    float p = 0.0f;
+// One workgroup per token of a tile; tokens beyond the last (and k beyond n) become zeros.
+template <int MODE, int TX>
+__global__ __launch_bounds__(kPrep) void prepare_kernel(MatvecArgs a) {
+  __shared__ float wave_max[kPrep / 64];
+  const int64_t t = blockIdx.x;
+  const int64_t tile = t >> 3;
+  const int steps = (a.n + kStep - 1) / kStep;
+  const bool real = t < a.tokens;
+  // 8 values a thread: dword d of step s
+  float v[8];
+  float top = 0.0f;
+  const int dwords = a.n / 8;
+  for (int u = threadIdx.x; real && u < dwords; u += kPrep) {
+    load_row<TX, 8>(a.x, t * a.n + 8 * u, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t c = (w >> (4 * i)) & 15;
-      const float v = a.fmt == RHTQ_FMT_INT4 ? (float)((int)(c << 28) >> 28) : e2m1(c);
-      p = __builtin_fmaf(v, x[i], p);
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, __builtin_fabsf(v[j]));
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+  if ((threadIdx.x & 63) == 0) wave_max[threadIdx.x >> 6] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPrep / 64; ++i) top = fmaxf(top, wave_max[i]);
+  const int e = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) : 0;
+  if (threadIdx.x == 0) a.exponents[t] = e;
+  const int a4 = (int)(t & 7) >> 1, b = (int)(t & 1);
+  const int m_hi = 4 * a4 + b, m_lo = m_hi + 2;
+  uint8_t* out = static_cast<uint8_t*>(a.halves) + tile * steps * 4 * kFrag;
+  for (int u = threadIdx.x; u < steps * 16; u += kPrep) {
+    const int s = u >> 4, i = (u >> 2) & 3, q = u & 3;      // operand i of step s, lane group q
+    const int k = kStep * s + 8 * dword_of<MODE>(i, q);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    if (real && k < a.n) load_row<TX, 8>(a.x, t * a.n + k, v);
+    f16x8 hi, lo;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float x = __builtin_amdgcn_ldexpf(v[value_of<MODE>(j)], -e);
+      hi[j] = (_Float16)x;
+      lo[j] = (_Float16)((x - (float)hi[j]) * 2048.0f);
     }
-    acc = __builtin_fmaf(p, group_scale(a, r * (a.n / group) + k / group), acc);
-  }
-#pragma unroll
-  for (int d = 32; d; d >>= 1) acc += __shfl_xor(acc, d);
-  if (lane == 0) {
-    if constexpr (TY == RHTQ_IN_F32) static_cast<float*>(a.y)[t * a.rows + r] = acc;
-    else static_cast<uint16_t*>(a.y)[t * a.rows + r] = (uint16_t)to16<TY>(acc);
+    uint8_t* o = out + (int64_t)(4 * s + i) * kFrag + 256 * q;
+    *reinterpret_cast<f16x8*>(o + 16 * m_hi) = hi;
+    *reinterpret_cast<f16x8*>(o + 16 * m_lo) = lo;
   }
 }
 
-template <int TX>
-hipError_t launch_x(int out, const MatvecArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.rows + 3) / 4), (unsigned)a.tokens);
-  if (out == RHTQ_IN_BF16) hipLaunchKernelGGL((matvec_kernel<TX, RHTQ_IN_BF16>), grid, dim3(kThreads), 0, s, a);
-  else if (out == RHTQ_IN_F16) hipLaunchKernelGGL((matvec_kernel<TX, RHTQ_IN_F16>), grid, dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL((matvec_kernel<TX, RHTQ_IN_F32>), grid, dim3(kThreads), 0, s, a);
+// ---- weights: one step of a row tile ---------------------------------------------------------------------------------------
+
+// Codes of a lane's row, and what scales them.
+struct Codes {
+  uint32_t w[4];       // product i's dword
+  float s[8];          // M128: [0]; M64: [0..1]; M32: [0..3]; M16: [0..7]; MMX: [0] the step's power of two, [1] the lane's
+  uint32_t e;          // MNV: two E4M3 bytes
+};
+
+template <int MODE>
+__device__ __forceinline__ void load_codes(const MatvecArgs& a, int64_t row, int step, int q, Codes& c) {
+  const int left = (a.n - kStep * step) / 8;          // dwords of the row from this step on
+  const uint32_t* p = reinterpret_cast<const uint32_t*>(a.packed) + row * (a.n / 8) + 16 * step;
+  if constexpr (MODE == M128 || MODE == MNV || MODE == MMX) {
+    u32x4 t = {0, 0, 0, 0};
+    if (4 * q < left) t = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + 4 * q));
+    c.w[0] = t.x; c.w[1] = t.y; c.w[2] = t.z; c.w[3] = t.w;
+  } else if constexpr (MODE == M64) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      u32x2 t = {0, 0};
+      if (8 * g + 2 * q < left) t = *reinterpret_cast<const u32x2*>(p + 8 * g + 2 * q);
+      c.w[2 * g] = t.x;
+      c.w[2 * g + 1] = t.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c.w[i] = 4 * i + q < left ? p[4 * i + q] : 0u;
+  }
+  if constexpr (MODE == M128) {
+    c.s[0] = load_scale(a.scales, row * a.groups + (a.group_log < 0 ? 0 : (kStep * step) >> a.group_log), a.scale_dtype);
+  } else if constexpr (MODE == M64 || MODE == M32 || MODE == M16) {
+    constexpr int PER = MODE == M64 ? 2 : (MODE == M32 ? 4 : 8);
+#pragma unroll
+    for (int g = 0; g < PER; ++g)
+      c.s[g] = PER * step + g < a.groups ? load_scale(a.scales, row * a.groups + PER * step + g, a.scale_dtype) : 0.0f;
+  } else if constexpr (MODE == MNV) {
+    c.e = 0;
+    if (4 * q < left) c.e = *reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(a.scales) + row * a.groups + 8 * step + 2 * q);
+  } else {
+    const uint8_t* s = static_cast<const uint8_t*>(a.scales) + row * a.groups + 4 * step;
+    uint32_t own = 0, top = 0;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const uint32_t b = 4 * g < left ? s[g] : 0u;
+      top = b > top ? b : top;
+      own = g == q ? b : own;
+    }
+    // 2^(top - 127), and 2^(own - top) kept above 2^-126: a block so far below another adds nothing
+    c.s[0] = __builtin_amdgcn_ldexpf(1.0f, (int)top - 127);
+    c.s[1] = __builtin_amdgcn_ldexpf(1.0f, own + 126 > top ? (int)own - (int)top : -126);
+  }
+}
+
+__device__ __forceinline__ f16x2 as_f16x2(uint32_t v) { return __builtin_bit_cast(f16x2, v); }
+
+// The 8 codes of product i as fp16, exactly.
+template <int MODE>
+__device__ __forceinline__ f16x8 unpack(const Codes& c, int i) {
+  f16x2 r[4];
+  if constexpr (MODE == MNV || MODE == MMX) {
+    const float s = MODE == MMX ? c.s[1] : 1.0f;
+    r[0] = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c.w[i], s, 0));
+    r[1] = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c.w[i], s, 1));
+    r[2] = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c.w[i], s, 2));
+    r[3] = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c.w[i], s, 3));
+    if constexpr (MODE == MNV) {
+      // dwords 0, 1 of the lane's 16 bytes are one 16-block, 2, 3 the next
+      const f16x2 b = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c.e, 1.0f, false));
+      const f16x2 f = {b[i >> 1], b[i >> 1]};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) r[k] *= f;
+    }
+  } else {
+    const uint32_t w = c.w[i] ^ 0x88888888u, h = w >> 8;           // nibbles are code + 8
+    const f16x2 low = {(_Float16)-1032.0f, (_Float16)-1032.0f};
+    const f16x2 part = {(_Float16)0.0625f, (_Float16)0.0625f}, high = {(_Float16)-72.0f, (_Float16)-72.0f};
+    r[0] = as_f16x2((w & 0x000F000Fu) | 0x64006400u) + low;                               // 1024 + u - 1032
+    r[1] = __builtin_elementwise_fma(as_f16x2((w & 0x00F000F0u) | 0x64006400u), part, high);   // (1024 + 16 u) / 16 - 72
+    r[2] = as_f16x2((h & 0x000F000Fu) | 0x64006400u) + low;
+    r[3] = __builtin_elementwise_fma(as_f16x2((h & 0x00F000F0u) | 0x64006400u), part, high);
+  }
+  f16x8 o;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    o[2 * k] = r[k][0];
+    o[2 * k + 1] = r[k][1];
+  }
+  return o;
+}
+
+__device__ __forceinline__ f32x4 mma(f16x8 x, f16x8 w, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(x, w, c, 0, 0, 0); }
+
+// acc += a step's products of one token tile: x[i] its operands, w[i] the codes.
+template <int MODE>
+__device__ __forceinline__ void step_into(f32x4& acc, const f16x8 (&x)[4], const f16x8 (&w)[4], const Codes& c) {
+  const f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+  if constexpr (MODE == MNV) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc = mma(x[i], w[i], acc);
+  } else if constexpr (MODE == M128 || MODE == MMX) {
+    f32x4 d = mma(x[0], w[0], z);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) d = mma(x[i], w[i], d);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = __builtin_fmaf(c.s[0], d[k], acc[k]);
+  } else if constexpr (MODE == M64) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const f32x4 d = mma(x[2 * g + 1], w[2 * g + 1], mma(x[2 * g], w[2 * g], z));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[k] = __builtin_fmaf(c.s[g], d[k], acc[k]);
+    }
+  } else if constexpr (MODE == M32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x4 d = mma(x[i], w[i], z);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[k] = __builtin_fmaf(c.s[i], d[k], acc[k]);
+    }
+  } else {
+    // product i holds groups 2 i (lane groups 0, 1) and 2 i + 1 (2, 3): each with the other's codes out
+    const bool upper = (threadIdx.x & 63) >= 32;
+    const f16x8 none = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x4 d0 = mma(x[i], upper ? none : w[i], z), d1 = mma(x[i], upper ? w[i] : none, z);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[k] = __builtin_fmaf(c.s[2 * i + 1], d1[k], __builtin_fmaf(c.s[2 * i], d0[k], acc[k]));
+    }
+  }
+}
+
+__device__ __forceinline__ void store_y(const MatvecArgs& a, int64_t t, int64_t row, float v) {
+  const int64_t at = t * a.rows + row;
+  if (a.out_dtype == RHTQ_IN_F32) static_cast<float*>(a.y)[at] = v;
+  else if (a.out_dtype == RHTQ_IN_BF16) static_cast<uint16_t*>(a.y)[at] = (uint16_t)to16<RHTQ_IN_BF16>(v);
+  else static_cast<uint16_t*>(a.y)[at] = (uint16_t)to16<RHTQ_IN_F16>(v);
+}
+
+// Both halves of a token, times its power of two and the tensor scale.
+__device__ __forceinline__ float whole(const MatvecArgs& a, int64_t t, float hi, float lo) {
+  const float v = __builtin_amdgcn_ldexpf(__builtin_fmaf(lo, 1.0f / 2048.0f, hi), a.exponents[t]);
+  return a.tensor_scale ? v * a.tensor_scale[0] : v;
+}
+
+// ---- few tokens: one tile of 16 rows per workgroup, k split over its waves -----------------------------------------------------
+
+constexpr int kWaves = 8;
+constexpr int kAhead = 4;          // steps whose codes are in flight
+
+template <int MODE>
+__global__ __launch_bounds__(64 * kWaves) void narrow_kernel(MatvecArgs a) {
+  __shared__ f32x4 part[kWaves][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int m = lane & 15, q = lane >> 4;
+  const int64_t tile = blockIdx.y;
+  const int64_t row0 = (int64_t)blockIdx.x * 16;
+  const int64_t row = row0 + m < a.rows ? row0 + m : a.rows - 1;
+  const int steps = (a.n + kStep - 1) / kStep;
+  const int s0 = steps * wave / kWaves, s1 = steps * (wave + 1) / kWaves;
+  const int left = (int)(a.tokens - 8 * tile);                    // tokens of this tile that there are
+  const bool mine = 2 * (m >> 2) + (m & 1) < left;
+  const uint8_t* x = static_cast<const uint8_t*>(a.halves) + tile * steps * 4 * kFrag + 16 * lane;
+  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s = s0; s < s1; s += kAhead) {
+    Codes c[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (s + k < s1) load_codes<MODE>(a, row, s + k, q, c[k]);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (s + k >= s1) break;
+      f16x8 v[4], w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = f16x8{};
+        if (mine) v[i] = *reinterpret_cast<const f16x8*>(x + (int64_t)(4 * (s + k) + i) * kFrag);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = unpack<MODE>(c[k], i);
+      step_into<MODE>(acc, v, w, c[k]);
+    }
+  }
+  part[wave][lane] = acc;
+  __syncthreads();
+  // 128 results: row m, token 2 q + b of lane (q, m), b = 0, 1
+  if (threadIdx.x >= 128) return;
+  const int b = threadIdx.x >> 6;
+  float hi = 0.0f, lo = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    const float* p = reinterpret_cast<const float*>(&part[w][lane]);
+    hi += p[b];
+    lo += p[b + 2];
+  }
+  const int64_t t = 8 * tile + 2 * q + b;
+  if (t < a.tokens && row0 + m < a.rows) store_y(a, t, row0 + m, whole(a, t, hi, lo));
+}
+
+// ---- many tokens: 128 rows x up to 64 tokens per workgroup, k split over the grid -------------------------------------------
+
+constexpr int kWide = 256;
+constexpr int kWideRows = 128;
+
+// TT token tiles.  Four waves share the operands of x through two buffers in LDS; each has 32 rows of its own.
+template <int MODE, int TT>
+__global__ __launch_bounds__(kWide) void wide_kernel(MatvecArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t buf[2][4 * TT * kFrag];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int m = lane & 15, q = lane >> 4;
+  const int64_t tile0 = (int64_t)blockIdx.z * TT;
+  const int64_t row0 = (int64_t)blockIdx.x * kWideRows + 32 * wave;
+  int64_t row[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) row[r] = row0 + 16 * r + m < a.rows ? row0 + 16 * r + m : a.rows - 1;
+  const int steps = (a.n + kStep - 1) / kStep;
+  const int s0 = (int)((int64_t)steps * blockIdx.y / a.k_splits), s1 = (int)((int64_t)steps * (blockIdx.y + 1) / a.k_splits);
+  const uint8_t* halves = static_cast<const uint8_t*>(a.halves);
+  u32x4 stage[TT];
+  auto fetch = [&](int s) {
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+      stage[t] = *reinterpret_cast<const u32x4*>(halves + ((tile0 + t) * steps + s) * 4 * kFrag + 16 * threadIdx.x);
+  };
+  auto put = [&](int b) {
+#pragma unroll
+    for (int t = 0; t < TT; ++t) *reinterpret_cast<u32x4*>(&buf[b][4 * t * kFrag + 16 * threadIdx.x]) = stage[t];
+  };
+  f32x4 acc[2][TT] = {};
+  Codes next[2];
+  if (s0 < s1) {
+    fetch(s0);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) load_codes<MODE>(a, row[r], s0, q, next[r]);
+    put(0);
+  }
+  __syncthreads();
+  for (int s = s0; s < s1; ++s) {
+    const int b = (s - s0) & 1;
+    Codes c[2] = {next[0], next[1]};
+    if (s + 1 < s1) {
+      fetch(s + 1);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) load_codes<MODE>(a, row[r], s + 1, q, next[r]);
+    }
+    f16x8 w[2][4];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[r][i] = unpack<MODE>(c[r], i);
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      f16x8 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const f16x8*>(&buf[b][(4 * t + i) * kFrag + 16 * lane]);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) step_into<MODE>(acc[r][t], v, w[r], c[r]);
+    }
+    if (s + 1 < s1) put(b ^ 1);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int64_t at = row0 + 16 * r + m;
+    if (at >= a.rows) continue;
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int64_t tok = 8 * (tile0 + t) + 2 * q + b;
+        if (tok >= a.tokens) continue;
+        const float v = whole(a, tok, acc[r][t][b], acc[r][t][b + 2]);
+        if (a.k_splits == 1) store_y(a, tok, at, v);
+        else a.partial[((int64_t)blockIdx.y * a.tokens + tok) * a.rows + at] = v;
+      }
+  }
+}
+
+__global__ __launch_bounds__(256) void join_kernel(MatvecArgs a) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, all = a.tokens * a.rows;
+  if (i >= all) return;
+  float v = 0.0f;
+  for (int k = 0; k < a.k_splits; ++k) v += a.partial[k * all + i];
+  store_y(a, i / a.rows, i % a.rows, v);
+}
+
+constexpr int kNarrowTokens = 4;
+
+template <int MODE>
+hipError_t launch_mode(int x_dtype, const MatvecArgs& a, hipStream_t s) {
+  const unsigned padded = (unsigned)matvec_padded(a.tokens);
+  if (x_dtype == RHTQ_IN_BF16) hipLaunchKernelGGL((prepare_kernel<MODE, RHTQ_IN_BF16>), dim3(padded), dim3(kPrep), 0, s, a);
+  else if (x_dtype == RHTQ_IN_F16) hipLaunchKernelGGL((prepare_kernel<MODE, RHTQ_IN_F16>), dim3(padded), dim3(kPrep), 0, s, a);
+  else hipLaunchKernelGGL((prepare_kernel<MODE, RHTQ_IN_F32>), dim3(padded), dim3(kPrep), 0, s, a);
+  if (a.tokens <= kNarrowTokens) {
+    hipLaunchKernelGGL((narrow_kernel<MODE>), dim3((unsigned)((a.rows + 15) / 16), 1), dim3(64 * kWaves), 0, s, a);
+    return hipGetLastError();
+  }
+  const unsigned tiles = padded / 8, blocks = (unsigned)((a.rows + kWideRows - 1) / kWideRows), ks = (unsigned)a.k_splits;
+  if (tiles == 1) hipLaunchKernelGGL((wide_kernel<MODE, 1>), dim3(blocks, ks, 1), dim3(kWide), 0, s, a);
+  else if (tiles == 2) hipLaunchKernelGGL((wide_kernel<MODE, 2>), dim3(blocks, ks, 1), dim3(kWide), 0, s, a);
+  else if (tiles <= 4) hipLaunchKernelGGL((wide_kernel<MODE, 4>), dim3(blocks, ks, 1), dim3(kWide), 0, s, a);
+  else hipLaunchKernelGGL((wide_kernel<MODE, 8>), dim3(blocks, ks, tiles / 8), dim3(kWide), 0, s, a);
+  if (a.k_splits > 1)
+    hipLaunchKernelGGL(join_kernel, dim3((unsigned)((a.tokens * a.rows + 255) / 256)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_matvec(int x_dtype, int out_dtype, const MatvecArgs& a, hipStream_t s) {
-  if (x_dtype == RHTQ_IN_BF16) return launch_x<RHTQ_IN_BF16>(out_dtype, a, s);
-  if (x_dtype == RHTQ_IN_F16) return launch_x<RHTQ_IN_F16>(out_dtype, a, s);
-  return launch_x<RHTQ_IN_F32>(out_dtype, a, s);
+// Tokens padded to whole tiles: 8, 16, 32 or a multiple of 64.
+int64_t matvec_padded(int64_t tokens) {
+  return tokens <= 8 ? 8 : (tokens <= 16 ? 16 : (tokens <= 32 ? 32 : (tokens + 63) / 64 * 64));
+}
+
+// Parts of k: enough workgroups for the chip, two steps each at least; none where one workgroup's waves split k.
+int32_t matvec_splits(int64_t tokens, int32_t n, int64_t rows) {
+  if (tokens <= kNarrowTokens) return 1;
+  const int64_t blocks = (rows + kWideRows - 1) / kWideRows * ((matvec_padded(tokens) + 63) / 64);
+  const int64_t steps = (n + kStep - 1) / kStep;
+  int64_t k = 512 / blocks;
+  if (k > steps / 2) k = steps / 2;
+  return k < 1 ? 1 : (int32_t)k;
+}
+
+// Bytes: two halves of every value, an exponent a token, and the parts' sums.
+int64_t matvec_halves_bytes(int64_t tokens, int32_t n) {
+  return matvec_padded(tokens) * ((n + kStep - 1) / kStep * (int64_t)kStep) * 4;
+}
+
+hipError_t launch_matvec(int x_dtype, const MatvecArgs& a, hipStream_t s) {
+  if (a.fmt == RHTQ_FMT_NVFP4) return launch_mode<MNV>(x_dtype, a, s);
+  if (a.fmt == RHTQ_FMT_MXFP4) return launch_mode<MMX>(x_dtype, a, s);
+  if (a.group_log < 0 || a.group_log >= 7) return launch_mode<M128>(x_dtype, a, s);
+  if (a.group_log == 6) return launch_mode<M64>(x_dtype, a, s);
+  if (a.group_log == 5) return launch_mode<M32>(x_dtype, a, s);
+  return launch_mode<M16>(x_dtype, a, s);
 }
 
 }  // namespace rhtq

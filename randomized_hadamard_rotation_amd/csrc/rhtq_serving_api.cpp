@@ -14,6 +14,8 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 int from_hip(hipError_t e) { return e == hipSuccess ? RHTQ_OK : RHTQ_EHIP; }
 int log2_of(int32_t v) { return 31 - __builtin_clz((unsigned)v); }
 bool in_type(int t) { return t == RHTQ_IN_BF16 || t == RHTQ_IN_F16 || t == RHTQ_IN_F32; }
+constexpr int64_t kMostTokens = 1 << 20;
+int64_t round16(int64_t v) { return (v + 15) & ~(int64_t)15; }
 uintptr_t scale_size(int t) { return t == RHTQ_SCALE_F32 ? 4 : (t == RHTQ_SCALE_F16 ? 2 : 1); }
 
 // Shape of a cache, without its pointers: RHTQ_OK or the status.
@@ -110,9 +112,12 @@ extern "C" {
 
 int rhtq_serving_version(void) { return RHTQ_SERVING_VERSION; }
 
-int64_t rhtq_matvec_workspace(int64_t tokens, int32_t n) {
-  if (tokens < 0 || n < 0 || (n > 0 && tokens > INT64_MAX / 8 / n)) return 0;
-  return 4 * tokens * n;
+// The operands of x, an exponent for each padded token, the sums of split k, and the rotated rows.
+int64_t rhtq_matvec_workspace(int64_t tokens, int32_t n, int64_t rows) {
+  if (tokens <= 0 || n <= 0 || rows <= 0 || tokens > kMostTokens || rows > INT32_MAX || n > (1 << 20)) return 0;
+  const int64_t parts = rhtq::matvec_splits(tokens, n, rows);
+  return rhtq::matvec_halves_bytes(tokens, n) + round16(4 * rhtq::matvec_padded(tokens)) +
+         (parts > 1 ? round16(4 * parts * tokens * rows) : 0) + 4 * tokens * n;
 }
 
 int rhtq_matvec(const void* x, int in_dtype, int64_t tokens, int32_t n, int32_t block, const int8_t* signs, int rotated,
@@ -130,8 +135,7 @@ int rhtq_matvec(const void* x, int in_dtype, int64_t tokens, int32_t n, int32_t 
   } else if (group != 32 || scale_dtype != RHTQ_SCALE_E8M0) {
     return RHTQ_EUNSUPPORTED;
   }
-  // rows x tokens tiles go into one grid
-  if (tokens > 65535 * (int64_t)16 || rows > (int64_t)INT32_MAX) return RHTQ_EINVAL;
+  if (tokens > kMostTokens || rows > (int64_t)INT32_MAX) return RHTQ_EINVAL;
   if (!rotated) {
     // the rotation's own checks of n and block, with no rows: nothing is enqueued
     const int st = block == n ? rhtq_rotate(x, in_dtype, 0, n, signs, nullptr, stream)
@@ -143,12 +147,20 @@ int rhtq_matvec(const void* x, int in_dtype, int64_t tokens, int32_t n, int32_t 
   if (!aligned(x, 16) || !aligned(packed, 16) || !aligned(y_out, 16) || !aligned(scales, scale_size(scale_dtype)) ||
       !aligned(tensor_scale, 4) || (!rotated && !aligned(signs, 16)))
     return RHTQ_EINVAL;
-  if (!workspace_ok(workspace, workspace_bytes, rhtq_matvec_workspace(tokens, n))) return RHTQ_EINVAL;
+  if (!workspace_ok(workspace, workspace_bytes, rhtq_matvec_workspace(tokens, n, rows))) return RHTQ_EINVAL;
   if (rhtq::getenv_test_fail_launch()) return RHTQ_EHIP;
   rhtq::MatvecArgs a{};
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  a.halves = w;
+  w += rhtq::matvec_halves_bytes(tokens, n);
+  a.exponents = reinterpret_cast<int32_t*>(w);
+  w += round16(4 * rhtq::matvec_padded(tokens));
+  a.k_splits = rhtq::matvec_splits(tokens, n, rows);
+  a.partial = reinterpret_cast<float*>(w);
+  if (a.k_splits > 1) w += round16(4 * (int64_t)a.k_splits * tokens * rows);
   a.x = x;
   if (!rotated) {
-    float* y = static_cast<float*>(workspace);
+    float* y = reinterpret_cast<float*>(w);
     const int st = block == n ? rhtq_rotate(x, in_dtype, tokens, n, signs, y, stream)
                               : rhtq_rotate_blocked(x, in_dtype, tokens, n, block, signs, y, stream);
     if (st != RHTQ_OK) return st;
@@ -157,15 +169,17 @@ int rhtq_matvec(const void* x, int in_dtype, int64_t tokens, int32_t n, int32_t 
   }
   a.packed = packed;
   a.scales = scales;
-  a.tensor_scale = tensor_scale;
+  a.tensor_scale = fmt == RHTQ_FMT_NVFP4 ? tensor_scale : nullptr;
   a.y = y_out;
   a.tokens = tokens;
   a.rows = rows;
   a.n = n;
+  a.groups = group ? n / group : 1;
+  a.group_log = group ? log2_of(group) : -1;
   a.fmt = fmt;
-  a.group = group;
   a.scale_dtype = scale_dtype;
-  return from_hip(rhtq::launch_matvec(in_dtype, out_dtype, a, reinterpret_cast<hipStream_t>(stream)));
+  a.out_dtype = out_dtype;
+  return from_hip(rhtq::launch_matvec(in_dtype, a, reinterpret_cast<hipStream_t>(stream)));
 }
 
 int rhtq_cache_append(const rhtq_cache_t* cache, const void* k, const void* v, int in_dtype, int64_t tokens,

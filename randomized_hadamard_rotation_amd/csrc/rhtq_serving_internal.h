@@ -68,19 +68,28 @@ hipError_t launch_paged_attention(int dtype, const AttentionArgs& a, hipStream_t
 
 struct MatvecArgs {
   const void* x;              // [tokens][n], rotated
+  void* halves;               // workspace: x in operand order, then the exponents, then the parts' sums
+  int32_t* exponents;
+  float* partial;
   const uint8_t* packed;
   const void* scales;
-  const float* tensor_scale;
+  const float* tensor_scale;  // NVFP4, else null
   void* y;
   int64_t tokens;
   int64_t rows;
   int32_t n;
+  int32_t groups;             // scales of a row
+  int32_t group_log;          // log2 of the group, -1: one group a row
   int32_t fmt;
-  int32_t group;
   int32_t scale_dtype;
+  int32_t out_dtype;
+  int32_t k_splits;
 };
 
-hipError_t launch_matvec(int x_dtype, int out_dtype, const MatvecArgs& a, hipStream_t s);
+int64_t matvec_padded(int64_t tokens);
+int32_t matvec_splits(int64_t tokens, int32_t n, int64_t rows);
+int64_t matvec_halves_bytes(int64_t tokens, int32_t n);
+hipError_t launch_matvec(int x_dtype, const MatvecArgs& a, hipStream_t s);
 
 struct PagesArgs {
   int32_t* table;

@@ -36,7 +36,7 @@ def _declare():
     cache = ctypes.POINTER(_CacheStruct)
     args = {
         "rhtq_serving_version": (ci, []),
-        "rhtq_matvec_workspace": (i64, [i64, i32]),
+        "rhtq_matvec_workspace": (i64, [i64, i32, i64]),
         "rhtq_matvec": (ci, [vp, ci, i64, i32, i32, vp, ci, vp, vp, vp, i64, ci, i32, ci, vp, ci, vp, i64, vp]),
         "rhtq_cache_append": (ci, [cache, vp, vp, ci, i64, i64, i64, i64, i64, vp, i32, vp, vp, i32, vp, vp, vp]),
         "rhtq_cache_read": (ci, [cache, vp, vp, ci, i64, vp, i32, vp, vp, i32, vp, vp, vp]),
@@ -166,7 +166,7 @@ def rhtq_matvec(packed, scales, x, signs=None, fmt: str = "int4", group: int = 0
         own = out is None
         if own:
             out = torch.empty((tokens, rows), dtype=out_dtype, device=dev)
-        need = lib.rhtq_matvec_workspace(tokens, n)
+        need = lib.rhtq_matvec_workspace(tokens, n, rows)
         work = torch.empty(need, dtype=torch.uint8, device=dev)
         _check(lib.rhtq_matvec(xc.data_ptr(), _IN[x.dtype], tokens, n, n if block is None else block, _p(s), int(rotated),
                                pc.data_ptr(), sc.data_ptr(), _p(tensor_scale), rows, _FMT[fmt], group, _SCALE[scale_dtype],
