@@ -221,7 +221,7 @@ int rhtq_cache_read(const rhtq_cache_t* cache, void* k_out, void* v_out, int out
 
 int64_t rhtq_paged_attention_workspace(int32_t seqs, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t width,
                                        int32_t page, int32_t window, int32_t sinks) {
-  if (seqs <= 0 || q_heads <= 0 || kv_heads <= 0 || head_dim <= 0 || width < 0 || page <= 0 || window < 0 || sinks < 0) return 0;
+  if (seqs <= 0 || kv_heads <= 0 || q_heads < kv_heads || head_dim <= 0 || width < 0 || page <= 0 || window < 0 || sinks < 0) return 0;
   const int32_t splits = rhtq::attention_splits(seqs, q_heads, kv_heads, width, page, window, sinks);
   return splits == 1 ? 0 : (int64_t)seqs * q_heads * splits * (head_dim + 2) * 4;
 }
@@ -266,6 +266,7 @@ int rhtq_paged_attention(const void* q, int in_dtype, int32_t seqs, int32_t q_he
   a.q_heads = q_heads;
   a.kv_heads = cache->kv_heads;
   a.each = q_heads / cache->kv_heads;
+  a.head_tiles = rhtq::attention_head_tiles(a.each);
   a.width = width;
   a.pages = cache->pages;
   a.page_log = log2_of(cache->page);

@@ -50,6 +50,7 @@ struct AttentionArgs {
   int32_t q_heads;
   int32_t kv_heads;
   int32_t each;               // q_heads / kv_heads
+  int32_t head_tiles;         // tiles of 8 query heads that share a key-value head
   int32_t width;
   int32_t pages;
   int32_t page_log;
@@ -61,6 +62,7 @@ struct AttentionArgs {
   float scale;
 };
 
+int32_t attention_head_tiles(int32_t each);
 // Parts that a sequence's positions are split into, from what the host knows (never from device memory).
 int32_t attention_splits(int32_t seqs, int32_t q_heads, int32_t kv_heads, int32_t width, int32_t page, int32_t window,
                          int32_t sinks);
