@@ -8,12 +8,15 @@
 //    codes), exactly.  q and the weights p_j s^v_j go in as two bytes, v = 256 hi + lo, of a 16-bit fixed point relative to the largest of
 //    their row: q over its head, the weights over a chunk of 64 positions.
 //  - S^T = K Q^T has positions as rows and, as its 16 columns, 8 query heads of one key-value head in hi and in lo bytes: lane (n, g) gets
-//    positions 4 g + i of each tile for column n, so after the softmax it holds the 16 weights that it supplies as an operand of
-//    O^T = V^T P^T, and nothing moves between lanes but the two halves of a score (a DPP rotation by 8) and two maxima a chunk.
+//    positions 4 g + i of each tile for column n.  Lanes n and n + 8 swap halves (a DPP rotation by 8) so that the lower one finishes
+//    positions 4 g, 4 g + 1 and the upper one 4 g + 2, 4 g + 3, and swap the finished weights back as bytes: the lane then holds the 16
+//    weights that it supplies as an operand of O^T = V^T P^T.
 //  - A lane loads one dword (at head_dim 128) of 16 rows of V; 4 x 4 byte transposes in registers make operands of four positions.
 //  - One pass: each wave keeps the running maximum m, sum l and the weighted sum o in fp32.  Parts (m, l, o) of waves and of
 //    splits join as m = max m_i, l = sum l_i 2^(m_i - m), o likewise, in a fixed order.
 // Scores are in units of log2, so a weight is one v_exp_f32.
+#include <type_traits>
+
 #include "rhtq_internal.h"
 #include "rhtq_serving_device.h"
 #include "rhtq_serving_internal.h"
@@ -22,12 +25,14 @@ namespace rhtq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kGroups = kThreads / 16;
 constexpr int kWaves = kThreads / 64;
 constexpr int kHeads = 8;               // query heads of a tile
 constexpr int kChunk = 4;               // tiles that a wave takes at once: 64 positions, the depth of one product
 constexpr int kLeastTiles = kWaves * kChunk;   // tiles of a part worth a workgroup
+constexpr int kMostTiles = 512;          // and at most: 8192 positions
+constexpr int kResident = 768;
 constexpr float kNone = -INFINITY;
+constexpr float kTiny = 7.7037197775489434e-34f;   // 2^-110
 constexpr float kLargest = 32639.0f;    // 127 * 256 + 127: the largest two-byte value
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
@@ -45,42 +50,73 @@ __device__ __forceinline__ void finish(const AttentionArgs& a, int64_t row, floa
   store_row<T, E>(a.out, row * (16 * E) + j * E, o);
 }
 
-// Largest of the four lanes 16 apart.
+// Values of lanes 16 and 32 apart side by side: v_permlane16_swap / v_permlane32_swap of a register with itself leave the even rows' (the
+// lower half's) values in one result and the odd rows' (the upper half's) in the other.
 __device__ __forceinline__ float max_over_groups(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16));
-  return fmaxf(v, __shfl_xor(v, 32));
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(h[0]), __uint_as_float(h[1]));
+}
+
+// Largest over the lanes that share a query head: 8 apart (in a row of 16) and 16 and 32 apart.
+__device__ __forceinline__ float max_over_head(float v) { return max_over_groups(fmaxf(v, lane_xor16<3>(v))); }
+
+// Where a chunk's tiles lie: first position (-1: none) and page.  The same in all lanes.
+struct Place {
+  int pos[kChunk];
+  int page[kChunk];
+};
+
+// `first` is the same in all lanes, so the table's entries come by scalar loads, which no wait for the codes holds up.  end > first.
+__device__ __forceinline__ void locate(const AttentionArgs& a, const Visible& vis, const int32_t* table, int first, int end, Place& c) {
+  int entry[kChunk], at[kChunk];
+#pragma unroll
+  for (int t = 0; t < kChunk; ++t) {
+    at[t] = tile_at(vis, first + t < end ? first + t : end - 1) * kTile;   // below the table's end, as every visible position
+    entry[t] = table[at[t] >> a.page_log];
+  }
+#pragma unroll
+  for (int t = 0; t < kChunk; ++t) {
+    const bool there = first + t < end && (uint32_t)entry[t] < (uint32_t)a.pages;
+    c.page[t] = there ? entry[t] : 0;
+    c.pos[t] = there ? at[t] : -1;
+  }
 }
 
 // What a wave has loaded of a chunk.
-template <int D>
+template <int D, bool F32>
 struct Loaded {
-  u32x4 k[kChunk][D >= 128 ? D / 128 : 1];      // D 64: two dwords used
-  uint32_t v[kChunk][4][D >= 128 ? D / 128 : 1];
-  uint32_t ks[kChunk][4], vs[kChunk][4];        // raw scales: four fp32, or four fp16 in two words
-  int pos[kChunk];                              // first position of the tile, -1: none
+  static constexpr int H = D >= 128 ? D / 128 : 1;
+  u32x4 k[kChunk][H];                           // D 64: two dwords used
+  uint32_t v[kChunk][4][H];
+  uint32_t ks[kChunk][F32 ? 2 : 1], vs[kChunk][F32 ? 2 : 1];   // this lane's two scales: fp32, or two fp16 in a word
 };
 
+// First slot of a tile, counted in rows.  A tile of no page takes page 0, which its weights of 0 make harmless, so that its loads need no
+// branch.
+__device__ __forceinline__ int64_t slot_of(const AttentionArgs& a, int kv, const Place& at, int t) {
+  const int pos = at.pos[t];
+  return (((int64_t)at.page[t] * a.kv_heads + kv) << a.page_log) + (pos >= 0 ? pos & ((1 << a.page_log) - 1) : 0);
+}
+
+template <bool F32, int N>
+__device__ __forceinline__ void load_scales(const void* p, int64_t slot, uint32_t (&s)[N]) {
+  if constexpr (F32) {
+    const u32x2 x = *reinterpret_cast<const u32x2*>(static_cast<const float*>(p) + slot);
+    s[0] = x.x;
+    s[1] = x.y;
+  } else {
+    s[0] = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + slot);
+  }
+}
+
 template <int D, bool F32>
-__device__ __forceinline__ void load_chunk(const AttentionArgs& a, const Visible& vis, const int32_t* table, int kv, int first,
-                                           int end, Loaded<D>& c) {
+__device__ __forceinline__ void load_keys(const AttentionArgs& a, int kv, const Place& at, Loaded<D, F32>& c) {
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int t = 0; t < kChunk; ++t) {
-    const int pos = first + t < end ? tile_at(vis, first + t) * kTile : -1;
-    const int page = pos >= 0 ? page_at(table, a.width, a.pages, pos >> a.page_log) : -1;
-    c.pos[t] = page >= 0 ? pos : -1;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c.vs[t][i] = c.ks[t][i] = 0;
-    if (page < 0) {
-#pragma unroll
-      for (int h = 0; h < (D >= 128 ? D / 128 : 1); ++h) {
-        c.k[t][h] = u32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c.v[t][i][h] = 0;
-      }
-      continue;
-    }
-    const int64_t slot = (((int64_t)page * a.kv_heads + kv) << a.page_log) + (pos & ((1 << a.page_log) - 1));
+    const int64_t slot = slot_of(a, kv, at, t);
     const uint8_t* k = a.k_codes + slot * (D / 2) + n * (D / 2);
     if constexpr (D == 64) {
       const u32x2 w = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(k + 8 * g));
@@ -90,6 +126,16 @@ __device__ __forceinline__ void load_chunk(const AttentionArgs& a, const Visible
       for (int h = 0; h < D / 128; ++h)
         c.k[t][h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(k + 64 * h + 16 * g));
     }
+    load_scales<F32>(a.k_scales, slot + 4 * g + 2 * (n >> 3), c.ks[t]);
+  }
+}
+
+template <int D, bool F32>
+__device__ __forceinline__ void load_values(const AttentionArgs& a, int kv, const Place& at, Loaded<D, F32>& c) {
+  const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int t = 0; t < kChunk; ++t) {
+    const int64_t slot = slot_of(a, kv, at, t);
     const uint8_t* v = a.v_codes + slot * (D / 2) + 4 * g * (D / 2) + n * (D / 32);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -101,30 +147,18 @@ __device__ __forceinline__ void load_chunk(const AttentionArgs& a, const Visible
         c.v[t][i][1] = w.y;
       }
     }
-    if constexpr (F32) {
-      const u32x4 x = *reinterpret_cast<const u32x4*>(static_cast<const float*>(a.k_scales) + slot + 4 * g);
-      const u32x4 y = *reinterpret_cast<const u32x4*>(static_cast<const float*>(a.v_scales) + slot + 4 * g);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        c.ks[t][i] = x[i];
-        c.vs[t][i] = y[i];
-      }
-    } else {
-      const u32x2 x = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(a.k_scales) + slot + 4 * g);
-      const u32x2 y = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(a.v_scales) + slot + 4 * g);
-      c.ks[t][0] = x.x;
-      c.ks[t][1] = x.y;
-      c.vs[t][0] = y.x;
-      c.vs[t][1] = y.y;
-    }
+    load_scales<F32>(a.v_scales, slot + 4 * g + 2 * (n >> 3), c.vs[t]);
   }
 }
 
-template <bool F32>
-__device__ __forceinline__ float scale_of(const uint32_t (&s)[4], int i) {
+template <bool F32, int N>
+__device__ __forceinline__ float scale_of(const uint32_t (&s)[N], int i) {
   if constexpr (F32) return __uint_as_float(s[i]);
-  else return __half2float(__ushort_as_half((uint16_t)(s[i >> 1] >> (16 * (i & 1)))));
+  else return __half2float(__ushort_as_half((uint16_t)(s[0] >> (16 * i))));
 }
+
+// a where the lane's mask is all ones, b where it is 0: one v_bfi_b32.
+__device__ __forceinline__ int select(int mask, int a, int b) { return (a & mask) | (b & ~mask); }
 
 // Even codes of four bytes as 16 c in each byte, and odd ones.
 __device__ __forceinline__ int even_codes(uint32_t w) { return (int)((w << 4) & 0xF0F0F0F0u); }
@@ -147,16 +181,12 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t sq[16][D];
   __shared__ float sf[kHeads];
   __shared__ float sm[kWaves][kHeads], sl[kWaves][kHeads];
-  __shared__ float so[kWaves][kHeads][D];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ __attribute__((aligned(16))) float so[kWaves][kHeads][D + 4];   // + 4: columns start in other banks
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int group = threadIdx.x >> 4, j = threadIdx.x & 15;
-  int64_t b = blockIdx.x;
-  const int split = (int)(b % a.splits);
-  b /= a.splits;
-  const int head0 = (int)(b % a.head_tiles) * kHeads;
-  b /= a.head_tiles;
-  const int kv = (int)(b % a.kv_heads), s = (int)(b / a.kv_heads);
+  const int split = blockIdx.x, s = blockIdx.z;
+  const int kv = blockIdx.y / a.head_tiles, head0 = (blockIdx.y - kv * a.head_tiles) * kHeads;
   const int heads = a.each - head0 < kHeads ? a.each - head0 : kHeads;
   const Visible vis = visible_of(a.lengths[s], a.width, 1 << a.page_log, a.window, a.sinks);
   const int per = tiles_per_split(vis.tiles, a.splits, kLeastTiles);
@@ -164,9 +194,15 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
   const int32_t* table = a.table + (int64_t)s * a.width;
   const int64_t row0 = (int64_t)s * a.q_heads + kv * a.each + head0;   // of [seqs][q_heads]
 
-  Loaded<D> c;
   int at = t0 + wave * kChunk;
-  if (at < t1) load_chunk<D, F32>(a, vis, table, kv, at, t1, c);
+  Place next;
+  Loaded<D, F32> c;
+  if (a.pages == 0) at = t1;              // no page can be named
+  if (at < t1) {
+    locate(a, vis, table, at, t1, next);
+    load_keys<D, F32>(a, kv, next, c);
+    load_values<D, F32>(a, kv, next, c);
+  }
 
   // q: 16 lanes rotate a head and leave its bytes as operand rows h (hi) and 8 + h (lo)
   if (group < kHeads) {
@@ -196,15 +232,23 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
 #pragma unroll
   for (int i = 0; i < NK; ++i) q[i] = *reinterpret_cast<const i32x4*>(&sq[n][(4 * i + g) * 16]);
   const float factor = sf[n & 7];
-  const int w_own = n < 8 ? 256 : 1, w_other = n < 8 ? 1 : 256;
-  // the weights' bytes: 1.5 * 2^23 in front makes the sum's low bits the whole number; hi is its second byte after + 128
-  const float magic = 12582912.0f + (n < 8 ? 128.0f : 0.0f);
-  const uint32_t pick = n < 8 ? 0x0C0C0501u : 0x0C0C0400u;
+  // the weights' bytes: 1.5 * 2^23 in front makes the sum's low bits the whole number, + 128 its second byte hi; the first is then
+  // lo + 128.  Of the lane's own two weights and its partner's, the lower lane supplies the hi bytes, the upper one the lo bytes.
+  const float magic = 12582912.0f + 128.0f;
+  const uint32_t pick = n < 8 ? 0x07050301u : 0x02000604u, flip = n < 8 ? 0u : 0x80808080u;
+  const int upper = n >= 8 ? -1 : 0;
 
   float m = kNone, l = 0.0f;
   float o[E][4] = {};                     // element E (4 g + i) + e of column n
-  while (at < t1) {
-    float x[kChunk][4], top = kNone;
+  // One chunk.  `more`: loads of the next one are issued as soon as registers are free, keys after the scores, values after their
+  // transposition.  A constant, so that what is in flight is known where a load is waited for.
+  auto chunk = [&](auto more) {
+    int positions[kChunk];
+#pragma unroll
+    for (int t = 0; t < kChunk; ++t) positions[t] = next.pos[t];
+    at += kWaves * kChunk;
+    if constexpr (more) locate(a, vis, table, at, t1, next);
+    float x[kChunk][2], top = kNone;
 #pragma unroll
     for (int t = 0; t < kChunk; ++t) {
       i32x4 d = {0, 0, 0, 0};
@@ -221,25 +265,36 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
           d = __builtin_amdgcn_mfma_i32_16x16x64_i8(k1, q[2 * h + 1], d, 0, 0, 0);
         }
       }
+      const int pos = positions[t];
+      const bool cut = pos < 0 || pos + kTile > vis.len || (pos < vis.start && pos + kTile > vis.sinks);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int v = __mul24(d[i], w_own) + __mul24(lane_xor16<3>(d[i]), w_other);
-        x[t][i] = (float)v * (scale_of<F32>(c.ks[t], i) * factor);
+      for (int i = 0; i < 2; ++i) {
+        const int own = select(upper, d[2 + i], d[i]), other = lane_xor16<3>(select(upper, d[i], d[2 + i]));
+        const int hi = select(upper, other, own), lo = select(upper, own, other);
+        x[t][i] = (float)(256 * hi + lo) * (scale_of<F32>(c.ks[t], i) * factor);
       }
-      const int pos = c.pos[t];
-      if (pos < 0 || pos + kTile > vis.len || (pos < vis.start && pos + kTile > vis.sinks)) {
+      if (cut) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (pos < 0 || !is_visible(vis, pos + 4 * g + i)) x[t][i] = kNone;
+        for (int i = 0; i < 2; ++i) {
+          const int at_pos = pos + 4 * g + 2 * (n >> 3) + i;
+          const bool seen = (at_pos < vis.len) & (pos >= 0) & ((at_pos >= vis.start) | (at_pos < vis.sinks));
+          x[t][i] = seen ? x[t][i] : kNone;
+        }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) top = fmaxf(top, x[t][i]);
+      top = fmaxf(top, fmaxf(x[t][0], x[t][1]));
     }
-    const float mn = fmaxf(m, max_over_groups(top));
+    if constexpr (more) load_keys<D, F32>(a, kv, next, c);
+    const float mn = fmaxf(m, max_over_head(top));
     const float base = mn == kNone ? 0.0f : mn;
     const float fade = m == kNone ? 0.0f : __builtin_amdgcn_exp2f(m - base);
+    if (__any(mn != m)) {
+      l *= fade;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[e][i] *= fade;
+    }
     m = mn;
-    l *= fade;
     top = 0.0f;
     {
       // a score is one rounded number wherever it is used: contracted into x - base it could exceed its own maximum
@@ -247,28 +302,30 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
 #pragma unroll
       for (int t = 0; t < kChunk; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
           const float p = __builtin_amdgcn_exp2f(x[t][i] - base);
           l += p;
           // what lies behind the last position may hold anything: it has weight 0 whatever its scale
-          x[t][i] = x[t][i] == kNone ? 0.0f : p * scale_of<F32>(c.vs[t], i);
+          const float weight = p * scale_of<F32>(c.vs[t], i);
+          x[t][i] = x[t][i] == kNone ? 0.0f : weight;
           top = fmaxf(top, x[t][i]);
         }
     }
-    top = max_over_groups(top);
-    const float unit = top > 0.0f ? kLargest / top : 0.0f;
+    top = max_over_head(top);
+    // weights below 2^-110 are none: their reciprocal stays finite
+    const float unit = top > kTiny ? kLargest * __builtin_amdgcn_rcpf(top) : 0.0f;
     i32x4 p;
 #pragma unroll
     for (int t = 0; t < kChunk; ++t) {
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(__builtin_fmaf(x[t][i], unit, magic));
-      const uint32_t lo = __builtin_amdgcn_perm(w[1], w[0], pick), hi = __builtin_amdgcn_perm(w[3], w[2], pick);
-      p[t] = (int)__builtin_amdgcn_perm(hi, lo, 0x05040100u);
+      const uint32_t w0 = __float_as_uint(__builtin_fmaf(x[t][0], unit, magic));
+      const uint32_t w1 = __float_as_uint(__builtin_fmaf(x[t][1], unit, magic));
+      const uint32_t own = __builtin_amdgcn_perm(w1, w0, 0x05040100u);
+      const uint32_t other = (uint32_t)lane_xor16<3>((int)own);
+      p[t] = (int)(__builtin_amdgcn_perm(other, own, pick) ^ flip);
     }
-    const float back = top * (1.0f / (16.0f * kLargest)) * (float)w_own;
+    const float back = top * (1.0f / (16.0f * kLargest)) * (n < 8 ? 256.0f : 1.0f);
     // V: byte r of the four rows of a lane's tile, transposed; its low nibbles are element 2 r, its high ones 2 r + 1
-    constexpr int R = D / 32;              // bytes of a row that a lane holds
+    constexpr int R = D / 32;
     uint32_t col[R][kChunk];
 #pragma unroll
     for (int t = 0; t < kChunk; ++t)
@@ -284,8 +341,7 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
           col[4 * h + 3][t] = __builtin_amdgcn_perm(y1, x1, 0x07060302u);
         }
       }
-    at += kWaves * kChunk;
-    if (at < t1) load_chunk<D, F32>(a, vis, table, kv, at, t1, c);
+    if constexpr (more) load_values<D, F32>(a, kv, next, c);
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -295,19 +351,28 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
         for (int t = 0; t < kChunk; ++t) v[t] = odd ? odd_codes(col[r][t]) : even_codes(col[r][t]);
         d = __builtin_amdgcn_mfma_i32_16x16x64_i8(v, p, d, 0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[2 * r + odd][i] = __builtin_fmaf((float)d[i], back, o[2 * r + odd][i] * fade);
+        for (int i = 0; i < 4; ++i) o[2 * r + odd][i] = __builtin_fmaf((float)d[i], back, o[2 * r + odd][i]);
       }
+  };
+  if (at < t1) {
+    while (at + kWaves * kChunk < t1) chunk(std::true_type{});
+    chunk(std::false_type{});
   }
   // both halves of a column's sum; l over the lanes that share it
+  l += lane_xor16<3>(l);
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
 #pragma unroll
   for (int e = 0; e < E; ++e)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float v = o[e][i] + lane_xor16<3>(o[e][i]);
-      if (n < kHeads) so[wave][n][E * (4 * g + i) + e] = v;
-    }
+    for (int i = 0; i < 4; ++i) o[e][i] += lane_xor16<3>(o[e][i]);
+  if (n < kHeads) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < E; e += 4)
+        *reinterpret_cast<f32x4*>(&so[wave][n][E * (4 * g + i) + e]) = f32x4{o[e][i], o[e + 1][i], o[e + 2][i], o[e + 3][i]};
+  }
   if (lane < kHeads) {
     sm[wave][lane] = m;
     sl[wave][lane] = l;
@@ -340,37 +405,59 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
   }
 }
 
+// One wave per query head: lane k of a stretch of 64 parts has that part's factor, and the wave's four groups of 16 lanes take the
+// parts' sums in turn.
 template <int T, int E>
 __global__ __launch_bounds__(kThreads) void join_kernel(AttentionArgs a) {
   constexpr int D = 16 * E;
-  const int j = threadIdx.x & 15;
-  const int64_t row = (int64_t)blockIdx.x * kGroups + (threadIdx.x >> 4);
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  const int64_t row = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
   if (row >= (int64_t)a.seqs * a.q_heads) return;
   const float* ml = a.partial + (int64_t)a.seqs * a.q_heads * a.splits * D + 2 * row * a.splits;
   const float* part = a.partial + row * a.splits * D;
   float m = kNone;
-  for (int k = 0; k < a.splits; ++k) m = fmaxf(m, ml[2 * k]);
-  float l = 0.0f, o[E] = {};
-  for (int k = 0; k < a.splits; ++k) {
-    if (ml[2 * k] == kNone) continue;
-    const float f = __builtin_amdgcn_exp2f(ml[2 * k] - m);
-    l += ml[2 * k + 1] * f;
-    float v[E];
-    load_row<RHTQ_IN_F32, E>(part, (int64_t)k * D + j * E, v);
+  for (int k = lane; k < a.splits; k += 64) m = fmaxf(m, ml[2 * k]);
 #pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = __builtin_fmaf(f, v[i], o[i]);
+  for (int d = 32; d; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+  float l = 0.0f, o[E] = {};
+  for (int first = 0; first < a.splits; first += 64) {
+    const int k = first + lane;
+    const float f = k < a.splits && ml[2 * k] != kNone ? __builtin_amdgcn_exp2f(ml[2 * k] - m) : 0.0f;
+    if (k < a.splits) l += f * ml[2 * k + 1];
+    const int some = a.splits - first < 64 ? a.splits - first : 64;
+    for (int i = 0; i < some; i += 16) {
+      float v[4][E];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int mine = i + 4 * u + g < some ? i + 4 * u + g : some - 1;
+        load_row<RHTQ_IN_F32, E>(part, (int64_t)(first + mine) * D + j * E, v[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float w = __shfl(f, i + 4 * u + g);      // 0 beyond the last part
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = __builtin_fmaf(w, v[u][e], o[e]);
+      }
+    }
   }
-  finish<T, E>(a, row, l, o);
+#pragma unroll
+  for (int d = 32; d; d >>= 1) l += __shfl_xor(l, d);
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    o[e] += __shfl_xor(o[e], 16);
+    o[e] += __shfl_xor(o[e], 32);
+  }
+  if (g == 0) finish<T, E>(a, row, l, o);
 }
 
 template <int T, int E>
 hipError_t launch_te(const AttentionArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)((int64_t)a.seqs * a.kv_heads * a.head_tiles * a.splits));
+  const dim3 grid((unsigned)a.splits, (unsigned)(a.kv_heads * a.head_tiles), (unsigned)a.seqs);
   if (a.scale_dtype == RHTQ_SCALE_F32) hipLaunchKernelGGL((attention_kernel<T, E, true>), grid, dim3(kThreads), 0, s, a);
   else hipLaunchKernelGGL((attention_kernel<T, E, false>), grid, dim3(kThreads), 0, s, a);
   const int64_t rows = (int64_t)a.seqs * a.q_heads;
   if (a.splits > 1)
-    hipLaunchKernelGGL((join_kernel<T, E>), dim3((unsigned)((rows + kGroups - 1) / kGroups)), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((join_kernel<T, E>), dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
@@ -395,7 +482,10 @@ int32_t attention_splits(int32_t seqs, int32_t q_heads, int32_t kv_heads, int32_
     if (most < tiles) tiles = most;
   }
   const int64_t rows = (int64_t)seqs * kv_heads * attention_head_tiles(q_heads / kv_heads);
-  int64_t want = (2048 + rows - 1) / (rows > 0 ? rows : 1);
+  // parts that fill the chip's 768 resident workgroups, and of no more than 8192 positions, so that a long sequence beside short
+  // ones does not end alone; at least 256 positions, one chunk a wave
+  int64_t want = rows > 0 ? (kResident + rows - 1) / rows : 1;
+  if (want < (tiles + kMostTiles - 1) / kMostTiles) want = (tiles + kMostTiles - 1) / kMostTiles;
   const int64_t most = (tiles + kLeastTiles - 1) / kLeastTiles;
   if (want > most) want = most;
   if (want > 1024) want = 1024;

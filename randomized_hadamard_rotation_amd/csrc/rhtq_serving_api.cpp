@@ -239,7 +239,9 @@ int rhtq_paged_attention(const void* q, int in_dtype, int32_t seqs, int32_t q_he
   if (q_seq_stride < 0 || q_head_stride < 0 || q_seq_stride % 8 || q_head_stride % 8) return RHTQ_EINVAL;
   if (seqs == 0) return RHTQ_OK;
   const int32_t splits = rhtq::attention_splits(seqs, q_heads, cache->kv_heads, width, cache->page, window, sinks);
-  if ((int64_t)seqs * q_heads * splits > INT32_MAX) return RHTQ_EINVAL;
+  if (seqs > 65535 || (int64_t)cache->kv_heads * rhtq::attention_head_tiles(q_heads / cache->kv_heads) > 65535 ||
+      (int64_t)seqs * q_heads * splits > INT32_MAX)
+    return RHTQ_EUNSUPPORTED;   // a grid's limits
   if (!q || !out || !lengths || !aligned(q, 16) || !aligned(out, 16) || !aligned(lengths, 4) || !aligned(k_signs, 4) ||
       !aligned(v_signs, 4))
     return RHTQ_EINVAL;
