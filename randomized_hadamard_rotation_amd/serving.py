@@ -13,8 +13,7 @@ from typing import NamedTuple
 import torch
 
 from . import (_DEFAULT_GROUP, _DEFAULT_SCALE, _FMT, _SCALE, RHTQ_IN_BF16, RHTQ_IN_F16, RHTQ_IN_F32, RHTQ_SCALE_F16,
-               RHTQ_SCALE_F32, _check, _expect, _keep_for, _resolve_stream, _same_device, _scale_torch_dtype,
-               _signs_tensor, lib, scale_shape)
+               RHTQ_SCALE_F32, _check, _expect, _resolve_stream, _same_device, _scale_torch_dtype, _signs_tensor, lib, scale_shape)
 
 EXPORTED_SERVING = ["rhtq_serving_version", "rhtq_matvec_workspace", "rhtq_matvec", "rhtq_cache_append", "rhtq_cache_read",
                     "rhtq_paged_attention_workspace", "rhtq_paged_attention", "rhtq_pages_workspace", "rhtq_pages_reserve",
@@ -22,6 +21,56 @@ EXPORTED_SERVING = ["rhtq_serving_version", "rhtq_matvec_workspace", "rhtq_matve
 
 _IN = {torch.bfloat16: RHTQ_IN_BF16, torch.float16: RHTQ_IN_F16, torch.float32: RHTQ_IN_F32}
 _SCALE_OF = {torch.float32: RHTQ_SCALE_F32, torch.float16: RHTQ_SCALE_F16}
+_U8, _I8, _I32 = torch.uint8, torch.int8, torch.int32
+_SCALE_TORCH = {"f32": torch.float32, "f16": torch.float16, "e4m3": torch.uint8, "e8m0": torch.uint8}
+
+
+# A decode step makes a few of these calls per layer, each a few microseconds of kernels, so the host's share counts: every check below
+# first takes a short form that only reads attributes, and goes to the spelled-out one, which raises, when that fails.
+
+class _On:
+    """The device and stream a call runs on.  Makes the tensors' device current; copies and fills of the wrapper go to its current
+    stream, which a caller's other stream then waits for (follow), and that one keeps what the wrapper allocated (keep)."""
+    __slots__ = ("raw", "stream", "before")
+
+    def __init__(self, index):
+        self.before = -1
+        now = torch.cuda.current_device()
+        if now != index:
+            self.before = now
+            torch.cuda.set_device(index)
+        self.stream = None
+        self.raw = _raw_stream(index)
+
+    def follow(self, stream):
+        st, other = _resolve_stream(stream)
+        if other:
+            self.raw, self.stream = st.cuda_stream, st
+
+    def keep(self, *owned):
+        if self.stream is not None:
+            for t in owned:
+                if t is not None:
+                    t.record_stream(self.stream)
+
+    def leave(self):
+        if self.before >= 0:
+            torch.cuda.set_device(self.before)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _one_device(index, named):
+    """Every tensor on device `index`; raises as the other calls do."""
+    if index >= 0:
+        for t in named.values():
+            if t is not None and t.get_device() != index:
+                break
+        else:
+            return
+    first = next(t for t in named.values() if t is not None)
+    _same_device(first.device, **named)
 
 
 class _CacheStruct(ctypes.Structure):
@@ -88,28 +137,34 @@ def rhtq_cache_new(pages: int, kv_heads: int, page: int, head_dim: int, scale_dt
 def _cache_struct(cache, layered):
     """The C struct of a cache whose four tensors agree; with `layered`, a leading axis is taken."""
     k, ks, v, vs = cache
-    dims = k.dim()
-    if dims != 4 and not (layered and dims == 5):
-        raise ValueError("k_codes must be [pages][kv_heads][page][head_dim/2]" + (", with layers in front or not" if layered else ""))
-    if k.dtype != torch.uint8:
-        raise ValueError(f"k_codes: dtype {k.dtype}, expected torch.uint8")
-    if ks.dtype not in _SCALE_OF:
-        raise ValueError(f"k_scales: dtype {ks.dtype}, expected float16 or float32")
     shape = k.shape
-    _expect(k, "k_codes", torch.uint8, shape)
-    _expect(ks, "k_scales", ks.dtype, shape[:-1])
-    _expect(v, "v_codes", torch.uint8, shape)
-    _expect(vs, "v_scales", ks.dtype, shape[:-1])
+    dims = len(shape)
+    sdt = ks.dtype
+    if not (k.dtype is _U8 and v.dtype is _U8 and vs.dtype is sdt and sdt in _SCALE_OF and (dims == 4 or layered and dims == 5)
+            and v.shape == shape and ks.shape == shape[:-1] and vs.shape == ks.shape and k.is_contiguous() and ks.is_contiguous()
+            and v.is_contiguous() and vs.is_contiguous()):
+        if dims != 4 and not (layered and dims == 5):
+            raise ValueError("k_codes must be [pages][kv_heads][page][head_dim/2]" + (", with layers in front or not" if layered else ""))
+        if sdt not in _SCALE_OF:
+            raise ValueError(f"k_scales: dtype {sdt}, expected float16 or float32")
+        for t, name, dtype, want in ((k, "k_codes", _U8, shape), (ks, "k_scales", sdt, shape[:-1]), (v, "v_codes", _U8, shape),
+                                     (vs, "v_scales", sdt, shape[:-1])):
+            _expect(t, name, dtype, want)
     return _CacheStruct(k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(), shape[0] if dims == 5 else 1, shape[-4],
-                        shape[-3], shape[-2], 2 * shape[-1], _SCALE_OF[ks.dtype])
+                        shape[-3], shape[-2], 2 * shape[-1], _SCALE_OF[sdt])
 
 
 def _int32(t, name, shape):
-    _expect(t, name, torch.int32, shape)
+    if not (t.dtype is _I32 and t.shape == shape and t.is_contiguous()):
+        _expect(t, name, _I32, shape)
 
 
-def _cache_signs(signs, dim, device):
-    return None if signs is None else _signs_tensor(signs, dim, device)
+def _signs(signs, n, x):
+    """Device int8 [n] (marshalling only)."""
+    if signs is None or (type(signs) is torch.Tensor and signs.dtype is _I8 and signs.dim() == 1 and signs.shape[0] == n
+                         and signs.is_contiguous() and signs.get_device() == x.get_device()):
+        return signs
+    return _signs_tensor(signs, n, x.device)
 
 
 def _p(t):
@@ -130,7 +185,8 @@ def rhtq_matvec(packed, scales, x, signs=None, fmt: str = "int4", group: int = 0
         raise ValueError(f"unknown fmt {fmt!r}")
     if x.dim() != 2 or packed.dim() != 2:
         raise ValueError("x must be 2-D [tokens][n] and packed 2-D [rows][n/2]")
-    if x.dtype not in _IN:
+    in_type = _IN.get(x.dtype)
+    if in_type is None:
         raise ValueError("x must be bfloat16, float16 or float32")
     tokens, n = x.shape
     rows = packed.shape[0]
@@ -138,11 +194,11 @@ def rhtq_matvec(packed, scales, x, signs=None, fmt: str = "int4", group: int = 0
         scale_dtype = _DEFAULT_SCALE[fmt]
     if group == 0:
         group = _DEFAULT_GROUP.get(fmt, 0)
-    if packed.dtype != torch.uint8 or packed.shape[1] * 2 != n:
+    if packed.dtype is not _U8 or packed.shape[1] * 2 != n:
         raise ValueError(f"packed: {packed.dtype} {tuple(packed.shape)}, expected uint8 {(rows, n // 2)}")
     sshape = scale_shape(rows, n, fmt, group)
-    sdt = _scale_torch_dtype(scale_dtype)
-    if scales.dtype != sdt or tuple(scales.shape) != sshape:
+    sdt = _SCALE_TORCH.get(scale_dtype) or _scale_torch_dtype(scale_dtype)
+    if scales.dtype is not sdt or scales.shape != sshape:
         raise ValueError(f"scales: {scales.dtype} {tuple(scales.shape)}, expected {sdt} {sshape}")
     if fmt == "nvfp4":
         if tensor_scale is None:
@@ -153,26 +209,31 @@ def rhtq_matvec(packed, scales, x, signs=None, fmt: str = "int4", group: int = 0
         tensor_scale = None
     if out_dtype is None:
         out_dtype = x.dtype if out is None else out.dtype
-    if out_dtype not in _IN:
+    out_type = _IN.get(out_dtype)
+    if out_type is None:
         raise ValueError("out_dtype must be bfloat16, float16 or float32")
     if out is not None:
         _expect(out, "out", out_dtype, (tokens, rows))
-    dev = x.device
-    _same_device(dev, x=x, packed=packed, scales=scales, tensor_scale=tensor_scale, out=out)
-    xc, pc, sc = x.contiguous(), packed.contiguous(), scales.contiguous()
-    s = None if rotated else _signs_tensor(signs, n, dev)
-    with torch.cuda.device(dev):
-        st, other = _resolve_stream(stream)
+    index = x.get_device()
+    _one_device(index, {"x": x, "packed": packed, "scales": scales, "tensor_scale": tensor_scale, "out": out})
+    on = _On(index)
+    try:
+        xc, pc, sc = x.contiguous(), packed.contiguous(), scales.contiguous()
+        s = None if rotated else _signs(signs, n, x)
         own = out is None
         if own:
-            out = torch.empty((tokens, rows), dtype=out_dtype, device=dev)
+            out = x.new_empty((tokens, rows), dtype=out_dtype)
         need = lib.rhtq_matvec_workspace(tokens, n, rows)
-        work = torch.empty(need, dtype=torch.uint8, device=dev)
-        _check(lib.rhtq_matvec(xc.data_ptr(), _IN[x.dtype], tokens, n, n if block is None else block, _p(s), int(rotated),
+        work = x.new_empty(need, dtype=_U8)
+        if stream is not None:
+            on.follow(stream)
+        _check(lib.rhtq_matvec(xc.data_ptr(), in_type, tokens, n, n if block is None else block, _p(s), rotated,
                                pc.data_ptr(), sc.data_ptr(), _p(tensor_scale), rows, _FMT[fmt], group, _SCALE[scale_dtype],
-                               out.data_ptr(), _IN[out_dtype], work.data_ptr(), need, st.cuda_stream), "rhtq_matvec")
-        _keep_for(st, other, xc if xc is not x else None, pc if pc is not packed else None, sc if sc is not scales else None, s,
-                  work, out if own else None)
+                               out.data_ptr(), out_type, work.data_ptr(), need, on.raw), "rhtq_matvec")
+        on.keep(xc if xc is not x else None, pc if pc is not packed else None, sc if sc is not scales else None, s, work,
+                out if own else None)
+    finally:
+        on.leave()
     return out
 
 
@@ -181,8 +242,9 @@ def _rows_of(cache, table, lengths, starts, tokens):
     c = _cache_struct(cache, False)
     if table.dim() != 2:
         raise ValueError("table must be 2-D [seqs][width]")
-    seqs, width = table.shape
-    _int32(table, "table", (seqs, width))
+    shape = table.shape
+    seqs, width = shape
+    _int32(table, "table", shape)
     _int32(lengths, "lengths", (seqs,))
     if starts is not None:
         _int32(starts, "starts", (seqs + 1,))
@@ -207,23 +269,28 @@ def rhtq_cache_append(cache: RhtqCache, k, v, table, lengths, starts=None, k_sig
     of sequence s, up to lengths[s] - 1; starts None: one row for each sequence.  Rows of no sequence, or on no page, are passed over."""
     if k.dim() != 3 or v.dim() != 3 or k.shape != v.shape:
         raise ValueError("k and v must be 3-D [tokens][kv_heads][head_dim], alike")
-    if k.dtype not in _IN or v.dtype != k.dtype:
+    in_type = _IN.get(k.dtype)
+    if in_type is None or v.dtype != k.dtype:
         raise ValueError("k and v must both be bfloat16, float16 or float32")
-    tokens = k.shape[0]
+    tokens, kv_heads, dim = k.shape
     c, seqs, width = _rows_of(cache, table, lengths, starts, tokens)
-    if (c.kv_heads, c.head_dim) != tuple(k.shape[1:]):
+    if c.kv_heads != kv_heads or c.head_dim != dim:
         raise ValueError(f"k: {tuple(k.shape)}, expected {(tokens, c.kv_heads, c.head_dim)}")
-    dev = k.device
-    _same_device(dev, k=k, v=v, k_codes=cache.k_codes, k_scales=cache.k_scales, v_codes=cache.v_codes, v_scales=cache.v_scales,
-                 table=table, lengths=lengths, starts=starts)
-    with torch.cuda.device(dev):
-        ks, vs = _cache_signs(k_signs, c.head_dim, dev), _cache_signs(v_signs, c.head_dim, dev)
+    index = k.get_device()
+    _one_device(index, {"k": k, "v": v, "k_codes": cache[0], "k_scales": cache[1], "v_codes": cache[2], "v_scales": cache[3],
+                        "table": table, "lengths": lengths, "starts": starts})
+    on = _On(index)
+    try:
+        ks, vs = _signs(k_signs, dim, k), _signs(v_signs, dim, k)
         kc, vc = _row_strides(k), _row_strides(v)
-        st, other = _resolve_stream(stream)
-        _check(lib.rhtq_cache_append(ctypes.byref(c), kc.data_ptr(), vc.data_ptr(), _IN[k.dtype], tokens, kc.stride(0), kc.stride(1),
+        if stream is not None:
+            on.follow(stream)
+        _check(lib.rhtq_cache_append(ctypes.byref(c), kc.data_ptr(), vc.data_ptr(), in_type, tokens, kc.stride(0), kc.stride(1),
                                      vc.stride(0), vc.stride(1), table.data_ptr(), width, lengths.data_ptr(), _p(starts), seqs,
-                                     _p(ks), _p(vs), st.cuda_stream), "rhtq_cache_append")
-        _keep_for(st, other, ks, vs, kc if kc is not k else None, vc if vc is not v else None)
+                                     _p(ks), _p(vs), on.raw), "rhtq_cache_append")
+        on.keep(ks, vs, kc if kc is not k else None, vc if vc is not v else None)
+    finally:
+        on.leave()
 
 
 def rhtq_cache_read(cache: RhtqCache, table, lengths, starts, tokens: int, k_signs=None, v_signs=None, dtype=torch.bfloat16,
@@ -240,20 +307,25 @@ def rhtq_cache_read(cache: RhtqCache, table, lengths, starts, tokens: int, k_sig
     for name, t in (("k_out", k_out), ("v_out", v_out)):
         if t is not None:
             _expect(t, name, dtype, shape)
-    dev = cache.k_codes.device
-    _same_device(dev, k_codes=cache.k_codes, k_scales=cache.k_scales, v_codes=cache.v_codes, v_scales=cache.v_scales, table=table,
-                 lengths=lengths, starts=starts, k_out=k_out, v_out=v_out)
-    with torch.cuda.device(dev):
-        ks, vs = _cache_signs(k_signs, c.head_dim, dev), _cache_signs(v_signs, c.head_dim, dev)
-        st, other = _resolve_stream(stream)
+    first = cache[0]
+    index = first.get_device()
+    _one_device(index, {"k_codes": first, "k_scales": cache[1], "v_codes": cache[2], "v_scales": cache[3], "table": table,
+                        "lengths": lengths, "starts": starts, "k_out": k_out, "v_out": v_out})
+    on = _On(index)
+    try:
+        ks, vs = _signs(k_signs, c.head_dim, first), _signs(v_signs, c.head_dim, first)
         own_k, own_v = k_out is None, v_out is None
         if own_k:
-            k_out = torch.empty(shape, dtype=dtype, device=dev)
+            k_out = first.new_empty(shape, dtype=dtype)
         if own_v:
-            v_out = torch.empty(shape, dtype=dtype, device=dev)
+            v_out = first.new_empty(shape, dtype=dtype)
+        if stream is not None:
+            on.follow(stream)
         _check(lib.rhtq_cache_read(ctypes.byref(c), k_out.data_ptr(), v_out.data_ptr(), _IN[dtype], tokens, table.data_ptr(), width,
-                                   lengths.data_ptr(), _p(starts), seqs, _p(ks), _p(vs), st.cuda_stream), "rhtq_cache_read")
-        _keep_for(st, other, ks, vs, k_out if own_k else None, v_out if own_v else None)
+                                   lengths.data_ptr(), _p(starts), seqs, _p(ks), _p(vs), on.raw), "rhtq_cache_read")
+        on.keep(ks, vs, k_out if own_k else None, v_out if own_v else None)
+    finally:
+        on.leave()
     return k_out, v_out
 
 
@@ -265,44 +337,51 @@ def rhtq_paged_attention(q, cache: RhtqCache, table, lengths, k_signs=None, v_si
     position gets zeros.  Returns [seqs][q_heads][head_dim] in q's type."""
     if q.dim() != 3:
         raise ValueError("q must be 3-D [seqs][q_heads][head_dim]")
-    if q.dtype not in (torch.bfloat16, torch.float16):
+    in_type = _IN.get(q.dtype, RHTQ_IN_F32)
+    if in_type == RHTQ_IN_F32:
         raise ValueError("q must be bfloat16 or float16")
     c, seqs, width = _rows_of(cache, table, lengths, None, q.shape[0])
     q_heads, dim = q.shape[1:]
-    if dim != c.head_dim or q_heads < 1 or q_heads % max(c.kv_heads, 1):
-        raise ValueError(f"q: {tuple(q.shape)} does not fit {c.kv_heads} key-value heads of {c.head_dim}")
+    kv_heads = c.kv_heads
+    if dim != c.head_dim or q_heads < 1 or q_heads % max(kv_heads, 1):
+        raise ValueError(f"q: {tuple(q.shape)} does not fit {kv_heads} key-value heads of {c.head_dim}")
     if window < 0 or sinks < 0:
         raise ValueError("window and sinks must not be negative")
     if out is not None:
         _expect(out, "out", q.dtype, q.shape)
-    dev = q.device
-    _same_device(dev, q=q, k_codes=cache.k_codes, k_scales=cache.k_scales, v_codes=cache.v_codes, v_scales=cache.v_scales, table=table,
-                 lengths=lengths, out=out)
-    with torch.cuda.device(dev):
-        ks, vs = _cache_signs(k_signs, dim, dev), _cache_signs(v_signs, dim, dev)
+    index = q.get_device()
+    _one_device(index, {"q": q, "k_codes": cache[0], "k_scales": cache[1], "v_codes": cache[2], "v_scales": cache[3], "table": table,
+                        "lengths": lengths, "out": out})
+    on = _On(index)
+    try:
+        ks, vs = _signs(k_signs, dim, q), _signs(v_signs, dim, q)
         qc = _row_strides(q)
-        st, other = _resolve_stream(stream)
         own = out is None
         if own:
-            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        need = lib.rhtq_paged_attention_workspace(seqs, q_heads, c.kv_heads, dim, width, c.page, window, sinks)
-        work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        _check(lib.rhtq_paged_attention(qc.data_ptr(), _IN[q.dtype], seqs, q_heads, qc.stride(0), qc.stride(1), ctypes.byref(c),
+            out = q.new_empty(q.shape)
+        need = lib.rhtq_paged_attention_workspace(seqs, q_heads, kv_heads, dim, width, c.page, window, sinks)
+        work = q.new_empty(need, dtype=_U8) if need else None
+        if stream is not None:
+            on.follow(stream)
+        _check(lib.rhtq_paged_attention(qc.data_ptr(), in_type, seqs, q_heads, qc.stride(0), qc.stride(1), ctypes.byref(c),
                                         table.data_ptr(), width, lengths.data_ptr(), _p(ks), _p(vs),
                                         1.0 / math.sqrt(dim) if scale is None else scale, window, sinks, out.data_ptr(), _p(work),
-                                        need, st.cuda_stream), "rhtq_paged_attention")
-        _keep_for(st, other, ks, vs, work, qc if qc is not q else None, out if own else None)
+                                        need, on.raw), "rhtq_paged_attention")
+        on.keep(ks, vs, work, qc if qc is not q else None, out if own else None)
+    finally:
+        on.leave()
     return out
 
 
 def _paging(table, lengths, refs):
     if table.dim() != 2 or refs.dim() != 1:
         raise ValueError("table must be 2-D [seqs][width] and refs 1-D [pages]")
-    _int32(table, "table", table.shape)
+    shape = table.shape
+    _int32(table, "table", shape)
     if lengths is not None:
-        _int32(lengths, "lengths", (table.shape[0],))
+        _int32(lengths, "lengths", shape[:1])
     _int32(refs, "refs", refs.shape)
-    return table.shape
+    return shape
 
 
 def _paged_cache(cache, refs):
@@ -312,16 +391,35 @@ def _paged_cache(cache, refs):
     return c
 
 
-def _index_list(t, name, count=None):
+def _index_list(t, name, shape=None):
     if t.dim() != 1:
         raise ValueError(f"{name} must be 1-D")
-    _int32(t, name, t.shape if count is None else (count,))
+    _int32(t, name, t.shape if shape is None else shape)
     return t.shape[0]
 
 
-def _work_for(pages, seqs, count, dev):
-    need = lib.rhtq_pages_workspace(pages, seqs, count)
-    return torch.empty(need, dtype=torch.uint8, device=dev), need
+def _page_call(name, named, stream, call, pages=None, seqs=0, count=0, word=False):
+    """call(raw stream, word, workspace, its size) on the tensors' device: with `pages`, a workspace of the page calls; with `word`, the
+    device int32 [1] that comes back."""
+    first = next(iter(named.values()))
+    index = first.get_device()
+    _one_device(index, named)
+    on = _On(index)
+    try:
+        told = first.new_empty(1, dtype=_I32) if word else None
+        need = 0 if pages is None else lib.rhtq_pages_workspace(pages, seqs, count)
+        work = first.new_empty(need, dtype=_U8) if need else None
+        if stream is not None:
+            on.follow(stream)
+        _check(call(on.raw, _p(told), _p(work), need), name)
+        on.keep(told, work)
+    finally:
+        on.leave()
+    return told
+
+
+def _tensors(cache):
+    return {"k_codes": cache[0], "k_scales": cache[1], "v_codes": cache[2], "v_scales": cache[3]}
 
 
 def rhtq_pages_reserve(table, lengths, refs, add, page: int, stream=None):
@@ -329,40 +427,29 @@ def rhtq_pages_reserve(table, lengths, refs, add, page: int, stream=None):
     free ones (refs int32 [pages] == 0) are taken.  All or nothing; returns a device int32 [1]: 0 done, otherwise the number of
     pages missing, or -1 for a negative amount."""
     seqs, width = _paging(table, lengths, refs)
-    _int32(add, "add", (seqs,))
-    dev = table.device
-    _same_device(dev, table=table, lengths=lengths, refs=refs, add=add)
-    with torch.cuda.device(dev):
-        st, other = _resolve_stream(stream)
-        status = torch.empty(1, dtype=torch.int32, device=dev)
-        work, need = _work_for(refs.shape[0], seqs, 0, dev)
-        _check(lib.rhtq_pages_reserve(table.data_ptr(), width, lengths.data_ptr(), seqs, refs.data_ptr(), refs.shape[0], page,
-                                      add.data_ptr(), status.data_ptr(), work.data_ptr(), need, st.cuda_stream), "rhtq_pages_reserve")
-        _keep_for(st, other, status, work)
-    return status
+    _int32(add, "add", lengths.shape)
+    pages = refs.shape[0]
+    return _page_call("rhtq_pages_reserve", {"table": table, "lengths": lengths, "refs": refs, "add": add}, stream,
+                      lambda raw, word, work, size: lib.rhtq_pages_reserve(table.data_ptr(), width, lengths.data_ptr(), seqs, refs.data_ptr(),
+                                                                           pages, page, add.data_ptr(), word, work, size, raw),
+                      pages, seqs, 0, True)
 
 
 def rhtq_pages_free(table, lengths, refs, seqs, stream=None):
     """Give up every page of the listed sequences (int32 [count]) and set their lengths to 0."""
     all_seqs, width = _paging(table, lengths, refs)
     count = _index_list(seqs, "seqs")
-    dev = table.device
-    _same_device(dev, table=table, lengths=lengths, refs=refs, seqs=seqs)
-    with torch.cuda.device(dev):
-        st, _ = _resolve_stream(stream)
-        _check(lib.rhtq_pages_free(table.data_ptr(), width, lengths.data_ptr(), all_seqs, refs.data_ptr(), refs.shape[0], seqs.data_ptr(),
-                                   count, st.cuda_stream), "rhtq_pages_free")
+    _page_call("rhtq_pages_free", {"table": table, "lengths": lengths, "refs": refs, "seqs": seqs}, stream,
+               lambda raw, word, work, size: lib.rhtq_pages_free(table.data_ptr(), width, lengths.data_ptr(), all_seqs, refs.data_ptr(),
+                                                                 refs.shape[0], seqs.data_ptr(), count, raw))
 
 
 def rhtq_pages_trim(table, lengths, refs, page: int, window: int, sinks: int = 0, stream=None):
     """Give up the pages that attention with this window and these first positions can never see again."""
     seqs, width = _paging(table, lengths, refs)
-    dev = table.device
-    _same_device(dev, table=table, lengths=lengths, refs=refs)
-    with torch.cuda.device(dev):
-        st, _ = _resolve_stream(stream)
-        _check(lib.rhtq_pages_trim(table.data_ptr(), width, lengths.data_ptr(), seqs, refs.data_ptr(), refs.shape[0], page, window,
-                                   sinks, st.cuda_stream), "rhtq_pages_trim")
+    _page_call("rhtq_pages_trim", {"table": table, "lengths": lengths, "refs": refs}, stream,
+               lambda raw, word, work, size: lib.rhtq_pages_trim(table.data_ptr(), width, lengths.data_ptr(), seqs, refs.data_ptr(),
+                                                                 refs.shape[0], page, window, sinks, raw))
 
 
 def rhtq_pages_fork(cache: RhtqCache, table, lengths, refs, src, dst, stream=None):
@@ -371,44 +458,28 @@ def rhtq_pages_fork(cache: RhtqCache, table, lengths, refs, src, dst, stream=Non
     c = _paged_cache(cache, refs)
     seqs, width = _paging(table, lengths, refs)
     count = _index_list(src, "src")
-    _index_list(dst, "dst", count)
-    dev = table.device
-    _same_device(dev, table=table, lengths=lengths, refs=refs, src=src, dst=dst, k_codes=cache.k_codes, k_scales=cache.k_scales,
-                 v_codes=cache.v_codes, v_scales=cache.v_scales)
-    with torch.cuda.device(dev):
-        st, other = _resolve_stream(stream)
-        status = torch.empty(1, dtype=torch.int32, device=dev)
-        work, need = _work_for(refs.shape[0], seqs, count, dev)
-        _check(lib.rhtq_pages_fork(ctypes.byref(c), table.data_ptr(), width, lengths.data_ptr(), seqs, refs.data_ptr(), src.data_ptr(),
-                                   dst.data_ptr(), count, status.data_ptr(), work.data_ptr(), need, st.cuda_stream), "rhtq_pages_fork")
-        _keep_for(st, other, status, work)
-    return status
+    _index_list(dst, "dst", src.shape)
+    return _page_call("rhtq_pages_fork", {"table": table, "lengths": lengths, "refs": refs, "src": src, "dst": dst, **_tensors(cache)}, stream,
+                      lambda raw, word, work, size: lib.rhtq_pages_fork(ctypes.byref(c), table.data_ptr(), width, lengths.data_ptr(), seqs,
+                                                                        refs.data_ptr(), src.data_ptr(), dst.data_ptr(), count, word, work,
+                                                                        size, raw),
+                      refs.shape[0], seqs, count, True)
 
 
 def rhtq_pages_copy(cache: RhtqCache, src, dst, stream=None):
     """Copy whole pages src[i] -> dst[i] (int32 [count]) in every layer; a page may be written once and not read by the same call."""
     c = _cache_struct(cache, True)
     count = _index_list(src, "src")
-    _index_list(dst, "dst", count)
-    dev = cache.k_codes.device
-    _same_device(dev, src=src, dst=dst, k_codes=cache.k_codes, k_scales=cache.k_scales, v_codes=cache.v_codes, v_scales=cache.v_scales)
-    with torch.cuda.device(dev):
-        st, _ = _resolve_stream(stream)
-        _check(lib.rhtq_pages_copy(ctypes.byref(c), src.data_ptr(), dst.data_ptr(), count, st.cuda_stream), "rhtq_pages_copy")
+    _index_list(dst, "dst", src.shape)
+    _page_call("rhtq_pages_copy", {**_tensors(cache), "src": src, "dst": dst}, stream,
+               lambda raw, word, work, size: lib.rhtq_pages_copy(ctypes.byref(c), src.data_ptr(), dst.data_ptr(), count, raw))
 
 
 def rhtq_pages_compact(cache: RhtqCache, table, refs, stream=None):
     """Move live pages into lower free ones until they fill [0, live); table and refs follow.  Returns live, a device int32 [1]."""
     c = _paged_cache(cache, refs)
     seqs, width = _paging(table, None, refs)
-    dev = table.device
-    _same_device(dev, table=table, refs=refs, k_codes=cache.k_codes, k_scales=cache.k_scales, v_codes=cache.v_codes,
-                 v_scales=cache.v_scales)
-    with torch.cuda.device(dev):
-        st, other = _resolve_stream(stream)
-        live = torch.empty(1, dtype=torch.int32, device=dev)
-        work, need = _work_for(refs.shape[0], seqs, 0, dev)
-        _check(lib.rhtq_pages_compact(ctypes.byref(c), table.data_ptr(), width, seqs, refs.data_ptr(), live.data_ptr(), work.data_ptr(),
-                                      need, st.cuda_stream), "rhtq_pages_compact")
-        _keep_for(st, other, live, work)
-    return live
+    return _page_call("rhtq_pages_compact", {"table": table, "refs": refs, **_tensors(cache)}, stream,
+                      lambda raw, word, work, size: lib.rhtq_pages_compact(ctypes.byref(c), table.data_ptr(), width, seqs, refs.data_ptr(), word,
+                                                                           work, size, raw),
+                      refs.shape[0], seqs, 0, True)
