@@ -24,13 +24,13 @@
 namespace rhtq {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
+constexpr int kWaves = 8;
+constexpr int kJoinWaves = 4;           // heads of a join's workgroup
 constexpr int kHeads = 8;               // query heads of a tile
 constexpr int kChunk = 4;               // tiles that a wave takes at once: 64 positions, the depth of one product
-constexpr int kLeastTiles = kWaves * kChunk;   // tiles of a part worth a workgroup
-constexpr int kMostTiles = 512;          // and at most: 8192 positions
-constexpr int kResident = 768;
+constexpr int kLeastTiles = kWaves * kChunk;   // tiles of a part worth a workgroup: 512 positions
+constexpr int kMostTiles = 320;         // and at most, where the whole is enough for the chip: 5120 positions
+constexpr int kEnough = 256;            // workgroups that fill the chip: one of 8 waves on each CU
 constexpr float kNone = -INFINITY;
 constexpr float kTiny = 7.7037197775489434e-34f;   // 2^-110
 constexpr float kLargest = 32639.0f;    // 127 * 256 + 127: the largest two-byte value
@@ -42,7 +42,7 @@ template <int T, int E>
 __device__ __forceinline__ void finish(const AttentionArgs& a, int64_t row, float l, float (&o)[E]) {
   const int j = threadIdx.x & 15;
   const float cnorm = E == 4 ? 0.125f : (E == 8 ? 0.088388347648318447f : 0.0625f);
-  const float f = l > 0.0f ? cnorm / l : 0.0f;
+  const float f = l > 0.0f ? cnorm * __builtin_amdgcn_rcpf(l) : 0.0f;
   fwht16<E>(o);
 #pragma unroll
   for (int i = 0; i < E; ++i) o[i] *= f;
@@ -68,13 +68,13 @@ struct Place {
   int page[kChunk];
 };
 
-// `first` is the same in all lanes, so the table's entries come by scalar loads, which no wait for the codes holds up.  end > first.
+// `first` is the same in all lanes, so the table's entries come by scalar loads, which no wait for the codes holds up.
 __device__ __forceinline__ void locate(const AttentionArgs& a, const Visible& vis, const int32_t* table, int first, int end, Place& c) {
   int entry[kChunk], at[kChunk];
 #pragma unroll
   for (int t = 0; t < kChunk; ++t) {
-    at[t] = tile_at(vis, first + t < end ? first + t : end - 1) * kTile;   // below the table's end, as every visible position
-    entry[t] = table[at[t] >> a.page_log];
+    at[t] = first + t < end ? tile_at(vis, first + t) * kTile : 0;   // in the table, whose width is at least 1
+    entry[t] = load_uniform(table + (at[t] >> a.page_log));
   }
 #pragma unroll
   for (int t = 0; t < kChunk; ++t) {
@@ -174,7 +174,7 @@ __device__ __forceinline__ int operand_byte(int d) {
 // One workgroup: a part of one sequence's positions for up to 8 query heads of one key-value head; its waves take the chunks
 // in turn.
 template <int T, int E, bool F32>
-__global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(64 * kWaves, E == 16 || F32 ? 2 : 4) void attention_kernel(AttentionArgs a) {
   constexpr int D = 16 * E;
   constexpr int NK = D / 64;              // products of a score
   constexpr int H = D >= 128 ? D / 128 : 1;
@@ -188,7 +188,14 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
   const int split = blockIdx.x, s = blockIdx.z;
   const int kv = blockIdx.y / a.head_tiles, head0 = (blockIdx.y - kv * a.head_tiles) * kHeads;
   const int heads = a.each - head0 < kHeads ? a.each - head0 : kHeads;
-  const Visible vis = visible_of(a.lengths[s], a.width, 1 << a.page_log, a.window, a.sinks);
+  // loads in the order of their use: q's rotation then runs while the first chunk's codes are on their way
+  const int length = load_uniform(a.lengths + s);
+  uint32_t signs[E / 4];
+  float x0[E] = {};
+  load_signs<E>(a.k_signs, j * E, signs);
+  const int from = group < heads ? group : heads - 1;
+  load_row<T, E>(a.q, s * a.q_seq_stride + (kv * a.each + head0 + from) * a.q_head_stride + j * E, x0);
+  const Visible vis = visible_of(length, a.width, 1 << a.page_log, a.window, a.sinks);
   const int per = tiles_per_split(vis.tiles, a.splits, kLeastTiles);
   const int t0 = split * per, t1 = t0 + per < vis.tiles ? t0 + per : vis.tiles;
   const int32_t* table = a.table + (int64_t)s * a.width;
@@ -197,29 +204,23 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
   int at = t0 + wave * kChunk;
   Place next;
   Loaded<D, F32> c;
-  if (a.pages == 0) at = t1;              // no page can be named
-  if (at < t1) {
-    locate(a, vis, table, at, t1, next);
-    load_keys<D, F32>(a, kv, next, c);
-    load_values<D, F32>(a, kv, next, c);
-  }
+  // a wave without a chunk loads too (page 0): the number of loads before the first wait is then known
+  locate(a, vis, table, at, t1, next);
+  load_keys<D, F32>(a, kv, next, c);
+  load_values<D, F32>(a, kv, next, c);
 
   // q: 16 lanes rotate a head and leave its bytes as operand rows h (hi) and 8 + h (lo)
   if (group < kHeads) {
-    float q[E] = {};
-    if (group < heads) {
-      load_row<T, E>(a.q, s * a.q_seq_stride + (kv * a.each + head0 + group) * a.q_head_stride + j * E, q);
-      apply_signs<E>(a.k_signs, j * E, q);
-      fwht16<E>(q);
-    }
+    apply_signs<E>(signs, x0);
+    fwht16<E>(x0);
     float amax = 0.0f;
 #pragma unroll
-    for (int i = 0; i < E; ++i) amax = fmaxf(amax, __builtin_fabsf(q[i]));
+    for (int i = 0; i < E; ++i) amax = fmaxf(amax, __builtin_fabsf(x0[i]));
     amax = max16(amax);
-    const float inv = amax > 0.0f ? kLargest / amax : 0.0f;
+    const float inv = amax > kTiny ? kLargest * __builtin_amdgcn_rcpf(amax) : 0.0f;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const int v = (int)__builtin_rintf(q[i] * inv);
+      const int v = (int)__builtin_rintf(x0[i] * inv);
       sq[group][operand_byte<D>(j * E + i)] = (uint8_t)((v + 128) >> 8);
       sq[8 + group][operand_byte<D>(j * E + i)] = (uint8_t)v;
     }
@@ -408,10 +409,10 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
 // One wave per query head: lane k of a stretch of 64 parts has that part's factor, and the wave's four groups of 16 lanes take the
 // parts' sums in turn.
 template <int T, int E>
-__global__ __launch_bounds__(kThreads) void join_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(AttentionArgs a) {
   constexpr int D = 16 * E;
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
-  const int64_t row = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+  const int64_t row = (int64_t)blockIdx.x * kJoinWaves + (threadIdx.x >> 6);
   if (row >= (int64_t)a.seqs * a.q_heads) return;
   const float* ml = a.partial + (int64_t)a.seqs * a.q_heads * a.splits * D + 2 * row * a.splits;
   const float* part = a.partial + row * a.splits * D;
@@ -453,12 +454,18 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttentionArgs a) {
 template <int T, int E>
 hipError_t launch_te(const AttentionArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)a.splits, (unsigned)(a.kv_heads * a.head_tiles), (unsigned)a.seqs);
-  if (a.scale_dtype == RHTQ_SCALE_F32) hipLaunchKernelGGL((attention_kernel<T, E, true>), grid, dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL((attention_kernel<T, E, false>), grid, dim3(kThreads), 0, s, a);
+  if (a.scale_dtype == RHTQ_SCALE_F32) hipLaunchKernelGGL((attention_kernel<T, E, true>), grid, dim3(64 * kWaves), 0, s, a);
+  else hipLaunchKernelGGL((attention_kernel<T, E, false>), grid, dim3(64 * kWaves), 0, s, a);
   const int64_t rows = (int64_t)a.seqs * a.q_heads;
   if (a.splits > 1)
-    hipLaunchKernelGGL((join_kernel<T, E>), dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((join_kernel<T, E>), dim3((unsigned)((rows + kJoinWaves - 1) / kJoinWaves)), dim3(64 * kJoinWaves), 0, s, a);
   return hipGetLastError();
+}
+
+// No page at all: no position is visible.
+__global__ __launch_bounds__(256) void zero_kernel(uint32_t* out, int64_t words) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < words) out[i] = 0;
 }
 
 template <int T>
@@ -482,17 +489,23 @@ int32_t attention_splits(int32_t seqs, int32_t q_heads, int32_t kv_heads, int32_
     if (most < tiles) tiles = most;
   }
   const int64_t rows = (int64_t)seqs * kv_heads * attention_head_tiles(q_heads / kv_heads);
-  // parts that fill the chip's 768 resident workgroups, and of no more than 8192 positions, so that a long sequence beside short
-  // ones does not end alone; at least 256 positions, one chunk a wave
-  int64_t want = rows > 0 ? (kResident + rows - 1) / rows : 1;
+  // Enough parts for a workgroup on every CU, and none so long that it would end alone beside shorter sequences.  More cost their
+  // start (about 3 us of latency each) and the join: 32 x 8 heads x 4096 positions 29.5 us whole, 32.9 in two parts; one
+  // sequence of 131072 32.8 us in 32 parts, 37.0 in 128; 24 x 8 heads of 1 .. 16384 44 us in two, 35 in four, 33 in eight.
+  int64_t want = rows > 0 ? (kEnough + rows - 1) / rows : 1;
   if (want < (tiles + kMostTiles - 1) / kMostTiles) want = (tiles + kMostTiles - 1) / kMostTiles;
-  const int64_t most = (tiles + kLeastTiles - 1) / kLeastTiles;
+  const int64_t most = (tiles + kLeastTiles / 2) / kLeastTiles;
   if (want > most) want = most;
   if (want > 1024) want = 1024;
   return want < 1 ? 1 : (int32_t)want;
 }
 
 hipError_t launch_paged_attention(int dtype, const AttentionArgs& a, hipStream_t s) {
+  if (a.pages == 0 || a.width == 0) {
+    const int64_t words = (int64_t)a.seqs * a.q_heads * a.head_dim / 2;
+    hipLaunchKernelGGL(zero_kernel, dim3((unsigned)((words + 255) / 256)), dim3(256), 0, s, static_cast<uint32_t*>(a.out), words);
+    return hipGetLastError();
+  }
   if (dtype == RHTQ_IN_BF16) return launch_t<RHTQ_IN_BF16>(a, s);
   return launch_t<RHTQ_IN_F16>(a, s);
 }

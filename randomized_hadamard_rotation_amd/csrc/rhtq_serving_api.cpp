@@ -45,7 +45,7 @@ int cache_rows(const rhtq_cache_t* c, int64_t tokens, const int32_t* table, int3
   if (st == RHTQ_OK) st = check_table(width, seqs, c->page);
   if (st != RHTQ_OK) return st;
   if (tokens < 0 || tokens > INT32_MAX || (!starts && tokens != seqs) || c->layers != 1) return RHTQ_EINVAL;
-  if (2 * tokens * c->kv_heads / 16 >= INT32_MAX) return RHTQ_EINVAL;
+  if (c->kv_heads > 65535) return RHTQ_EUNSUPPORTED;   // a grid's limit
   if (tokens == 0) return RHTQ_OK;
   if (!cache_pointers(c, scale_size(c->scale_dtype)) || !table || !lengths) return RHTQ_EINVAL;
   if (!aligned(table, 4) || !aligned(lengths, 4) || !aligned(starts, 4) || !aligned(k_signs, 4) || !aligned(v_signs, 4))

@@ -47,12 +47,10 @@ __device__ __forceinline__ int sum16(int v) {
 
 template <int B, int E>
 __device__ __forceinline__ void lane_stage16(float (&v)[E]) {
-  const bool up = (threadIdx.x >> B) & 1;
+  // o + v in the lower lane, o - v in the upper: one fma with +-1, rounded as the sum is
+  const float sign = (threadIdx.x >> B) & 1 ? -1.0f : 1.0f;
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const float o = lane_xor16<B>(v[i]);
-    v[i] = up ? o - v[i] : o + v[i];
-  }
+  for (int i = 0; i < E; ++i) v[i] = __builtin_fmaf(v[i], sign, lane_xor16<B>(v[i]));
 }
 
 // Walsh-Hadamard transform (Sylvester order, no factor) of a row of 16 E elements held by 16 lanes, lane j with elements
@@ -137,17 +135,32 @@ __device__ __forceinline__ void store_row(void* p, int64_t at, const float (&v)[
   }
 }
 
-// x *= +-1 by the sign bytes of elements at .. at + E - 1 (null: all +1)
+// Sign bytes of elements at .. at + E - 1 (null: all +1), and x *= +-1 by them.
+template <int E>
+__device__ __forceinline__ void load_signs(const int8_t* s, int at, uint32_t (&w)[E / 4]) {
+#pragma unroll
+  for (int i = 0; i < E / 4; ++i) w[i] = 0;
+  if (s)
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) w[i] = *reinterpret_cast<const uint32_t*>(s + at + 4 * i);
+}
+template <int E>
+__device__ __forceinline__ void apply_signs(const uint32_t (&w)[E / 4], float (&v)[E]) {
+#pragma unroll
+  for (int i = 0; i < E; ++i)
+    v[i] = __uint_as_float(__float_as_uint(v[i]) ^ ((w[i / 4] << (24 - 8 * (i % 4))) & 0x80000000u));
+}
 template <int E>
 __device__ __forceinline__ void apply_signs(const int8_t* s, int at, float (&v)[E]) {
-  if (!s) return;
-#pragma unroll
-  for (int i = 0; i < E; i += 4) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(s + at + i);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      v[i + j] = __uint_as_float(__float_as_uint(v[i + j]) ^ (((w >> (8 * j + 7)) & 1u) << 31));
-  }
+  uint32_t w[E / 4];
+  load_signs<E>(s, at, w);
+  apply_signs<E>(w, v);
+}
+
+// A value that the kernel does not write, at an address that is the same in all lanes, by a scalar load: what waits for vector loads
+// does not wait for it, nor the other way round.
+__device__ __forceinline__ int32_t load_uniform(const int32_t* p) {
+  return *reinterpret_cast<const __attribute__((address_space(4))) int32_t*>(reinterpret_cast<uintptr_t>(p));
 }
 
 __device__ __forceinline__ float load_scale(const void* p, int64_t at, int dtype) {
