@@ -45,50 +45,80 @@ __host__ __device__ constexpr int value_of(int j) {
 
 constexpr int kPrep = 1024;
 
-// One workgroup per token of a tile; tokens beyond the last (and k beyond n) become zeros.
+// x in [-1, 1] as its two halves.
+__device__ __forceinline__ void split_halves(float x, _Float16& hi, _Float16& lo) {
+  hi = (_Float16)x;
+  lo = (_Float16)((x - (float)hi) * 2048.0f);
+}
+
+// Largest of a workgroup's values, in every thread.
+template <int WAVES>
+__device__ __forceinline__ float workgroup_max(float v, float* wave_max) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
+  if ((threadIdx.x & 63) == 0) wave_max[threadIdx.x >> 6] = v;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < WAVES; ++i) v = fmaxf(v, wave_max[i]);
+  return v;
+}
+
+// One workgroup per token of a tile; tokens beyond the last (and k beyond n) become zeros.  Rows of up to 16384 stay in registers between
+// the search for the largest value and the split.
 template <int MODE, int TX>
 __global__ __launch_bounds__(kPrep) void prepare_kernel(MatvecArgs a) {
   __shared__ float wave_max[kPrep / 64];
+  constexpr int HELD = 2;
   const int64_t t = blockIdx.x;
   const int64_t tile = t >> 3;
   const int steps = (a.n + kStep - 1) / kStep;
   const bool real = t < a.tokens;
-  // 8 values a thread: dword d of step s
-  float v[8];
+  float v[HELD][8];
   float top = 0.0f;
-  const int dwords = a.n / 8;
-  for (int u = threadIdx.x; real && u < dwords; u += kPrep) {
-    load_row<TX, 8>(a.x, t * a.n + 8 * u, v);
+  // item u: operand i of step s, lane group q -- a dword of 8 values of k; every dword of the row is one item
+  auto k_of = [&](int u) { return kStep * (u >> 4) + 8 * dword_of<MODE>((u >> 2) & 3, u & 3); };
 #pragma unroll
-    for (int j = 0; j < 8; ++j) top = fmaxf(top, __builtin_fabsf(v[j]));
+  for (int h = 0; h < HELD; ++h) {
+    const int u = threadIdx.x + h * kPrep, k = k_of(u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[h][j] = 0.0f;
+    if (real && k < a.n) load_row<TX, 8>(a.x, t * a.n + k, v[h]);
   }
 #pragma unroll
-  for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-  if ((threadIdx.x & 63) == 0) wave_max[threadIdx.x >> 6] = top;
-  __syncthreads();
+  for (int h = 0; h < HELD; ++h)
 #pragma unroll
-  for (int i = 0; i < kPrep / 64; ++i) top = fmaxf(top, wave_max[i]);
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, __builtin_fabsf(v[h][j]));
+  for (int u = threadIdx.x + HELD * kPrep; u < steps * 16; u += kPrep) {
+    float w[8] = {};
+    if (real && k_of(u) < a.n) load_row<TX, 8>(a.x, t * a.n + k_of(u), w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, __builtin_fabsf(w[j]));
+  }
+  top = workgroup_max<kPrep / 64>(top, wave_max);
   const int e = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) : 0;
   if (threadIdx.x == 0) a.exponents[t] = e;
-  const int a4 = (int)(t & 7) >> 1, b = (int)(t & 1);
-  const int m_hi = 4 * a4 + b, m_lo = m_hi + 2;
+  const int m_hi = 4 * ((int)(t & 7) >> 1) + (int)(t & 1), m_lo = m_hi + 2;
   uint8_t* out = static_cast<uint8_t*>(a.halves) + tile * steps * 4 * kFrag;
-  for (int u = threadIdx.x; u < steps * 16; u += kPrep) {
-    const int s = u >> 4, i = (u >> 2) & 3, q = u & 3;      // operand i of step s, lane group q
-    const int k = kStep * s + 8 * dword_of<MODE>(i, q);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-    if (real && k < a.n) load_row<TX, 8>(a.x, t * a.n + k, v);
+  auto put = [&](int u, const float (&w)[8]) {
     f16x8 hi, lo;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float x = __builtin_amdgcn_ldexpf(v[value_of<MODE>(j)], -e);
-      hi[j] = (_Float16)x;
-      lo[j] = (_Float16)((x - (float)hi[j]) * 2048.0f);
+      _Float16 h, l;
+      split_halves(__builtin_amdgcn_ldexpf(w[value_of<MODE>(j)], -e), h, l);
+      hi[j] = h;
+      lo[j] = l;
     }
-    uint8_t* o = out + (int64_t)(4 * s + i) * kFrag + 256 * q;
+    uint8_t* o = out + (int64_t)(u >> 2) * kFrag + 256 * (u & 3);
     *reinterpret_cast<f16x8*>(o + 16 * m_hi) = hi;
     *reinterpret_cast<f16x8*>(o + 16 * m_lo) = lo;
+  };
+#pragma unroll
+  for (int h = 0; h < HELD; ++h)
+    if ((int)threadIdx.x + h * kPrep < steps * 16) put(threadIdx.x + h * kPrep, v[h]);
+  for (int u = threadIdx.x + HELD * kPrep; u < steps * 16; u += kPrep) {
+    float w[8] = {};
+    if (real && k_of(u) < a.n) load_row<TX, 8>(a.x, t * a.n + k_of(u), w);
+    put(u, w);
   }
 }
 
@@ -97,52 +127,74 @@ __global__ __launch_bounds__(kPrep) void prepare_kernel(MatvecArgs a) {
 // Codes of a lane's row, and what scales them.
 struct Codes {
   uint32_t w[4];       // product i's dword
-  float s[8];          // M128: [0]; M64: [0..1]; M32: [0..3]; M16: [0..7]; MMX: [0] the step's power of two, [1] the lane's
+  float s[8];          // convert_scales'
   uint32_t e;          // MNV: two E4M3 bytes
+  uint32_t b[8];       // the scales as they lie: MMX the step's four E8M0 bytes, INT4 fp32 or fp16
 };
 
-template <int MODE>
+// Every load is made, of a place within the row where the row ends inside the step: x is 0 there, and codes and scales are finite.  With a
+// branch around a load, a later wait would not know how many are in flight and would wait for all.
+template <int MODE, bool F32>
 __device__ __forceinline__ void load_codes(const MatvecArgs& a, int64_t row, int step, int q, Codes& c) {
-  const int left = (a.n - kStep * step) / 8;          // dwords of the row from this step on
+  const int last = a.n / 8 - 16 * step - 1;           // the row's last dword, counted from this step on
   const uint32_t* p = reinterpret_cast<const uint32_t*>(a.packed) + row * (a.n / 8) + 16 * step;
   if constexpr (MODE == M128 || MODE == MNV || MODE == MMX) {
-    u32x4 t = {0, 0, 0, 0};
-    if (4 * q < left) t = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + 4 * q));
+    const int at = 4 * q < last ? 4 * q : last - 3;   // n is a multiple of 32: four dwords at least
+    const u32x4 t = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + at));
     c.w[0] = t.x; c.w[1] = t.y; c.w[2] = t.z; c.w[3] = t.w;
   } else if constexpr (MODE == M64) {
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      u32x2 t = {0, 0};
-      if (8 * g + 2 * q < left) t = *reinterpret_cast<const u32x2*>(p + 8 * g + 2 * q);
+      const int at = 8 * g + 2 * q < last ? 8 * g + 2 * q : last - 1;
+      const u32x2 t = *reinterpret_cast<const u32x2*>(p + at);
       c.w[2 * g] = t.x;
       c.w[2 * g + 1] = t.y;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c.w[i] = 4 * i + q < left ? p[4 * i + q] : 0u;
+    for (int i = 0; i < 4; ++i) c.w[i] = p[4 * i + q < last ? 4 * i + q : last];
   }
+  const int64_t scales = row * a.groups;
+  auto scale_at = [&](int64_t at) {
+    if constexpr (F32) return static_cast<const uint32_t*>(a.scales)[at];
+    else return (uint32_t) static_cast<const uint16_t*>(a.scales)[at];
+  };
   if constexpr (MODE == M128) {
-    c.s[0] = load_scale(a.scales, row * a.groups + (a.group_log < 0 ? 0 : (kStep * step) >> a.group_log), a.scale_dtype);
+    c.b[0] = scale_at(scales + (a.group_log < 0 ? 0 : (kStep * step) >> a.group_log));
   } else if constexpr (MODE == M64 || MODE == M32 || MODE == M16) {
     constexpr int PER = MODE == M64 ? 2 : (MODE == M32 ? 4 : 8);
 #pragma unroll
-    for (int g = 0; g < PER; ++g)
-      c.s[g] = PER * step + g < a.groups ? load_scale(a.scales, row * a.groups + PER * step + g, a.scale_dtype) : 0.0f;
+    for (int g = 0; g < PER; ++g) {
+      const int at = PER * step + g;
+      c.b[g] = scale_at(scales + (at < a.groups ? at : a.groups - 1));
+    }
   } else if constexpr (MODE == MNV) {
-    c.e = 0;
-    if (4 * q < left) c.e = *reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(a.scales) + row * a.groups + 8 * step + 2 * q);
+    const int at = 4 * q < last ? 2 * q : (last - 3) / 2;
+    c.e = *reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(a.scales) + scales + 8 * step + at);
   } else {
-    const uint8_t* s = static_cast<const uint8_t*>(a.scales) + row * a.groups + 4 * step;
-    uint32_t own = 0, top = 0;
+    const uint8_t* s = static_cast<const uint8_t*>(a.scales) + scales + 4 * step;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) c.b[g] = s[4 * g < last ? g : (last - 3) / 4];
+  }
+}
+
+// The scales as fp32, once they are needed.  MXFP4's powers of two: the step's largest 2^(top - 127), and the lane's block relative to it,
+// 2^(own - top), kept above 2^-126 (a block so far below another adds nothing).
+template <int MODE, bool F32>
+__device__ __forceinline__ void convert_scales(Codes& c, int q) {
+  if constexpr (MODE == MMX) {
+    uint32_t top = 0, own = c.b[0];
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      const uint32_t b = 4 * g < left ? s[g] : 0u;
-      top = b > top ? b : top;
-      own = g == q ? b : own;
+      top = c.b[g] > top ? c.b[g] : top;
+      own = g == q ? c.b[g] : own;
     }
-    // 2^(top - 127), and 2^(own - top) kept above 2^-126: a block so far below another adds nothing
     c.s[0] = __builtin_amdgcn_ldexpf(1.0f, (int)top - 127);
     c.s[1] = __builtin_amdgcn_ldexpf(1.0f, own + 126 > top ? (int)own - (int)top : -126);
+  } else if constexpr (MODE != MNV) {
+    constexpr int PER = MODE == M128 ? 1 : (MODE == M64 ? 2 : (MODE == M32 ? 4 : 8));
+#pragma unroll
+    for (int g = 0; g < PER; ++g) c.s[g] = F32 ? __uint_as_float(c.b[g]) : __half2float(__ushort_as_half((uint16_t)c.b[g]));
   }
 }
 
@@ -233,48 +285,111 @@ __device__ __forceinline__ void store_y(const MatvecArgs& a, int64_t t, int64_t 
 }
 
 // Both halves of a token, times its power of two and the tensor scale.
-__device__ __forceinline__ float whole(const MatvecArgs& a, int64_t t, float hi, float lo) {
-  const float v = __builtin_amdgcn_ldexpf(__builtin_fmaf(lo, 1.0f / 2048.0f, hi), a.exponents[t]);
+__device__ __forceinline__ float whole(const MatvecArgs& a, int exponent, float hi, float lo) {
+  const float v = __builtin_amdgcn_ldexpf(__builtin_fmaf(lo, 1.0f / 2048.0f, hi), exponent);
   return a.tensor_scale ? v * a.tensor_scale[0] : v;
 }
 
 // ---- few tokens: one tile of 16 rows per workgroup, k split over its waves -----------------------------------------------------
 
 constexpr int kWaves = 8;
-constexpr int kAhead = 4;          // steps whose codes are in flight
+constexpr int kAhead = 4;          // steps whose codes and operands are in flight
+constexpr int kOwnTokens = 2;      // tokens that a workgroup splits into halves itself
+constexpr int kOwnWidth = 4096;    // and widths, as LDS holds them,
+constexpr int kOwnRows = 8192;     // and rows: beyond, one launch that does it once costs less
 
-template <int MODE>
+// OWN: x fp32 is split by every workgroup for itself, in LDS, while its codes are on their way, which saves a launch; otherwise the halves
+// lie ready.
+template <int MODE, bool F32, bool OWN>
 __global__ __launch_bounds__(64 * kWaves) void narrow_kernel(MatvecArgs a) {
   __shared__ f32x4 part[kWaves][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ float wave_max[kOwnTokens][kWaves];
+  // operands of two tokens: rows t + 2 half of lane group q of operand i
+  __shared__ __attribute__((aligned(16))) f16x8 own[OWN ? kOwnWidth / 8 : 1][4];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, q = lane >> 4;
-  const int64_t tile = blockIdx.y;
   const int64_t row0 = (int64_t)blockIdx.x * 16;
   const int64_t row = row0 + m < a.rows ? row0 + m : a.rows - 1;
   const int steps = (a.n + kStep - 1) / kStep;
   const int s0 = steps * wave / kWaves, s1 = steps * (wave + 1) / kWaves;
-  const int left = (int)(a.tokens - 8 * tile);                    // tokens of this tile that there are
-  const bool mine = 2 * (m >> 2) + (m & 1) < left;
-  const uint8_t* x = static_cast<const uint8_t*>(a.halves) + tile * steps * 4 * kFrag + 16 * lane;
+  const int token = 2 * (m >> 2) + (m & 1);                       // of this lane's operand row; half m >> 1 & 1
+  // rows of no token take another's: nothing reads what comes of them
+  const uint8_t* halves = static_cast<const uint8_t*>(a.halves) + 16 * (token < a.tokens ? lane : 16 * q);
+  int exponent[kOwnTokens] = {};
+
+  Codes c[kAhead];
+  f16x8 v[kAhead][4];
+  auto load = [&](int s) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) load_codes<MODE, F32>(a, row, s + k < steps ? s + k : steps - 1, q, c[k]);
+    if constexpr (!OWN)
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int step = s + k < steps ? s + k : steps - 1;
+          v[k][i] = *reinterpret_cast<const f16x8*>(halves + (int64_t)(4 * step + i) * kFrag);
+        }
+  };
+  if constexpr (OWN) {
+    // thread u has item u of each token: 8 values of k, at most one item a token (kOwnWidth / 8 threads)
+    const int u = threadIdx.x, k = kStep * (u >> 4) + 8 * dword_of<MODE>((u >> 2) & 3, u & 3);
+    float x[kOwnTokens][8];
+#pragma unroll
+    for (int t = 0; t < kOwnTokens; ++t) load_row<RHTQ_IN_F32, 8>(a.x, (t < a.tokens ? t : 0) * (int64_t)a.n + (k < a.n ? k : 0), x[t]);
+    load(s0);
+#pragma unroll
+    for (int t = 0; t < kOwnTokens; ++t) {
+      float top = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[t][e] = k < a.n ? x[t][e] : 0.0f;
+        top = fmaxf(top, __builtin_fabsf(x[t][e]));
+      }
+      top = workgroup_max<kWaves>(top, wave_max[t]);
+      exponent[t] = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) : 0;
+      f16x8 hi, lo;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        _Float16 h, l;
+        split_halves(__builtin_amdgcn_ldexpf(x[t][value_of<MODE>(e)], -exponent[t]), h, l);
+        hi[e] = h;
+        lo[e] = l;
+      }
+      if (u < 16 * steps) {
+        own[u][t] = hi;
+        own[u][t + 2] = lo;
+      }
+    }
+    __syncthreads();
+  } else {
+    load(s0);
+  }
   f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int s = s0; s < s1; s += kAhead) {
-    Codes c[kAhead];
+  auto step = [&](int s, int k) {
+    f16x8 w[4];
+    if constexpr (OWN)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[k][i] = own[16 * (s + k) + 4 * i + q][m & 3];
+    convert_scales<MODE, F32>(c[k], q);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = unpack<MODE>(c[k], i);
+    step_into<MODE>(acc, v[k], w, c[k]);
+  };
+  // Whole batches without a branch between their steps: the compiler moves a load behind a branch that may skip its use.
+  int s = s0;
+  for (; s + kAhead < s1; load(s)) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) step(s, k);
+    s += kAhead;
+  }
+  if (s + kAhead == s1) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) step(s, k);
+  } else {
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)
-      if (s + k < s1) load_codes<MODE>(a, row, s + k, q, c[k]);
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (s + k >= s1) break;
-      f16x8 v[4], w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] = f16x8{};
-        if (mine) v[i] = *reinterpret_cast<const f16x8*>(x + (int64_t)(4 * (s + k) + i) * kFrag);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = unpack<MODE>(c[k], i);
-      step_into<MODE>(acc, v, w, c[k]);
-    }
+      if (s + k < s1) step(s, k);
   }
   part[wave][lane] = acc;
   __syncthreads();
@@ -288,8 +403,8 @@ __global__ __launch_bounds__(64 * kWaves) void narrow_kernel(MatvecArgs a) {
     hi += p[b];
     lo += p[b + 2];
   }
-  const int64_t t = 8 * tile + 2 * q + b;
-  if (t < a.tokens && row0 + m < a.rows) store_y(a, t, row0 + m, whole(a, t, hi, lo));
+  const int64_t t = 2 * q + b;
+  if (t < a.tokens && row0 + m < a.rows) store_y(a, t, row0 + m, whole(a, OWN ? exponent[b] : a.exponents[t], hi, lo));
 }
 
 // ---- many tokens: 128 rows x up to 64 tokens per workgroup, k split over the grid -------------------------------------------
@@ -298,7 +413,7 @@ constexpr int kWide = 256;
 constexpr int kWideRows = 128;
 
 // TT token tiles.  Four waves share the operands of x through two buffers in LDS; each has 32 rows of its own.
-template <int MODE, int TT>
+template <int MODE, bool F32, int TT>
 __global__ __launch_bounds__(kWide) void wide_kernel(MatvecArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t buf[2][4 * TT * kFrag];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -323,12 +438,10 @@ __global__ __launch_bounds__(kWide) void wide_kernel(MatvecArgs a) {
   };
   f32x4 acc[2][TT] = {};
   Codes next[2];
-  if (s0 < s1) {
-    fetch(s0);
+  fetch(s0);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) load_codes<MODE>(a, row[r], s0, q, next[r]);
-    put(0);
-  }
+  for (int r = 0; r < 2; ++r) load_codes<MODE, F32>(a, row[r], s0, q, next[r]);
+  put(0);
   __syncthreads();
   for (int s = s0; s < s1; ++s) {
     const int b = (s - s0) & 1;
@@ -336,13 +449,15 @@ __global__ __launch_bounds__(kWide) void wide_kernel(MatvecArgs a) {
     if (s + 1 < s1) {
       fetch(s + 1);
 #pragma unroll
-      for (int r = 0; r < 2; ++r) load_codes<MODE>(a, row[r], s + 1, q, next[r]);
+      for (int r = 0; r < 2; ++r) load_codes<MODE, F32>(a, row[r], s + 1, q, next[r]);
     }
     f16x8 w[2][4];
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < 2; ++r) {
+      convert_scales<MODE, F32>(c[r], q);
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[r][i] = unpack<MODE>(c[r], i);
+    }
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
       f16x8 v[4];
@@ -364,7 +479,7 @@ __global__ __launch_bounds__(kWide) void wide_kernel(MatvecArgs a) {
       for (int b = 0; b < 2; ++b) {
         const int64_t tok = 8 * (tile0 + t) + 2 * q + b;
         if (tok >= a.tokens) continue;
-        const float v = whole(a, tok, acc[r][t][b], acc[r][t][b + 2]);
+        const float v = whole(a, a.exponents[tok], acc[r][t][b], acc[r][t][b + 2]);
         if (a.k_splits == 1) store_y(a, tok, at, v);
         else a.partial[((int64_t)blockIdx.y * a.tokens + tok) * a.rows + at] = v;
       }
@@ -375,27 +490,38 @@ __global__ __launch_bounds__(256) void join_kernel(MatvecArgs a) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, all = a.tokens * a.rows;
   if (i >= all) return;
   float v = 0.0f;
-  for (int k = 0; k < a.k_splits; ++k) v += a.partial[k * all + i];
+  for (int k = 0; k < a.k_splits; k += 8) {
+    float p[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) p[u] = k + u < a.k_splits ? a.partial[(k + u) * all + i] : 0.0f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v += p[u];
+  }
   store_y(a, i / a.rows, i % a.rows, v);
 }
 
 constexpr int kNarrowTokens = 4;
 
-template <int MODE>
+template <int MODE, bool F32>
 hipError_t launch_mode(int x_dtype, const MatvecArgs& a, hipStream_t s) {
   const unsigned padded = (unsigned)matvec_padded(a.tokens);
+  const dim3 tiles16((unsigned)((a.rows + 15) / 16));
+  if (x_dtype == RHTQ_IN_F32 && a.tokens <= kOwnTokens && a.n <= kOwnWidth && a.rows <= kOwnRows) {
+    hipLaunchKernelGGL((narrow_kernel<MODE, F32, true>), tiles16, dim3(64 * kWaves), 0, s, a);
+    return hipGetLastError();
+  }
   if (x_dtype == RHTQ_IN_BF16) hipLaunchKernelGGL((prepare_kernel<MODE, RHTQ_IN_BF16>), dim3(padded), dim3(kPrep), 0, s, a);
   else if (x_dtype == RHTQ_IN_F16) hipLaunchKernelGGL((prepare_kernel<MODE, RHTQ_IN_F16>), dim3(padded), dim3(kPrep), 0, s, a);
   else hipLaunchKernelGGL((prepare_kernel<MODE, RHTQ_IN_F32>), dim3(padded), dim3(kPrep), 0, s, a);
   if (a.tokens <= kNarrowTokens) {
-    hipLaunchKernelGGL((narrow_kernel<MODE>), dim3((unsigned)((a.rows + 15) / 16), 1), dim3(64 * kWaves), 0, s, a);
+    hipLaunchKernelGGL((narrow_kernel<MODE, F32, false>), tiles16, dim3(64 * kWaves), 0, s, a);
     return hipGetLastError();
   }
   const unsigned tiles = padded / 8, blocks = (unsigned)((a.rows + kWideRows - 1) / kWideRows), ks = (unsigned)a.k_splits;
-  if (tiles == 1) hipLaunchKernelGGL((wide_kernel<MODE, 1>), dim3(blocks, ks, 1), dim3(kWide), 0, s, a);
-  else if (tiles == 2) hipLaunchKernelGGL((wide_kernel<MODE, 2>), dim3(blocks, ks, 1), dim3(kWide), 0, s, a);
-  else if (tiles <= 4) hipLaunchKernelGGL((wide_kernel<MODE, 4>), dim3(blocks, ks, 1), dim3(kWide), 0, s, a);
-  else hipLaunchKernelGGL((wide_kernel<MODE, 8>), dim3(blocks, ks, tiles / 8), dim3(kWide), 0, s, a);
+  if (tiles == 1) hipLaunchKernelGGL((wide_kernel<MODE, F32, 1>), dim3(blocks, ks, 1), dim3(kWide), 0, s, a);
+  else if (tiles == 2) hipLaunchKernelGGL((wide_kernel<MODE, F32, 2>), dim3(blocks, ks, 1), dim3(kWide), 0, s, a);
+  else if (tiles <= 4) hipLaunchKernelGGL((wide_kernel<MODE, F32, 4>), dim3(blocks, ks, 1), dim3(kWide), 0, s, a);
+  else hipLaunchKernelGGL((wide_kernel<MODE, F32, 8>), dim3(blocks, ks, tiles / 8), dim3(kWide), 0, s, a);
   if (a.k_splits > 1)
     hipLaunchKernelGGL(join_kernel, dim3((unsigned)((a.tokens * a.rows + 255) / 256)), dim3(256), 0, s, a);
   return hipGetLastError();
@@ -424,12 +550,14 @@ int64_t matvec_halves_bytes(int64_t tokens, int32_t n) {
 }
 
 hipError_t launch_matvec(int x_dtype, const MatvecArgs& a, hipStream_t s) {
-  if (a.fmt == RHTQ_FMT_NVFP4) return launch_mode<MNV>(x_dtype, a, s);
-  if (a.fmt == RHTQ_FMT_MXFP4) return launch_mode<MMX>(x_dtype, a, s);
-  if (a.group_log < 0 || a.group_log >= 7) return launch_mode<M128>(x_dtype, a, s);
-  if (a.group_log == 6) return launch_mode<M64>(x_dtype, a, s);
-  if (a.group_log == 5) return launch_mode<M32>(x_dtype, a, s);
-  return launch_mode<M16>(x_dtype, a, s);
+  if (a.fmt == RHTQ_FMT_NVFP4) return launch_mode<MNV, false>(x_dtype, a, s);
+  if (a.fmt == RHTQ_FMT_MXFP4) return launch_mode<MMX, false>(x_dtype, a, s);
+  const bool f32 = a.scale_dtype == RHTQ_SCALE_F32;
+  const int group = a.group_log < 0 || a.group_log > 7 ? 7 : a.group_log;
+  if (group == 7) return f32 ? launch_mode<M128, true>(x_dtype, a, s) : launch_mode<M128, false>(x_dtype, a, s);
+  if (group == 6) return f32 ? launch_mode<M64, true>(x_dtype, a, s) : launch_mode<M64, false>(x_dtype, a, s);
+  if (group == 5) return f32 ? launch_mode<M32, true>(x_dtype, a, s) : launch_mode<M32, false>(x_dtype, a, s);
+  return f32 ? launch_mode<M16, true>(x_dtype, a, s) : launch_mode<M16, false>(x_dtype, a, s);
 }
 
 }  // namespace rhtq
