@@ -294,9 +294,10 @@ __device__ __forceinline__ float whole(const MatvecArgs& a, int exponent, float 
 
 constexpr int kWaves = 8;
 constexpr int kAhead = 4;          // steps whose codes and operands are in flight
-constexpr int kOwnTokens = 2;      // tokens that a workgroup splits into halves itself
-constexpr int kOwnWidth = 4096;    // and widths, as LDS holds them,
-constexpr int kOwnRows = 8192;     // and rows: beyond, one launch that does it once costs less
+// Rows of x that a workgroup splits into halves itself, and their width, as LDS holds them.  With one token this took 8.5 us instead of 11.4
+// for 4096 x 4096 and 24.3 instead of 28.1 for 24576 x 4096 (rotation included); with four, 12.9 instead of 12.1 and 22.1 instead of 19.8.
+constexpr int kOwnTokens = 2;
+constexpr int kOwnWidth = 4096;
 
 // OWN: x fp32 is split by every workgroup for itself, in LDS, while its codes are on their way, which saves a launch; otherwise the halves
 // lie ready.
@@ -304,8 +305,8 @@ template <int MODE, bool F32, bool OWN>
 __global__ __launch_bounds__(64 * kWaves) void narrow_kernel(MatvecArgs a) {
   __shared__ f32x4 part[kWaves][64];
   __shared__ float wave_max[kOwnTokens][kWaves];
-  // operands of two tokens: rows t + 2 half of lane group q of operand i
-  __shared__ __attribute__((aligned(16))) f16x8 own[OWN ? kOwnWidth / 8 : 1][4];
+  // operands: rows t + kOwnTokens * half of lane group q of operand i
+  __shared__ __attribute__((aligned(16))) f16x8 own[OWN ? kOwnWidth / 8 : 1][2 * kOwnTokens];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, q = lane >> 4;
   const int64_t row0 = (int64_t)blockIdx.x * 16;
@@ -315,6 +316,7 @@ __global__ __launch_bounds__(64 * kWaves) void narrow_kernel(MatvecArgs a) {
   const int token = 2 * (m >> 2) + (m & 1);                       // of this lane's operand row; half m >> 1 & 1
   // rows of no token take another's: nothing reads what comes of them
   const uint8_t* halves = static_cast<const uint8_t*>(a.halves) + 16 * (token < a.tokens ? lane : 16 * q);
+  const int own_row = (token < a.tokens ? token : 0) % kOwnTokens + (m & 2 ? kOwnTokens : 0);
   int exponent[kOwnTokens] = {};
 
   Codes c[kAhead];
@@ -336,17 +338,29 @@ __global__ __launch_bounds__(64 * kWaves) void narrow_kernel(MatvecArgs a) {
     const int u = threadIdx.x, k = kStep * (u >> 4) + 8 * dword_of<MODE>((u >> 2) & 3, u & 3);
     float x[kOwnTokens][8];
 #pragma unroll
-    for (int t = 0; t < kOwnTokens; ++t) load_row<RHTQ_IN_F32, 8>(a.x, (t < a.tokens ? t : 0) * (int64_t)a.n + (k < a.n ? k : 0), x[t]);
+    for (int t = 0; t < kOwnTokens; ++t)
+      if (t < a.tokens) load_row<RHTQ_IN_F32, 8>(a.x, t * (int64_t)a.n + (k < a.n ? k : 0), x[t]);
     load(s0);
 #pragma unroll
     for (int t = 0; t < kOwnTokens; ++t) {
+      if (t >= a.tokens) break;
       float top = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         x[t][e] = k < a.n ? x[t][e] : 0.0f;
         top = fmaxf(top, __builtin_fabsf(x[t][e]));
       }
-      top = workgroup_max<kWaves>(top, wave_max[t]);
+#pragma unroll
+      for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+      if (lane == 0) wave_max[t][wave] = top;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < kOwnTokens; ++t) {
+      if (t >= a.tokens) break;
+      float top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) top = fmaxf(top, wave_max[t][i]);
       exponent[t] = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) : 0;
       f16x8 hi, lo;
 #pragma unroll
@@ -358,7 +372,7 @@ __global__ __launch_bounds__(64 * kWaves) void narrow_kernel(MatvecArgs a) {
       }
       if (u < 16 * steps) {
         own[u][t] = hi;
-        own[u][t + 2] = lo;
+        own[u][t + kOwnTokens] = lo;
       }
     }
     __syncthreads();
@@ -370,7 +384,7 @@ __global__ __launch_bounds__(64 * kWaves) void narrow_kernel(MatvecArgs a) {
     f16x8 w[4];
     if constexpr (OWN)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[k][i] = own[16 * (s + k) + 4 * i + q][m & 3];
+      for (int i = 0; i < 4; ++i) v[k][i] = own[16 * (s + k) + 4 * i + q][own_row];
     convert_scales<MODE, F32>(c[k], q);
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = unpack<MODE>(c[k], i);
@@ -403,8 +417,16 @@ __global__ __launch_bounds__(64 * kWaves) void narrow_kernel(MatvecArgs a) {
     hi += p[b];
     lo += p[b + 2];
   }
-  const int64_t t = 2 * q + b;
-  if (t < a.tokens && row0 + m < a.rows) store_y(a, t, row0 + m, whole(a, OWN ? exponent[b] : a.exponents[t], hi, lo));
+  const int t = 2 * q + b;
+  if (t >= a.tokens || row0 + m >= a.rows) return;
+  int e = 0;
+  if constexpr (OWN) {
+#pragma unroll
+    for (int i = 0; i < kOwnTokens; ++i) e = i == t ? exponent[i] : e;
+  } else {
+    e = a.exponents[t];
+  }
+  store_y(a, t, row0 + m, whole(a, e, hi, lo));
 }
 
 // ---- many tokens: 128 rows x up to 64 tokens per workgroup, k split over the grid -------------------------------------------
@@ -506,7 +528,7 @@ template <int MODE, bool F32>
 hipError_t launch_mode(int x_dtype, const MatvecArgs& a, hipStream_t s) {
   const unsigned padded = (unsigned)matvec_padded(a.tokens);
   const dim3 tiles16((unsigned)((a.rows + 15) / 16));
-  if (x_dtype == RHTQ_IN_F32 && a.tokens <= kOwnTokens && a.n <= kOwnWidth && a.rows <= kOwnRows) {
+  if (x_dtype == RHTQ_IN_F32 && a.tokens <= kOwnTokens && a.n <= kOwnWidth) {
     hipLaunchKernelGGL((narrow_kernel<MODE, F32, true>), tiles16, dim3(64 * kWaves), 0, s, a);
     return hipGetLastError();
   }
