@@ -53,7 +53,8 @@ int rhtq_matvec(const void* x, int in_dtype, int64_t tokens, int32_t n, int32_t 
  * each row an INT4 row of rhtq_forward with one scale (group = head_dim).  head_dim 64, 128 or 256; page a
  * power of two, 16 to 256.  Position p of a sequence lies in page table[seq][p / page], slot p % page;
  * `table` is [seqs][width] int32.  An entry outside [0, pages) is no page: its positions are not stored, read as
- * zero and seen by no query.  A length beyond width * page counts as width * page, a negative one as 0.
+ * zero and seen by no query.  A length beyond width * page counts as width * page, a negative one as 0.  width * page stays below
+ * 2^31 - 256, a grid takes at most 65535 sequences' queries or key-value heads (RHTQ_EUNSUPPORTED beyond).
  *
  * The `tokens` new rows belong to sequences by `starts` [seqs+1], ascending from 0: rows starts[s] .. starts[s+1]-1
  * are the last positions of sequence s, up to lengths[s]-1 (lengths count them already).  starts NULL: one row
@@ -93,8 +94,9 @@ int rhtq_cache_read(const rhtq_cache_t* cache, void* k_out, void* v_out, int out
  *   q   [seqs][q_heads][head_dim] bf16 or fp16, strides in elements (rows 16-byte aligned); q_heads a multiple of kv_heads
  *   out [seqs][q_heads][head_dim] contiguous, q's type
  *   workspace  rhtq_paged_attention_workspace(...) bytes, 16-byte aligned
- * Scores, softmax and sums are in fp32 (exact integer products inside a stretch of positions).  The new token's own row has to
- * be appended first.
+ * Scores, softmax and sums are in fp32.  q enters the products as whole numbers to 2^-16 of a head's largest rotated value, the weights
+ * p_j * (scale of v_j) to 2^-16 of the largest among 64 positions; below 2^-110 they count as 0.  scale is finite, and scores
+ * stay finite in fp32.  The new token's own row has to be appended first.
  */
 int64_t rhtq_paged_attention_workspace(int32_t seqs, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t width,
                                        int32_t page, int32_t window, int32_t sinks);
@@ -107,7 +109,7 @@ int rhtq_paged_attention(const void* q, int in_dtype, int32_t seqs, int32_t q_he
  * Pages.  refs [pages] int32 counts the table entries that hold a page; 0 = free.  A fresh page is always the lowest free one.
  * The calls that take pages are all or nothing: *status (device int32) is 0 when done, the number of pages missing when there
  * were too few (nothing changed), or -1 when an index or an amount was invalid (nothing changed).
- * workspace: rhtq_pages_workspace(pages, seqs, count) bytes, 4-byte aligned.
+ * workspace: rhtq_pages_workspace(pages, seqs, count) bytes, 16-byte aligned.  The cache's scales are 16-byte aligned here.
  */
 int64_t rhtq_pages_workspace(int32_t pages, int32_t seqs, int32_t count);
 

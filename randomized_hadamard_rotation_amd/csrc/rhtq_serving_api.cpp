@@ -30,7 +30,8 @@ int check_cache(const rhtq_cache_t* c) {
 
 int check_table(int32_t width, int32_t seqs, int32_t page) {
   if (width < 0 || seqs < 0) return RHTQ_EINVAL;
-  if ((int64_t)width * page > INT32_MAX) return RHTQ_EINVAL;
+  // positions and the tiles beyond them stay 32-bit numbers
+  if ((int64_t)width * page > INT32_MAX - 256) return RHTQ_EINVAL;
   return RHTQ_OK;
 }
 
@@ -47,7 +48,7 @@ int cache_rows(const rhtq_cache_t* c, int64_t tokens, const int32_t* table, int3
   if (tokens < 0 || tokens > INT32_MAX || (!starts && tokens != seqs) || c->layers != 1) return RHTQ_EINVAL;
   if (c->kv_heads > 65535) return RHTQ_EUNSUPPORTED;   // a grid's limit
   if (tokens == 0) return RHTQ_OK;
-  if (!cache_pointers(c, scale_size(c->scale_dtype)) || !table || !lengths) return RHTQ_EINVAL;
+  if ((c->pages > 0 && !cache_pointers(c, scale_size(c->scale_dtype))) || (width > 0 && !table) || !lengths) return RHTQ_EINVAL;
   if (!aligned(table, 4) || !aligned(lengths, 4) || !aligned(starts, 4) || !aligned(k_signs, 4) || !aligned(v_signs, 4))
     return RHTQ_EINVAL;
   a.tokens = tokens;
@@ -234,7 +235,7 @@ int rhtq_paged_attention(const void* q, int in_dtype, int32_t seqs, int32_t q_he
   int st = check_cache(cache);
   if (st == RHTQ_OK) st = check_table(width, seqs, cache->page);
   if (st != RHTQ_OK) return st;
-  if (q_heads < 1 || cache->layers != 1 || window < 0 || sinks < 0 || !(scale == scale)) return RHTQ_EINVAL;
+  if (q_heads < 1 || cache->layers != 1 || window < 0 || sinks < 0 || !(scale - scale == 0.0f)) return RHTQ_EINVAL;
   if (q_heads % cache->kv_heads) return RHTQ_EUNSUPPORTED;
   if (q_seq_stride < 0 || q_head_stride < 0 || q_seq_stride % 8 || q_head_stride % 8) return RHTQ_EINVAL;
   if (seqs == 0) return RHTQ_OK;

@@ -433,6 +433,108 @@ def test_attention_huge_scores_stay_finite(R, size):
     assert np.allclose(g[clear], v[clear], rtol=2.0 ** -7, atol=2.0 ** -14 * np.abs(v).max())
 
 
+@pytest.mark.parametrize("sd", ["f16", "f32"])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 5)])
+def test_attention_sees_nothing_of_masked_places(R, sd, window, sinks):
+    """NaN, infinities and any bytes behind the last position, between the first positions and the window, and on unused pages."""
+    say("attention masked places", sd, window, sinks)
+    lens = [1, 15, 130, 700, 0]
+    cache, table, lengths = paged(R, lens, 2, 128, 16, sd, seed=17)
+    q = torch.randn(5, 8, 128, device="cuda", dtype=torch.float16)
+    ref = R.rhtq_paged_attention(q, cache, table, lengths, window=window, sinks=sinks)
+    tb = table.cpu().numpy()
+    seen = np.zeros((cache.k_codes.shape[0], 16), dtype=bool)
+    for s, n in enumerate(lens):
+        for p in range(n):
+            if not window or p >= n - window or p < sinks:
+                seen[tb[s, p // 16], p % 16] = True
+    hidden = torch.from_numpy(~seen).cuda()[:, None, :].expand(-1, 2, -1)
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        for t in (cache.k_scales, cache.v_scales):
+            t[hidden] = bad
+        for t in (cache.k_codes, cache.v_codes):
+            t[hidden] = 0x87
+        assert torch.equal(R.rhtq_paged_attention(q, cache, table, lengths, window=window, sinks=sinks), ref)
+
+
+def test_offsets_beyond_32_bits(R):
+    """Pages whose bytes start beyond 4 GiB: stored, read, attended to, copied, moved."""
+    say("offsets beyond 32 bits")
+    pages, kv, page, dim = 34000, 4, 256, 256                 # 131 KB a page and tensor: 4.4 GB of keys
+    cache = R.rhtq_cache_new(pages, kv, page, dim)
+    small, _, _ = paged(R, [1], kv, dim, page, "f16", seed=1, spare=7)
+    n = 300
+    far = torch.tensor([[33999, 33001]], dtype=torch.int32, device="cuda")
+    near = torch.tensor([[3, 5]], dtype=torch.int32, device="cuda")
+    lengths = torch.tensor([n], dtype=torch.int32, device="cuda")
+    starts = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    x = torch.randn(2, n, kv, dim, device="cuda", dtype=torch.bfloat16)
+    q = torch.randn(1, 8, dim, device="cuda", dtype=torch.bfloat16)
+    out = []
+    for c, t in ((cache, far), (small, near)):
+        R.rhtq_cache_append(c, x[0], x[1], t, lengths, starts)
+        out.append(R.rhtq_cache_read(c, t, lengths, starts, n) + (R.rhtq_paged_attention(q, c, t, lengths),))
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    R.rhtq_pages_copy(cache, ints(33999, 33001), ints(33500, 40))
+    t = torch.tensor([[33500, 40]], dtype=torch.int32, device="cuda")
+    assert torch.equal(R.rhtq_paged_attention(q, cache, t, lengths), out[0][2])
+    refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    refs[far[0].long()] = 1
+    assert R.rhtq_pages_compact(cache, far, refs).item() == 2
+    assert sorted(far[0].tolist()) == [0, 1] and torch.equal(R.rhtq_paged_attention(q, cache, far, lengths), out[0][2])
+
+
+def test_cache_without_pages(R):
+    """No page, or a table without columns: rows are passed over, zeros come back."""
+    say("cache without pages")
+    empty = R.rhtq_cache_new(0, 2, 16, 128)
+    lengths = torch.tensor([5, 9], dtype=torch.int32, device="cuda")
+    x = torch.randn(2, 2, 128, device="cuda", dtype=torch.float16)
+    full, table, _ = paged(R, [5, 9], 2, 128, 16, "f16", seed=2)
+    for c, t in ((empty, table), (empty, table[:, :0].contiguous()), (full, table[:, :0].contiguous())):
+        R.rhtq_cache_append(c, x, x, t, lengths)
+        k, v = R.rhtq_cache_read(c, t, lengths, None, 2, dtype=torch.float16)
+        assert (k == 0).all() and (v == 0).all()
+        assert (R.rhtq_paged_attention(x, c, t, lengths) == 0).all()
+
+
+def test_calls_from_many_threads(R):
+    """Eight threads on streams of their own, all calls at once, against the calls one after another."""
+    import threading
+    say("calls from many threads")
+    cache, table, lengths = paged(R, [700, 90, 33], 2, 128, 16, "f16", seed=41)
+    p, s, ts, w = weights(300, 1024, "int4", 64, "f16", 5)
+    dp, ds, _ = device_weights(p, s, ts)
+    qs = [torch.randn(3, 8, 128, device="cuda", dtype=torch.bfloat16) for _ in range(8)]
+    xs = [torch.randn(1 + 3 * i, 1024, device="cuda", dtype=torch.bfloat16) for i in range(8)]
+    sg = torch.from_numpy(signs_of(1024, 3)).cuda()
+
+    def calls(i):
+        return (R.rhtq_paged_attention(qs[i], cache, table, lengths), R.rhtq_matvec(dp, ds, xs[i], sg, group=64, scale_dtype="f16"),
+                R.rhtq_cache_read(cache, table, lengths, None, 3)[0])
+    one = [calls(i) for i in range(8)]
+    torch.cuda.synchronize()
+    got, errors = [None] * 8, []
+
+    def run(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(5):
+                    got[i] = calls(i)
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for a, b in zip(one, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 def test_attention_missing_pages(R):
     """Entries that name no page are seen by no query; a sequence with none left gets zeros.  Lengths beyond the table end with it."""
     say("attention missing pages")

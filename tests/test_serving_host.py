@@ -103,7 +103,7 @@ def test_bad_caches(kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(tokens=-1), EINVAL), (dict(tokens=5), EINVAL), (dict(dt=7), EINVAL), (dict(table=NIL), EINVAL), (dict(lengths=NIL), EINVAL),
     (dict(lengths=FAKE + 2), EINVAL), (dict(starts=FAKE + 2), EINVAL), (dict(signs=FAKE + 1), EINVAL), (dict(width=-1), EINVAL),
-    (dict(width=1 << 30), EINVAL), (dict(seqs=-1, starts=FAKE), EINVAL), (dict(tokens=0, seqs=0, table=NIL, lengths=NIL), OK),
+    (dict(width=1 << 30), EINVAL), (dict(width=(1 << 27) - 1), EINVAL), (dict(seqs=-1, starts=FAKE), EINVAL), (dict(tokens=0, seqs=0, table=NIL, lengths=NIL), OK),
     (dict(tokens=1 << 40, starts=FAKE), EINVAL),
 ])
 def test_row_refusals(kw, status):
@@ -125,7 +125,7 @@ def attention(c=None, q=FAKE, dt=0, seqs=4, heads=8, qs=1024, qh=128, table=FAKE
 
 @pytest.mark.parametrize("kw,status", [
     (dict(dt=R.RHTQ_IN_F32), EUNS), (dict(dt=9), EINVAL), (dict(heads=0), EINVAL), (dict(heads=3), EUNS), (dict(qs=100), EINVAL),
-    (dict(qh=-8), EINVAL), (dict(window=-1), EINVAL), (dict(sinks=-1), EINVAL), (dict(scale=float("nan")), EINVAL), (dict(q=NIL), EINVAL),
+    (dict(qh=-8), EINVAL), (dict(window=-1), EINVAL), (dict(sinks=-1), EINVAL), (dict(scale=float("nan")), EINVAL), (dict(scale=float("inf")), EINVAL), (dict(seqs=70000), EUNS), (dict(q=NIL), EINVAL),
     (dict(out=MIS), EINVAL), (dict(lengths=NIL), EINVAL), (dict(table=NIL), EINVAL), (dict(seqs=-1), EINVAL), (dict(seqs=0, q=NIL), OK),
     (dict(width=1 << 20, work=NIL), EINVAL), (dict(width=1 << 20, size=4), EINVAL), (dict(signs=FAKE + 1), EINVAL),
 ])
