@@ -429,12 +429,12 @@ __global__ __launch_bounds__(64 * kWaves) void narrow_kernel(MatvecArgs a) {
   store_y(a, t, row0 + m, whole(a, e, hi, lo));
 }
 
-// ---- many tokens: 128 rows x up to 64 tokens per workgroup, k split over the grid -------------------------------------------
+// ---- many tokens: 256 rows x up to 64 tokens per workgroup, k split over the grid -------------------------------------------
 
-constexpr int kWide = 256;
-constexpr int kWideRows = 128;
+constexpr int kWide = 512;
+constexpr int kWideRows = 256;
 
-// TT token tiles.  Four waves share the operands of x through two buffers in LDS; each has 32 rows of its own.
+// TT token tiles.  Eight waves share the operands of x through two buffers in LDS; each has 32 rows of its own.
 template <int MODE, bool F32, int TT>
 __global__ __launch_bounds__(kWide) void wide_kernel(MatvecArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t buf[2][4 * TT * kFrag];
@@ -448,15 +448,21 @@ __global__ __launch_bounds__(kWide) void wide_kernel(MatvecArgs a) {
   const int steps = (a.n + kStep - 1) / kStep;
   const int s0 = (int)((int64_t)steps * blockIdx.y / a.k_splits), s1 = (int)((int64_t)steps * (blockIdx.y + 1) / a.k_splits);
   const uint8_t* halves = static_cast<const uint8_t*>(a.halves);
-  u32x4 stage[TT];
+  // half the workgroup's threads hold a token tile's operands of a step, 16 bytes each
+  constexpr int FETCH = (TT + 1) / 2;
+  const int tile_half = threadIdx.x >> 8, piece = 16 * (threadIdx.x & 255);
+  u32x4 stage[FETCH];
   auto fetch = [&](int s) {
 #pragma unroll
-    for (int t = 0; t < TT; ++t)
-      stage[t] = *reinterpret_cast<const u32x4*>(halves + ((tile0 + t) * steps + s) * 4 * kFrag + 16 * threadIdx.x);
+    for (int t = 0; t < FETCH; ++t) {
+      const int tile = 2 * t + tile_half < TT ? 2 * t + tile_half : 0;
+      stage[t] = *reinterpret_cast<const u32x4*>(halves + ((tile0 + tile) * steps + s) * 4 * kFrag + piece);
+    }
   };
   auto put = [&](int b) {
 #pragma unroll
-    for (int t = 0; t < TT; ++t) *reinterpret_cast<u32x4*>(&buf[b][4 * t * kFrag + 16 * threadIdx.x]) = stage[t];
+    for (int t = 0; t < FETCH; ++t)
+      if (TT > 1 || tile_half == 0) *reinterpret_cast<u32x4*>(&buf[b][4 * (2 * t + tile_half) * kFrag + piece]) = stage[t];
   };
   f32x4 acc[2][TT] = {};
   Codes next[2];
@@ -561,7 +567,7 @@ int32_t matvec_splits(int64_t tokens, int32_t n, int64_t rows) {
   if (tokens <= kNarrowTokens) return 1;
   const int64_t blocks = (rows + kWideRows - 1) / kWideRows * ((matvec_padded(tokens) + 63) / 64);
   const int64_t steps = (n + kStep - 1) / kStep;
-  int64_t k = 512 / blocks;
+  int64_t k = 256 / blocks;
   if (k > steps / 2) k = steps / 2;
   return k < 1 ? 1 : (int32_t)k;
 }
