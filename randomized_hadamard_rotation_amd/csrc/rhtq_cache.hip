@@ -198,7 +198,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(CacheArgs a) {
       const f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int u = 0; u < 2; ++u) d[r][u] = stage1_mma<H16>(v, h[u], z);
-  }
+    }
 #pragma unroll
     for (int b = 1; b < NB; b *= 2)
 #pragma unroll
@@ -216,7 +216,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(CacheArgs a) {
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] = d[e % NB][e / NB][k];
       store_codes<E>(a, which, slot[4 * l + k], v);
-  }
+    }
   }
 }
 
