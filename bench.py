@@ -55,6 +55,15 @@ KERNEL_SOURCES = ["randomized_hadamard_rotation_amd/csrc/rhtq_fast.hip",
                   "randomized_hadamard_rotation_amd/csrc/rhtq_floor.hip",
                   "include/rhtq.h",
                   "include/rhtq_floor.h",
+                  "randomized_hadamard_rotation_amd/csrc/rhtq_attention.hip",
+                  "randomized_hadamard_rotation_amd/csrc/rhtq_cache.hip",
+                  "randomized_hadamard_rotation_amd/csrc/rhtq_matvec.hip",
+                  "randomized_hadamard_rotation_amd/csrc/rhtq_pages.hip",
+                  "randomized_hadamard_rotation_amd/csrc/rhtq_paging.h",
+                  "randomized_hadamard_rotation_amd/csrc/rhtq_serving_api.cpp",
+                  "randomized_hadamard_rotation_amd/csrc/rhtq_serving_device.h",
+                  "randomized_hadamard_rotation_amd/csrc/rhtq_serving_internal.h",
+                  "include/serving/rhtq_serving.h",
                   "randomized_hadamard_rotation_amd/build.py"]   # compiler flags shape the kernels too
 
 

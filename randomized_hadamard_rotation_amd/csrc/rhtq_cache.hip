@@ -334,7 +334,7 @@ __global__ __launch_bounds__(kThreads) void read_kernel(CacheArgs a) {
           d[1][r][u] = d[0][r][u] - d[1][r][u];
           d[0][r][u] = sum;
         }
-  }
+    }
     const float cnorm = D == 64 ? 0.125f : (D == 128 ? 0.088388347648318447f : 0.0625f);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -348,7 +348,7 @@ __global__ __launch_bounds__(kThreads) void read_kernel(CacheArgs a) {
         apply_signs<E>(signs[h], v);
         store_row<T, E>(a.y[which], ((int64_t)t[4 * l + k] * a.kv_heads + head) * D + 128 * h + E * n, v);
       }
-  }
+    }
   }
 }
 

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from typing import NamedTuple
 
 import torch
@@ -80,9 +81,14 @@ class _CacheStruct(ctypes.Structure):
                 ("scale_dtype", ctypes.c_int32)]
 
 
+# the same struct as bytes, which a pointer argument takes as they are (a third of the time of a Structure)
+_pack_cache = struct.Struct("@4P6i").pack
+assert struct.calcsize("@4P6i") == ctypes.sizeof(_CacheStruct)
+
+
 def _declare():
     vp, i32, i64, ci, fl = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int, ctypes.c_float
-    cache = ctypes.POINTER(_CacheStruct)
+    cache = vp
     args = {
         "rhtq_serving_version": (ci, []),
         "rhtq_matvec_workspace": (i64, [i64, i32, i64]),
@@ -135,7 +141,7 @@ def rhtq_cache_new(pages: int, kv_heads: int, page: int, head_dim: int, scale_dt
 
 
 def _cache_struct(cache, layered):
-    """The C struct of a cache whose four tensors agree; with `layered`, a leading axis is taken."""
+    """(C struct, pages, kv_heads, page, head_dim) of a cache whose four tensors agree; with `layered`, a leading axis is taken."""
     k, ks, v, vs = cache
     shape = k.shape
     dims = len(shape)
@@ -150,8 +156,9 @@ def _cache_struct(cache, layered):
         for t, name, dtype, want in ((k, "k_codes", _U8, shape), (ks, "k_scales", sdt, shape[:-1]), (v, "v_codes", _U8, shape),
                                      (vs, "v_scales", sdt, shape[:-1])):
             _expect(t, name, dtype, want)
-    return _CacheStruct(k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(), shape[0] if dims == 5 else 1, shape[-4],
-                        shape[-3], shape[-2], 2 * shape[-1], _SCALE_OF[sdt])
+    pages, kv_heads, page, half = shape[-4:]
+    return (_pack_cache(k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(), shape[0] if dims == 5 else 1, pages, kv_heads, page,
+                        2 * half, _SCALE_OF[sdt]), pages, kv_heads, page, 2 * half)
 
 
 def _int32(t, name, shape):
@@ -274,8 +281,8 @@ def rhtq_cache_append(cache: RhtqCache, k, v, table, lengths, starts=None, k_sig
         raise ValueError("k and v must both be bfloat16, float16 or float32")
     tokens, kv_heads, dim = k.shape
     c, seqs, width = _rows_of(cache, table, lengths, starts, tokens)
-    if c.kv_heads != kv_heads or c.head_dim != dim:
-        raise ValueError(f"k: {tuple(k.shape)}, expected {(tokens, c.kv_heads, c.head_dim)}")
+    if c[2] != kv_heads or c[4] != dim:
+        raise ValueError(f"k: {tuple(k.shape)}, expected {(tokens, c[2], c[4])}")
     index = k.get_device()
     _one_device(index, {"k": k, "v": v, "k_codes": cache[0], "k_scales": cache[1], "v_codes": cache[2], "v_scales": cache[3],
                         "table": table, "lengths": lengths, "starts": starts})
@@ -285,7 +292,7 @@ def rhtq_cache_append(cache: RhtqCache, k, v, table, lengths, starts=None, k_sig
         kc, vc = _row_strides(k), _row_strides(v)
         if stream is not None:
             on.follow(stream)
-        _check(lib.rhtq_cache_append(ctypes.byref(c), kc.data_ptr(), vc.data_ptr(), in_type, tokens, kc.stride(0), kc.stride(1),
+        _check(lib.rhtq_cache_append(c[0], kc.data_ptr(), vc.data_ptr(), in_type, tokens, kc.stride(0), kc.stride(1),
                                      vc.stride(0), vc.stride(1), table.data_ptr(), width, lengths.data_ptr(), _p(starts), seqs,
                                      _p(ks), _p(vs), on.raw), "rhtq_cache_append")
         on.keep(ks, vs, kc if kc is not k else None, vc if vc is not v else None)
@@ -303,7 +310,8 @@ def rhtq_cache_read(cache: RhtqCache, table, lengths, starts, tokens: int, k_sig
     if tokens < 0:
         raise ValueError("tokens must not be negative")
     c, seqs, width = _rows_of(cache, table, lengths, starts, tokens)
-    shape = (tokens, c.kv_heads, c.head_dim)
+    dim = c[4]
+    shape = (tokens, c[2], dim)
     for name, t in (("k_out", k_out), ("v_out", v_out)):
         if t is not None:
             _expect(t, name, dtype, shape)
@@ -313,7 +321,7 @@ def rhtq_cache_read(cache: RhtqCache, table, lengths, starts, tokens: int, k_sig
                         "lengths": lengths, "starts": starts, "k_out": k_out, "v_out": v_out})
     on = _On(index)
     try:
-        ks, vs = _signs(k_signs, c.head_dim, first), _signs(v_signs, c.head_dim, first)
+        ks, vs = _signs(k_signs, dim, first), _signs(v_signs, dim, first)
         own_k, own_v = k_out is None, v_out is None
         if own_k:
             k_out = first.new_empty(shape, dtype=dtype)
@@ -321,7 +329,7 @@ def rhtq_cache_read(cache: RhtqCache, table, lengths, starts, tokens: int, k_sig
             v_out = first.new_empty(shape, dtype=dtype)
         if stream is not None:
             on.follow(stream)
-        _check(lib.rhtq_cache_read(ctypes.byref(c), k_out.data_ptr(), v_out.data_ptr(), _IN[dtype], tokens, table.data_ptr(), width,
+        _check(lib.rhtq_cache_read(c[0], k_out.data_ptr(), v_out.data_ptr(), _IN[dtype], tokens, table.data_ptr(), width,
                                    lengths.data_ptr(), _p(starts), seqs, _p(ks), _p(vs), on.raw), "rhtq_cache_read")
         on.keep(ks, vs, k_out if own_k else None, v_out if own_v else None)
     finally:
@@ -342,9 +350,9 @@ def rhtq_paged_attention(q, cache: RhtqCache, table, lengths, k_signs=None, v_si
         raise ValueError("q must be bfloat16 or float16")
     c, seqs, width = _rows_of(cache, table, lengths, None, q.shape[0])
     q_heads, dim = q.shape[1:]
-    kv_heads = c.kv_heads
-    if dim != c.head_dim or q_heads < 1 or q_heads % max(kv_heads, 1):
-        raise ValueError(f"q: {tuple(q.shape)} does not fit {kv_heads} key-value heads of {c.head_dim}")
+    kv_heads = c[2]
+    if dim != c[4] or q_heads < 1 or q_heads % max(kv_heads, 1):
+        raise ValueError(f"q: {tuple(q.shape)} does not fit {kv_heads} key-value heads of {c[4]}")
     if window < 0 or sinks < 0:
         raise ValueError("window and sinks must not be negative")
     if out is not None:
@@ -359,11 +367,11 @@ def rhtq_paged_attention(q, cache: RhtqCache, table, lengths, k_signs=None, v_si
         own = out is None
         if own:
             out = q.new_empty(q.shape)
-        need = lib.rhtq_paged_attention_workspace(seqs, q_heads, kv_heads, dim, width, c.page, window, sinks)
+        need = lib.rhtq_paged_attention_workspace(seqs, q_heads, kv_heads, dim, width, c[3], window, sinks)
         work = q.new_empty(need, dtype=_U8) if need else None
         if stream is not None:
             on.follow(stream)
-        _check(lib.rhtq_paged_attention(qc.data_ptr(), in_type, seqs, q_heads, qc.stride(0), qc.stride(1), ctypes.byref(c),
+        _check(lib.rhtq_paged_attention(qc.data_ptr(), in_type, seqs, q_heads, qc.stride(0), qc.stride(1), c[0],
                                         table.data_ptr(), width, lengths.data_ptr(), _p(ks), _p(vs),
                                         1.0 / math.sqrt(dim) if scale is None else scale, window, sinks, out.data_ptr(), _p(work),
                                         need, on.raw), "rhtq_paged_attention")
@@ -386,8 +394,8 @@ def _paging(table, lengths, refs):
 
 def _paged_cache(cache, refs):
     c = _cache_struct(cache, True)
-    if c.pages != refs.shape[0]:
-        raise ValueError(f"refs has {refs.shape[0]} entries, the cache {c.pages} pages")
+    if c[1] != refs.shape[0]:
+        raise ValueError(f"refs has {refs.shape[0]} entries, the cache {c[1]} pages")
     return c
 
 
@@ -460,7 +468,7 @@ def rhtq_pages_fork(cache: RhtqCache, table, lengths, refs, src, dst, stream=Non
     count = _index_list(src, "src")
     _index_list(dst, "dst", src.shape)
     return _page_call("rhtq_pages_fork", {"table": table, "lengths": lengths, "refs": refs, "src": src, "dst": dst, **_tensors(cache)}, stream,
-                      lambda raw, word, work, size: lib.rhtq_pages_fork(ctypes.byref(c), table.data_ptr(), width, lengths.data_ptr(), seqs,
+                      lambda raw, word, work, size: lib.rhtq_pages_fork(c[0], table.data_ptr(), width, lengths.data_ptr(), seqs,
                                                                         refs.data_ptr(), src.data_ptr(), dst.data_ptr(), count, word, work,
                                                                         size, raw),
                       refs.shape[0], seqs, count, True)
@@ -472,7 +480,7 @@ def rhtq_pages_copy(cache: RhtqCache, src, dst, stream=None):
     count = _index_list(src, "src")
     _index_list(dst, "dst", src.shape)
     _page_call("rhtq_pages_copy", {**_tensors(cache), "src": src, "dst": dst}, stream,
-               lambda raw, word, work, size: lib.rhtq_pages_copy(ctypes.byref(c), src.data_ptr(), dst.data_ptr(), count, raw))
+               lambda raw, word, work, size: lib.rhtq_pages_copy(c[0], src.data_ptr(), dst.data_ptr(), count, raw))
 
 
 def rhtq_pages_compact(cache: RhtqCache, table, refs, stream=None):
@@ -480,6 +488,6 @@ def rhtq_pages_compact(cache: RhtqCache, table, refs, stream=None):
     c = _paged_cache(cache, refs)
     seqs, width = _paging(table, None, refs)
     return _page_call("rhtq_pages_compact", {"table": table, "refs": refs, **_tensors(cache)}, stream,
-                      lambda raw, word, work, size: lib.rhtq_pages_compact(ctypes.byref(c), table.data_ptr(), width, seqs, refs.data_ptr(), word,
+                      lambda raw, word, work, size: lib.rhtq_pages_compact(c[0], table.data_ptr(), width, seqs, refs.data_ptr(), word,
                                                                            work, size, raw),
                       refs.shape[0], seqs, 0, True)

@@ -104,7 +104,7 @@ def test_bad_caches(kw, status):
     (dict(tokens=-1), EINVAL), (dict(tokens=5), EINVAL), (dict(dt=7), EINVAL), (dict(table=NIL), EINVAL), (dict(lengths=NIL), EINVAL),
     (dict(lengths=FAKE + 2), EINVAL), (dict(starts=FAKE + 2), EINVAL), (dict(signs=FAKE + 1), EINVAL), (dict(width=-1), EINVAL),
     (dict(width=1 << 30), EINVAL), (dict(width=(1 << 27) - 1), EINVAL), (dict(seqs=-1, starts=FAKE), EINVAL), (dict(tokens=0, seqs=0, table=NIL, lengths=NIL), OK),
-    (dict(tokens=1 << 40, starts=FAKE), EINVAL),
+    (dict(tokens=1 << 40, starts=FAKE), EINVAL), (dict(tokens=(1 << 31) - 1, starts=FAKE), EINVAL),
 ])
 def test_row_refusals(kw, status):
     assert append(**kw) == status
