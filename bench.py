@@ -63,7 +63,6 @@ KERNEL_SOURCES = ["randomized_hadamard_rotation_amd/csrc/rhtq_fast.hip",
                   "randomized_hadamard_rotation_amd/csrc/rhtq_serving_api.cpp",
                   "randomized_hadamard_rotation_amd/csrc/rhtq_serving_device.h",
                   "randomized_hadamard_rotation_amd/csrc/rhtq_serving_internal.h",
-                  "include/serving/rhtq_serving.h",
                   "randomized_hadamard_rotation_amd/build.py"]   # compiler flags shape the kernels too
 
 
