@@ -37,6 +37,11 @@ __device__ __forceinline__ int token_block() { return (int)(blockIdx.y + blockId
 // sequence is the number of sequences that end at or before it, counted by the 16 lanes together.
 template <int N>
 __device__ __forceinline__ void slots_of(const CacheArgs& a, const int (&t)[N], int head, int64_t (&slot)[N]) {
+  if (a.seqs == 0) {                       // nothing of starts (but its 0) and lengths is there to read
+#pragma unroll
+    for (int k = 0; k < N; ++k) slot[k] = -1;
+    return;
+  }
   const int tokens = (int)a.tokens;        // below 2^31
   int s[N], pos[N];
 #pragma unroll

@@ -48,7 +48,8 @@ int cache_rows(const rhtq_cache_t* c, int64_t tokens, const int32_t* table, int3
   if (tokens < 0 || tokens > INT32_MAX - 1024 || (!starts && tokens != seqs) || c->layers != 1) return RHTQ_EINVAL;
   if (c->kv_heads > 65535) return RHTQ_EUNSUPPORTED;   // a grid's limit
   if (tokens == 0) return RHTQ_OK;
-  if ((c->pages > 0 && !cache_pointers(c, scale_size(c->scale_dtype))) || (width > 0 && !table) || !lengths) return RHTQ_EINVAL;
+  if (c->pages > 0 && !cache_pointers(c, scale_size(c->scale_dtype))) return RHTQ_EINVAL;
+  if (seqs > 0 && ((width > 0 && !table) || !lengths)) return RHTQ_EINVAL;
   if (!aligned(table, 4) || !aligned(lengths, 4) || !aligned(starts, 4) || !aligned(k_signs, 4) || !aligned(v_signs, 4))
     return RHTQ_EINVAL;
   a.tokens = tokens;
@@ -202,6 +203,7 @@ int rhtq_cache_append(const rhtq_cache_t* cache, const void* k, const void* v, i
   a.token_stride[1] = v_token_stride;
   a.head_stride[0] = k_head_stride;
   a.head_stride[1] = v_head_stride;
+  if (seqs == 0) return RHTQ_OK;   // no row belongs to a sequence
   if (rhtq::getenv_test_fail_launch()) return RHTQ_EHIP;
   return from_hip(rhtq::launch_cache_append(in_dtype, a, reinterpret_cast<hipStream_t>(stream)));
 }

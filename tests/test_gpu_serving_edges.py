@@ -1,0 +1,57 @@
+"""GPU: calls at the edges of what the serving header allows."""
+import sys
+
+import numpy as np
+import pytest
+
+import oracle as O
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+def say(*msg):
+    print("[case]", *msg, flush=True)
+    sys.stdout.flush()
+
+
+@pytest.fixture(scope="module")
+def R():
+    if not torch.cuda.is_available():
+        pytest.fail("no GPU visible")
+    import randomized_hadamard_rotation_amd as R
+    return R
+
+
+def ints(*v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def filled(R, pages, kv, page, dim, seed, **kw):
+    """A cache of random rows."""
+    rs = np.random.RandomState(seed)
+    cache = R.rhtq_cache_new(pages, kv, page, dim, **kw)
+    for c in (cache.k_codes, cache.v_codes):
+        c.copy_(torch.from_numpy(rs.randint(0, 256, tuple(c.shape)).astype(np.uint8)))
+    for s in (cache.k_scales, cache.v_scales):
+        s.copy_(torch.from_numpy(0.1 + 0.2 * rs.rand(*s.shape)))
+    return cache
+
+
+# ------------------------------------------------------------------------------------------------------------ cache
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_rows_without_sequences(R, dim):
+    """No sequence at all: rows belong to none, so nothing is stored and zeros are read."""
+    say("rows without sequences", dim)
+    cache = filled(R, 3, 2, 16, dim, 1)
+    before = [t.clone() for t in cache]
+    table, none = torch.zeros((0, 4), dtype=torch.int32, device="cuda"), ints()
+    for dtype in (torch.bfloat16, torch.float32):
+        x = torch.randn(5, 2, dim, device="cuda", dtype=dtype)
+        R.rhtq_cache_append(cache, x, x, table, none, ints(0))
+        out = [torch.full((5, 2, dim), float("nan"), dtype=dtype, device="cuda") for _ in range(2)]
+        R.rhtq_cache_read(cache, table, none, ints(0), 5, dtype=dtype, k_out=out[0], v_out=out[1])
+        assert all((o == 0).all() for o in out)
+    assert all(torch.equal(a, b) for a, b in zip(before, cache))

@@ -1,0 +1,36 @@
+"""CPU: calls at the edges of what the serving header allows, answered or refused on the host before any HIP call."""
+import ctypes
+
+import pytest
+import torch
+
+import randomized_hadamard_rotation_amd as R
+from randomized_hadamard_rotation_amd import serving
+
+FAKE, NIL = 0x100000, None       # never dereferenced: every call below is refused or has nothing to do
+EINVAL, EUNS, OK = R.RHTQ_EINVAL, R.RHTQ_EUNSUPPORTED, R.RHTQ_OK
+
+
+def cache(**kw):
+    a = dict(k_codes=FAKE, k_scales=FAKE, v_codes=FAKE, v_scales=FAKE, layers=1, pages=10, kv_heads=2, page=16, head_dim=128,
+             scale_dtype=R.RHTQ_SCALE_F16)
+    a.update(kw)
+    return ctypes.byref(serving._CacheStruct(**a))
+
+
+def append(c=None, k=FAKE, tokens=4, table=FAKE, width=3, lengths=FAKE, starts=NIL, seqs=4):
+    return R.lib.rhtq_cache_append(c or cache(), k, k, R.RHTQ_IN_BF16, tokens, 256, 128, 256, 128, table, width, lengths, starts, seqs, NIL,
+                                   NIL, NIL)
+
+
+def read(c=None, k=FAKE, tokens=4, table=FAKE, width=3, lengths=FAKE, starts=NIL, seqs=4):
+    return R.lib.rhtq_cache_read(c or cache(), k, k, R.RHTQ_IN_BF16, tokens, table, width, lengths, starts, seqs, NIL, NIL, NIL)
+
+
+def test_rows_of_no_sequence_without_sequences():
+    """seqs = 0: lengths and the table have no entry, and starts has one.  Rows are passed over; nothing is enqueued to store them."""
+    assert append(seqs=0, starts=FAKE, lengths=NIL, table=NIL) == OK
+    assert append(seqs=0, starts=FAKE) == OK
+    assert append(seqs=0, starts=NIL) == EINVAL          # without starts there is one row a sequence
+    assert append(seqs=0, starts=FAKE, k=NIL) == EINVAL
+    assert append(seqs=1, starts=FAKE, lengths=NIL) == EINVAL and read(seqs=1, starts=FAKE, table=NIL) == EINVAL
