@@ -53,8 +53,9 @@ int rhtq_matvec(const void* x, int in_dtype, int64_t tokens, int32_t n, int32_t 
  * each row an INT4 row of rhtq_forward with one scale (group = head_dim).  head_dim 64, 128 or 256; page a
  * power of two, 16 to 256.  Position p of a sequence lies in page table[seq][p / page], slot p % page;
  * `table` is [seqs][width] int32.  An entry outside [0, pages) is no page: its positions are not stored, read as
- * zero and seen by no query.  A length beyond width * page counts as width * page, a negative one as 0.  width * page stays below
- * 2^31 - 256, a call takes up to 2^31 - 1024 rows a head, and a grid at most 65535 sequences' queries or key-value heads (RHTQ_EUNSUPPORTED beyond).
+ * zero and seen by no query.  A length beyond width * page counts as width * page, a negative one as 0.
+ * Limits: width * page below 2^31 - 256 and up to 2^31 - 2^23 rows a call (RHTQ_EINVAL beyond); 65535 sequences of a query call, 65535
+ * key-value heads (RHTQ_EUNSUPPORTED beyond).
  *
  * The `tokens` new rows belong to sequences by `starts` [seqs+1], ascending from 0: rows starts[s] .. starts[s+1]-1
  * are the last positions of sequence s, up to lengths[s]-1 (lengths count them already).  starts NULL: one row

@@ -30,7 +30,7 @@ constexpr int kWaves = kThreads / 64;
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int64_t kColumn = 32768;      // token blocks in a grid's y; the rest in z
+// token blocks: kColumn in a grid's y, the rest in z
 __device__ __forceinline__ int token_block() { return (int)(blockIdx.y + blockIdx.z * kColumn); }
 
 // Places of N tokens of a group of 16 lanes, the same in all of them: offset of the slot in rows of the code arrays, or -1.  A token's
@@ -362,6 +362,7 @@ __global__ __launch_bounds__(kThreads) void read_kernel(CacheArgs a) {
 // Heads of keys and values run fastest, then tokens: workgroups that run together then read and write neighbouring memory.  With tokens first
 // they all took the same head of rows 16 KB apart, a few channels' worth: with one tile a wave, 188 us to store and
 // 227 us to read where this order took 185 and 220.
+static_assert(kMostRows + kColumn * kBlockRows <= INT32_MAX && 32 * kWaves <= kBlockRows && kGroups <= kBlockRows, "row numbers");
 dim3 grid_of(const CacheArgs& a, int per) {
   const int64_t blocks = (a.tokens + per - 1) / per, y = blocks < kColumn ? blocks : kColumn;
   return dim3((unsigned)(2 * a.kv_heads), (unsigned)y, (unsigned)((blocks + kColumn - 1) / kColumn));

@@ -13,6 +13,12 @@ namespace rhtq {
 
 constexpr int kTile = 16;   // positions of a tile: divides every page size, so a tile lies in one page
 
+// A cache call's grid has a column of kColumn blocks of up to kBlockRows rows, and as many columns as needed, the last one whole too: up to
+// kColumn * kBlockRows row numbers lie behind the last row, and they have to be 32-bit numbers as well.
+constexpr int64_t kColumn = 32768;
+constexpr int64_t kBlockRows = 128;
+constexpr int64_t kMostRows = ((int64_t)1 << 31) - 2 * kColumn * kBlockRows;
+
 // Page of slot group `idx` of a sequence's table row, or -1 where there is none.
 RHTQ_HD int page_at(const int32_t* row, int width, int pages, int64_t idx) {
   if (idx < 0 || idx >= width) return -1;

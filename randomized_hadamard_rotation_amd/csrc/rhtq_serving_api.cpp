@@ -5,6 +5,7 @@
 #include <climits>
 
 #include "rhtq_internal.h"
+#include "rhtq_paging.h"
 #include "rhtq_serving_internal.h"
 
 namespace {
@@ -45,7 +46,7 @@ int cache_rows(const rhtq_cache_t* c, int64_t tokens, const int32_t* table, int3
   int st = check_cache(c);
   if (st == RHTQ_OK) st = check_table(width, seqs, c->page);
   if (st != RHTQ_OK) return st;
-  if (tokens < 0 || tokens > INT32_MAX - 1024 || (!starts && tokens != seqs) || c->layers != 1) return RHTQ_EINVAL;
+  if (tokens < 0 || tokens > rhtq::kMostRows || (!starts && tokens != seqs) || c->layers != 1) return RHTQ_EINVAL;
   if (c->kv_heads > 65535) return RHTQ_EUNSUPPORTED;   // a grid's limit
   if (tokens == 0) return RHTQ_OK;
   if (c->pages > 0 && !cache_pointers(c, scale_size(c->scale_dtype))) return RHTQ_EINVAL;

@@ -34,3 +34,14 @@ def test_rows_of_no_sequence_without_sequences():
     assert append(seqs=0, starts=NIL) == EINVAL          # without starts there is one row a sequence
     assert append(seqs=0, starts=FAKE, k=NIL) == EINVAL
     assert append(seqs=1, starts=FAKE, lengths=NIL) == EINVAL and read(seqs=1, starts=FAKE, table=NIL) == EINVAL
+
+
+def test_most_rows_of_a_call():
+    """2^31 - 2^23 rows: the numbers of the rows that a call's last, partly empty column of blocks stands for stay below 2^31."""
+    most = 2 ** 31 - 2 ** 23
+    assert append(tokens=most + 1, starts=FAKE) == EINVAL and read(tokens=most + 1, starts=FAKE) == EINVAL
+    assert append(tokens=most, starts=FAKE, seqs=0) == OK
+    for per in (16, 64, 128):                            # rows of a block
+        blocks = -(-most // per)
+        last = -(-blocks // 32768) * 32768 * per         # blocks in whole columns of 32768
+        assert last <= 2 ** 31 - 1
