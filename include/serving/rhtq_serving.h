@@ -125,7 +125,8 @@ int rhtq_pages_reserve(int32_t* table, int32_t width, int32_t* lengths, int32_t 
 int rhtq_pages_free(int32_t* table, int32_t width, int32_t* lengths, int32_t seqs, int32_t* refs, int32_t pages,
                     const int32_t* list, int32_t count, rhtq_stream_t stream);
 
-/* Give up the pages that a window (> 0) with its first `sinks` positions can never show again; lengths stay. */
+/* Give up the pages that a window (> 0) with its first `sinks` positions can never show again; lengths stay, and count as they do for
+ * attention. */
 int rhtq_pages_trim(int32_t* table, int32_t width, const int32_t* lengths, int32_t seqs, int32_t* refs, int32_t pages,
                     int32_t page, int32_t window, int32_t sinks, rhtq_stream_t stream);
 

@@ -118,7 +118,7 @@ __global__ __launch_bounds__(kCopy) void free_kernel(PagesArgs a) {
 
 __global__ __launch_bounds__(kCopy) void trim_kernel(PagesArgs a) {
   const int s = blockIdx.x;
-  const int64_t len = a.lengths[s];
+  const int64_t len = clamp_length(a.lengths[s], a.width, a.page);   // where attention's window lies
   for (int i = threadIdx.x; i < a.width; i += kCopy) {
     const int64_t first = (int64_t)i * a.page;
     if (first >= a.sinks && first + a.page <= len - a.window) release(a, (int64_t)s * a.width + i);

@@ -55,3 +55,24 @@ def test_rows_without_sequences(R, dim):
         R.rhtq_cache_read(cache, table, none, ints(0), 5, dtype=dtype, k_out=out[0], v_out=out[1])
         assert all((o == 0).all() for o in out)
     assert all(torch.equal(a, b) for a, b in zip(before, cache))
+
+
+# ------------------------------------------------------------------------------------------------------------ pages
+
+def held(table, pages):
+    t = table.cpu().numpy()
+    return np.bincount(t[(t >= 0) & (t < pages)], minlength=pages)
+
+
+@pytest.mark.parametrize("given", [64, 65, 1000, 2 ** 31 - 1])
+def test_trim_keeps_what_attention_sees(R, given):
+    """A length beyond the table's end counts as its end, for the window that attention takes and for the one that trim takes."""
+    say("trim, length", given)
+    page, window, sinks = 16, 20, 3
+    cache = filled(R, 8, 2, page, 64, 3)
+    table, lengths, refs = torch.tensor([[5, 2, 7, 0]], dtype=torch.int32, device="cuda"), ints(given), ints(1, 0, 1, 0, 0, 1, 0, 1)
+    q = torch.randn(1, 4, 64, device="cuda", dtype=torch.float16)
+    before = R.rhtq_paged_attention(q, cache, table, lengths, window=window, sinks=sinks)
+    R.rhtq_pages_trim(table, lengths, refs, page, window, sinks)
+    assert table.tolist() == [[5, -1, 7, 0]] and refs.tolist() == [1, 0, 0, 0, 0, 1, 0, 1]      # positions 16 .. 31 alone are behind it
+    assert torch.equal(R.rhtq_paged_attention(q, cache, table, lengths, window=window, sinks=sinks), before)
