@@ -109,13 +109,13 @@ int rhtq_paged_attention(const void* q, int in_dtype, int32_t seqs, int32_t q_he
 /*
  * Pages.  refs [pages] int32 counts the table entries that hold a page; 0 = free.  A fresh page is always the lowest free one.
  * The calls that take pages are all or nothing: *status (device int32) is 0 when done, the number of pages missing when there
- * were too few (nothing changed), or -1 when an index or an amount was invalid (nothing changed).
+ * were too few (nothing changed), or -1 when an index, an amount or a length was invalid (nothing changed).
  * workspace: rhtq_pages_workspace(pages, seqs, count) bytes, 16-byte aligned.  The cache's scales are 16-byte aligned here.
  */
 int64_t rhtq_pages_workspace(int32_t pages, int32_t seqs, int32_t count);
 
-/* Room for add[s] >= 0 more positions of every sequence: lengths[s] += add[s], fresh pages where table has none.  Positions
- * beyond width * page count as missing pages. */
+/* Room for add[s] >= 0 more positions of every sequence: lengths[s] += add[s], fresh pages where table has none (any entry outside
+ * [0, pages)).  Positions beyond width * page count as missing pages. */
 int rhtq_pages_reserve(int32_t* table, int32_t width, int32_t* lengths, int32_t seqs, int32_t* refs, int32_t pages,
                        int32_t page, const int32_t* add, int32_t* status, void* workspace, int64_t workspace_bytes,
                        rhtq_stream_t stream);

@@ -63,6 +63,9 @@ __device__ __forceinline__ int64_t list_free(const PagesArgs& a, int32_t* list, 
   return total;
 }
 
+// An entry that names no page, whatever it holds.
+__device__ __forceinline__ bool no_page(const PagesArgs& a, int32_t entry) { return (uint32_t)entry >= (uint32_t)a.pages; }
+
 // First page slot that a sequence of this length has no position in.
 __device__ __forceinline__ int64_t slots_of(int64_t length, int page) { return (length + page - 1) / page; }
 
@@ -81,7 +84,7 @@ __global__ __launch_bounds__(kPlan) void reserve_kernel(PagesArgs a) {
     }
     const int64_t need = slots_of(len + more, a.page);
     if (need > a.width) beyond += need - a.width;
-    for (int64_t i = slots_of(len, a.page); i < need && i < a.width; ++i) mine += a.table[(int64_t)s * a.width + i] < 0;
+    for (int64_t i = slots_of(len, a.page); i < need && i < a.width; ++i) mine += no_page(a, a.table[(int64_t)s * a.width + i]);
   }
   int64_t wanted, over;
   int64_t at = scan(mine, wanted);
@@ -95,7 +98,7 @@ __global__ __launch_bounds__(kPlan) void reserve_kernel(PagesArgs a) {
     const int64_t len = a.lengths[s], need = slots_of(len + a.add[s], a.page);
     for (int64_t i = slots_of(len, a.page); i < need; ++i) {
       int32_t& e = a.table[(int64_t)s * a.width + i];
-      if (e < 0) {
+      if (no_page(a, e)) {
         e = a.work[at++];
         a.refs[e] = 1;
       }
@@ -148,7 +151,7 @@ __global__ __launch_bounds__(kPlan) void fork_kernel(PagesArgs a) {
   __syncthreads();
   if (!bad)
     for (int64_t e = threadIdx.x; e < (int64_t)a.count * a.width; e += kPlan)
-      if (a.table[(int64_t)a.dst[e / a.width] * a.width + e % a.width] >= 0) bad = 1;
+      if (!no_page(a, a.table[(int64_t)a.dst[e / a.width] * a.width + e % a.width])) bad = 1;
   __syncthreads();
   if (bad) {
     if (threadIdx.x == 0) a.status[0] = -1;

@@ -76,3 +76,29 @@ def test_trim_keeps_what_attention_sees(R, given):
     R.rhtq_pages_trim(table, lengths, refs, page, window, sinks)
     assert table.tolist() == [[5, -1, 7, 0]] and refs.tolist() == [1, 0, 0, 0, 0, 1, 0, 1]      # positions 16 .. 31 alone are behind it
     assert torch.equal(R.rhtq_paged_attention(q, cache, table, lengths, window=window, sinks=sinks), before)
+
+
+@pytest.mark.parametrize("entry", [6, 7, 1 << 20, 2 ** 31 - 1, -1, -7, -2 ** 31])
+def test_entries_that_name_no_page(R, entry):
+    """Whatever an entry outside [0, pages) holds: reserve supplies the page, its rows are stored, and a fork's target counts as empty."""
+    say("entries that name no page", entry)
+    page, dim = 16, 64
+    cache = filled(R, 6, 2, page, dim, 5)
+    table = torch.full((3, 3), entry, dtype=torch.int32, device="cuda")
+    table[0, 0] = 4
+    lengths, refs = ints(16, 0, 0), ints(0, 0, 0, 0, 1, 0)
+    assert R.rhtq_pages_reserve(table, lengths, refs, ints(3, 17, 0), page).item() == 0
+    assert table.tolist() == [[4, 0, entry], [1, 2, entry], [entry] * 3]
+    assert lengths.tolist() == [19, 17, 0] and refs.tolist() == [1, 1, 1, 0, 1, 0]
+    x = torch.randn(20, 2, dim, device="cuda", dtype=torch.float16)
+    starts = ints(0, 3, 20, 20)
+    R.rhtq_cache_append(cache, x, x, table, lengths, starts)
+    k, v = R.rhtq_cache_read(cache, table, lengths, starts, 20, dtype=torch.float16)
+    # stored, not zero: a row is off by at most half a step, 1/14 of its largest rotated value, in each of 64 directions, and that value is
+    # below 5 of the row's deviations: 8 * 5 / 14 of the norm's 8
+    assert (k.float().norm(dim=-1) > 0.5 * x.float().norm(dim=-1)).all() and torch.equal(k, v)
+    assert R.rhtq_pages_fork(cache, table, lengths, refs, ints(0), ints(2)).item() == 0
+    assert table.tolist() == [[4, 0, entry], [1, 2, entry], [4, 3, -1]] and refs.tolist() == [1, 1, 1, 1, 2, 0]
+    assert R.rhtq_pages_fork(cache, table, lengths, refs, ints(0), ints(1)).item() == -1       # not empty
+    R.rhtq_pages_free(table, lengths, refs, ints(0, 1, 2))
+    assert refs.tolist() == [0] * 6
