@@ -115,7 +115,8 @@ int rhtq_paged_attention(const void* q, int in_dtype, int32_t seqs, int32_t q_he
 int64_t rhtq_pages_workspace(int32_t pages, int32_t seqs, int32_t count);
 
 /* Room for add[s] >= 0 more positions of every sequence: lengths[s] += add[s], fresh pages where table has none (any entry outside
- * [0, pages)).  Positions beyond width * page count as missing pages. */
+ * [0, pages)), also where the first new position's slot is partly filled and has lost its page: the older positions of such a slot are seen
+ * again from then on, and hold nothing until they are appended anew.  Positions beyond width * page count as missing pages. */
 int rhtq_pages_reserve(int32_t* table, int32_t width, int32_t* lengths, int32_t seqs, int32_t* refs, int32_t pages,
                        int32_t page, const int32_t* add, int32_t* status, void* workspace, int64_t workspace_bytes,
                        rhtq_stream_t stream);

@@ -66,7 +66,8 @@ __device__ __forceinline__ int64_t list_free(const PagesArgs& a, int32_t* list, 
 // An entry that names no page, whatever it holds.
 __device__ __forceinline__ bool no_page(const PagesArgs& a, int32_t entry) { return (uint32_t)entry >= (uint32_t)a.pages; }
 
-// First page slot that a sequence of this length has no position in.
+// Page slots that a sequence of this length has positions in.  The next position's slot is length / page: the last of these where that one
+// is partly filled.
 __device__ __forceinline__ int64_t slots_of(int64_t length, int page) { return (length + page - 1) / page; }
 
 __global__ __launch_bounds__(kPlan) void reserve_kernel(PagesArgs a) {
@@ -84,7 +85,8 @@ __global__ __launch_bounds__(kPlan) void reserve_kernel(PagesArgs a) {
     }
     const int64_t need = slots_of(len + more, a.page);
     if (need > a.width) beyond += need - a.width;
-    for (int64_t i = slots_of(len, a.page); i < need && i < a.width; ++i) mine += no_page(a, a.table[(int64_t)s * a.width + i]);
+    if (more > 0)
+      for (int64_t i = len / a.page; i < need && i < a.width; ++i) mine += no_page(a, a.table[(int64_t)s * a.width + i]);
   }
   int64_t wanted, over;
   int64_t at = scan(mine, wanted);
@@ -95,8 +97,9 @@ __global__ __launch_bounds__(kPlan) void reserve_kernel(PagesArgs a) {
   if (threadIdx.x == 0) a.status[0] = bad ? -1 : (int32_t)short_of;
   if (bad || short_of) return;
   for (int s = from; s < to; ++s) {
+    if (a.add[s] == 0) continue;
     const int64_t len = a.lengths[s], need = slots_of(len + a.add[s], a.page);
-    for (int64_t i = slots_of(len, a.page); i < need; ++i) {
+    for (int64_t i = len / a.page; i < need; ++i) {
       int32_t& e = a.table[(int64_t)s * a.width + i];
       if (no_page(a, e)) {
         e = a.work[at++];

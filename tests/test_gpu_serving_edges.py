@@ -102,3 +102,19 @@ def test_entries_that_name_no_page(R, entry):
     assert R.rhtq_pages_fork(cache, table, lengths, refs, ints(0), ints(1)).item() == -1       # not empty
     R.rhtq_pages_free(table, lengths, refs, ints(0, 1, 2))
     assert refs.tolist() == [0] * 6
+
+
+def test_reserve_under_a_partly_filled_slot(R):
+    """The page of the slot that the first new position falls into is missing: it is supplied.  A sequence that asks for nothing gets
+    nothing."""
+    say("reserve, partly filled slot")
+    page = 16
+    table = torch.tensor([[2, -1, -1, -1], [-1, -1, -1, -1], [-1, 3, -1, -1]], dtype=torch.int32, device="cuda")
+    lengths, refs = ints(21, 5, 20), ints(0, 0, 1, 1, 0, 0)
+    assert R.rhtq_pages_reserve(table, lengths, refs, ints(2, 0, 1), page).item() == 0
+    assert table.tolist() == [[2, 0, -1, -1], [-1, -1, -1, -1], [-1, 3, -1, -1]] and lengths.tolist() == [23, 5, 21]
+    assert refs.tolist() == [1, 0, 1, 1, 0, 0]
+    assert R.rhtq_pages_reserve(table, lengths, refs, ints(0, 30, 0), page).item() == 0
+    assert table.tolist()[1] == [1, 4, 5, -1] and lengths.tolist() == [23, 35, 21] and refs.tolist() == [1] * 6
+    assert R.rhtq_pages_reserve(table, lengths, refs, ints(9, 0, 0), page).item() == 0       # up to the slot's last position
+    assert R.rhtq_pages_reserve(table, lengths, refs, ints(1, 0, 0), page).item() == 1 and lengths.tolist() == [32, 35, 21]
