@@ -75,7 +75,8 @@ typedef struct {
 } rhtq_cache_t;
 
 /* Rotate, quantise and store k, v [tokens][kv_heads][head_dim] (row strides in elements; head_dim contiguous, every row
- * 16-byte aligned).  signs: int8 [head_dim] +-1 or NULL.  Two rows of one call must not fall on the same slot. */
+ * 16-byte aligned).  signs: int8 [head_dim] +-1 or NULL.  Two rows of one call must not fall on the same slot, nor any on a page that
+ * sequences share (rhtq_pages_reserve refuses room there). */
 int rhtq_cache_append(const rhtq_cache_t* cache, const void* k, const void* v, int in_dtype, int64_t tokens,
                       int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
                       const int32_t* table, int32_t width, const int32_t* lengths, const int32_t* starts, int32_t seqs,
@@ -116,7 +117,9 @@ int64_t rhtq_pages_workspace(int32_t pages, int32_t seqs, int32_t count);
 
 /* Room for add[s] >= 0 more positions of every sequence: lengths[s] += add[s], fresh pages where table has none (any entry outside
  * [0, pages)), also where the first new position's slot is partly filled and has lost its page: the older positions of such a slot are seen
- * again from then on, and hold nothing until they are appended anew.  Positions beyond width * page count as missing pages. */
+ * again from then on, and hold nothing until they are appended anew.  Positions beyond width * page count as missing pages.
+ * A new position on a page that another entry holds too (refs > 1) is invalid.  It comes about where lengths[s] was lowered below what
+ * sequences share: such a sequence is forked at its new length, which gives the fork a page of its own there, and freed. */
 int rhtq_pages_reserve(int32_t* table, int32_t width, int32_t* lengths, int32_t seqs, int32_t* refs, int32_t pages,
                        int32_t page, const int32_t* add, int32_t* status, void* workspace, int64_t workspace_bytes,
                        rhtq_stream_t stream);

@@ -86,7 +86,11 @@ __global__ __launch_bounds__(kPlan) void reserve_kernel(PagesArgs a) {
     const int64_t need = slots_of(len + more, a.page);
     if (need > a.width) beyond += need - a.width;
     if (more > 0)
-      for (int64_t i = len / a.page; i < need && i < a.width; ++i) mine += no_page(a, a.table[(int64_t)s * a.width + i]);
+      for (int64_t i = len / a.page; i < need && i < a.width; ++i) {
+        const int32_t e = a.table[(int64_t)s * a.width + i];
+        if (no_page(a, e)) ++mine;
+        else if (a.refs[e] > 1) bad = 1;     // new rows would overwrite another sequence's
+      }
   }
   int64_t wanted, over;
   int64_t at = scan(mine, wanted);

@@ -433,7 +433,8 @@ def _tensors(cache):
 def rhtq_pages_reserve(table, lengths, refs, add, page: int, stream=None):
     """Room for add[s] more positions of every sequence: lengths grow, and where `table` int32 [seqs][width] has no page yet the lowest
     free ones (refs int32 [pages] == 0) are taken.  All or nothing; returns a device int32 [1]: 0 done, otherwise the number of
-    pages missing, or -1 for a negative amount."""
+    pages missing, or -1 for a negative amount or a new position on a page that another sequence shares (after lengths were lowered: fork
+    the sequence at its new length and go on with the fork)."""
     seqs, width = _paging(table, lengths, refs)
     _int32(add, "add", lengths.shape)
     pages = refs.shape[0]

@@ -118,3 +118,32 @@ def test_reserve_under_a_partly_filled_slot(R):
     assert table.tolist()[1] == [1, 4, 5, -1] and lengths.tolist() == [23, 35, 21] and refs.tolist() == [1] * 6
     assert R.rhtq_pages_reserve(table, lengths, refs, ints(9, 0, 0), page).item() == 0       # up to the slot's last position
     assert R.rhtq_pages_reserve(table, lengths, refs, ints(1, 0, 0), page).item() == 1 and lengths.tolist() == [32, 35, 21]
+
+
+def test_reserve_refuses_shared_pages(R):
+    """A draft is taken back after a fork, so that the next position lies on a page the other sequence still reads: no room there.  Forked at
+    its new length the sequence goes on, and the other one's rows stay."""
+    say("reserve, shared pages")
+    page, dim = 16, 64
+    cache = filled(R, 9, 2, page, dim, 7)
+    table = torch.full((3, 3), -1, dtype=torch.int32, device="cuda")
+    lengths, refs = ints(0, 0, 0), torch.zeros(9, dtype=torch.int32, device="cuda")
+    assert R.rhtq_pages_reserve(table, lengths, refs, ints(40, 0, 0), page).item() == 0
+    assert R.rhtq_pages_fork(cache, table, lengths, refs, ints(0), ints(1)).item() == 0
+    assert refs.tolist() == [2, 2, 1, 1] + [0] * 5
+    for cut in (20, 16, 31, 0):                          # inside a shared page, at its start, at its last position, everything
+        lengths[0] = cut
+        state = [t.clone() for t in (table, lengths, refs)]
+        assert R.rhtq_pages_reserve(table, lengths, refs, ints(1, 0, 0), page).item() == -1
+        assert all(torch.equal(a, b) for a, b in zip(state, (table, lengths, refs)))
+    lengths[0] = 32                                       # the third page is its own
+    assert R.rhtq_pages_reserve(table, lengths, refs, ints(1, 1, 0), page).item() == 0
+    lengths[0] = 20
+    assert R.rhtq_pages_fork(cache, table, lengths, refs, ints(0), ints(2)).item() == 0
+    R.rhtq_pages_free(table, lengths, refs, ints(0))
+    assert R.rhtq_pages_reserve(table, lengths, refs, ints(0, 0, 1), page).item() == 0
+    rows = [t[table[1, :2].long()].clone() for t in cache]
+    x = torch.randn(3, 2, dim, device="cuda", dtype=torch.float16)
+    R.rhtq_cache_append(cache, x, x, table, lengths)
+    assert all(torch.equal(a, t[table[1, :2].long()]) for a, t in zip(rows, cache))
+    assert lengths.tolist() == [0, 41, 21] and refs.tolist() == held(table, 9).tolist()
