@@ -7,7 +7,8 @@
 //    The halves stand in the order in which lanes take them as a matrix operand (below), so they are read as they lie.
 //  - Codes become fp16 exactly: INT4 by setting them into the low mantissa bits of 1024 (two values per instruction, 1.25 instructions
 //    a value in all), E2M1 by the conversion instruction, with the E4M3 scale of a 16-block (product exact: 2 + 4 bits)
-//    or the power of two of a 32-block relative to the largest in its 128 values (exact down to 2^-22 of that one).
+//    or the power of two of a 32-block relative to the largest in its 128 values (exact down to 2^-22 of that one; a wave that meets a block
+//    further below takes its steps again with each block's power of two on the block's own sum).
 //  - v_mfma_f32_16x16x32_f16 multiplies 16 weight rows by 16 rows of halves (8 tokens, hi and lo); sums are fp32.  INT4 scales multiply
 //    the sum of their group.  y = 2^e (sum_hi + 2^-11 sum_lo).
 //
@@ -178,10 +179,12 @@ __device__ __forceinline__ void load_codes(const MatvecArgs& a, int64_t row, int
   }
 }
 
+constexpr int kFar = 22;           // E2M1 codes times 2^-22 are fp16 numbers still (subnormal ones: 0.5 * 2^-22 = 2^-23)
+
 // The scales as fp32, once they are needed.  MXFP4's powers of two: the step's largest 2^(top - 127), and the lane's block relative to it,
-// 2^(own - top), kept above 2^-126 (a block so far below another adds nothing).
+// 2^(own - top).  Returns whether the lane's block has codes that do not fit there.
 template <int MODE, bool F32>
-__device__ __forceinline__ void convert_scales(Codes& c, int q) {
+__device__ __forceinline__ bool convert_scales(Codes& c, int q) {
   if constexpr (MODE == MMX) {
     uint32_t top = 0, own = c.b[0];
 #pragma unroll
@@ -190,12 +193,14 @@ __device__ __forceinline__ void convert_scales(Codes& c, int q) {
       own = g == q ? c.b[g] : own;
     }
     c.s[0] = __builtin_amdgcn_ldexpf(1.0f, (int)top - 127);
-    c.s[1] = __builtin_amdgcn_ldexpf(1.0f, own + 126 > top ? (int)own - (int)top : -126);
+    c.s[1] = __builtin_amdgcn_ldexpf(1.0f, own + kFar > top ? (int)own - (int)top : -kFar);
+    return own + kFar < top && ((c.w[0] | c.w[1] | c.w[2] | c.w[3]) & 0x77777777u) != 0;
   } else if constexpr (MODE != MNV) {
     constexpr int PER = MODE == M128 ? 1 : (MODE == M64 ? 2 : (MODE == M32 ? 4 : 8));
 #pragma unroll
     for (int g = 0; g < PER; ++g) c.s[g] = F32 ? __uint_as_float(c.b[g]) : __half2float(__ushort_as_half((uint16_t)c.b[g]));
   }
+  return false;
 }
 
 __device__ __forceinline__ f16x2 as_f16x2(uint32_t v) { return __builtin_bit_cast(f16x2, v); }
@@ -277,6 +282,23 @@ __device__ __forceinline__ void step_into(f32x4& acc, const f16x8 (&x)[4], const
   }
 }
 
+// The same for MXFP4 blocks of any distance: block g's codes are those of lane group g, so that the others' are left out of its products.
+__device__ __forceinline__ void far_step_into(f32x4& acc, const f16x8 (&x)[4], Codes& c) {
+  const int q = (threadIdx.x & 63) >> 4;
+  const f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+  const f16x8 none = {};
+  c.s[1] = 1.0f;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    f32x4 d = z;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d = mma(x[i], q == g ? unpack<MMX>(c, i) : none, d);
+    const float s = __builtin_amdgcn_ldexpf(1.0f, (int)c.b[g] - 127);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = __builtin_fmaf(s, d[k], acc[k]);
+  }
+}
+
 __device__ __forceinline__ void store_y(const MatvecArgs& a, int64_t t, int64_t row, float v) {
   const int64_t at = t * a.rows + row;
   if (a.out_dtype == RHTQ_IN_F32) static_cast<float*>(a.y)[at] = v;
@@ -304,7 +326,7 @@ constexpr int kOwnWidth = 4096;
 // OWN: x fp32 is split by every workgroup for itself, in LDS, while its codes are on their way, which saves a launch; otherwise the halves
 // lie ready.
 template <int MODE, bool F32, bool OWN>
-__global__ __launch_bounds__(64 * kWaves) void narrow_kernel(MatvecArgs a) {
+__global__ __launch_bounds__(64 * kWaves, MODE == MMX ? 4 : 1) void narrow_kernel(MatvecArgs a) {
   __shared__ f32x4 part[kWaves][64];
   __shared__ float wave_max[kOwnTokens][kWaves];
   // operands: rows t + kOwnTokens * half of lane group q of operand i
@@ -382,12 +404,13 @@ __global__ __launch_bounds__(64 * kWaves) void narrow_kernel(MatvecArgs a) {
     load(s0);
   }
   f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  bool far = false;
   auto step = [&](int s, int k) {
     f16x8 w[4];
     if constexpr (OWN)
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[k][i] = own[16 * (s + k) + 4 * i + q][own_row];
-    convert_scales<MODE, F32>(c[k], q);
+    far |= convert_scales<MODE, F32>(c[k], q);
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = unpack<MODE>(c[k], i);
     step_into<MODE>(acc, v[k], w, c[k]);
@@ -407,6 +430,20 @@ __global__ __launch_bounds__(64 * kWaves) void narrow_kernel(MatvecArgs a) {
     for (int k = 0; k < kAhead; ++k)
       if (s + k < s1) step(s, k);
   }
+  if constexpr (MODE == MMX)
+    if (__any(far)) {
+      acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+      for (s = s0; s < s1; ++s) {
+        load_codes<MODE, F32>(a, row, s, q, c[0]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (OWN) v[0][i] = own[16 * s + 4 * i + q][own_row];
+          else v[0][i] = *reinterpret_cast<const f16x8*>(halves + (int64_t)(4 * s + i) * kFrag);
+        }
+        far_step_into(acc, v[0], c[0]);
+      }
+    }
   part[wave][lane] = acc;
   __syncthreads();
   // 128 results: row m, token 2 q + b of lane (q, m), b = 0, 1
@@ -470,6 +507,7 @@ __global__ __launch_bounds__(kWide) void wide_kernel(MatvecArgs a) {
       if (TT > 1 || tile_half == 0) *reinterpret_cast<u32x4*>(&buf[b][4 * (2 * t + tile_half) * kFrag + piece]) = stage[t];
   };
   f32x4 acc[2][TT] = {};
+  bool far = false;
   Codes next[2];
   fetch(s0);
 #pragma unroll
@@ -487,7 +525,7 @@ __global__ __launch_bounds__(kWide) void wide_kernel(MatvecArgs a) {
     f16x8 w[2][4];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      convert_scales<MODE, F32>(c[r], q);
+      far |= convert_scales<MODE, F32>(c[r], q);
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[r][i] = unpack<MODE>(c[r], i);
     }
@@ -502,6 +540,24 @@ __global__ __launch_bounds__(kWide) void wide_kernel(MatvecArgs a) {
     if (s + 1 < s1) put(b ^ 1);
     __syncthreads();
   }
+  if constexpr (MODE == MMX)
+    if (__any(far))                    // no barrier in here: the waves' rows differ
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        acc[0][t] = acc[1][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+        for (int s = s0; s < s1; ++s) {
+          f16x8 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            v[i] = *reinterpret_cast<const f16x8*>(halves + (((tile0 + t) * steps + s) * 4 + i) * kFrag + 16 * lane);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            load_codes<MODE, F32>(a, row[r], s, q, next[r]);
+            far_step_into(acc[r][t], v, next[r]);
+          }
+        }
+      }
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     const int64_t at = row0 + 16 * r + m;

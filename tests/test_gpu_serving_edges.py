@@ -147,3 +147,45 @@ def test_reserve_refuses_shared_pages(R):
     R.rhtq_cache_append(cache, x, x, table, lengths)
     assert all(torch.equal(a, t[table[1, :2].long()]) for a, t in zip(rows, cache))
     assert lengths.tolist() == [0, 41, 21] and refs.tolist() == held(table, 9).tolist()
+
+
+# ----------------------------------------------------------------------------------------------------------- matvec
+
+def product_bound(x, w, n):
+    """Allowed |error| before the output's rounding, of x as carried: 2^-22 of each value and, where it is not 0, 2^-35 of the row's largest;
+    and of fp32 sums: n / 16 + 64 additions one after another."""
+    carried = 2.0 ** -22 * np.abs(x) + 2.0 ** -35 * np.abs(x).max(-1, keepdims=True) * (x != 0)
+    return carried @ np.abs(w).T + (n / 16 + 64) * 2.0 ** -24 * (np.abs(x) @ np.abs(w).T)
+
+
+@pytest.mark.parametrize("tokens", [1, 2, 3, 7, 16, 30, 61])
+@pytest.mark.parametrize("n,rows", [(32, 3), (96, 18), (512, 40), (1376, 300)])
+def test_mxfp4_blocks_far_apart(R, n, rows, tokens):
+    """Block scales of a row up to 2^60 apart, x zero in the larger blocks of every other token: the smaller blocks' sum is an ordinary
+    number and is returned.  Some rows have scales close together, some all-zero blocks with the smallest scale, as rhtq_forward leaves
+    them."""
+    say("mxfp4 blocks far apart", n, rows, tokens)
+    rs = np.random.RandomState(n + tokens)
+    blocks = n // 32
+    codes = rs.randint(0, 16, (rows, n))
+    e = rs.randint(-3, 4, (rows, blocks))
+    large = rs.rand(rows, blocks) < 0.3
+    large[:, 1::5] = True
+    distance = rs.choice([15, 22, 23, 24, 30, 60], (rows, 1))
+    distance[::3] = 0
+    e = e + np.where(large, distance, 0)
+    if blocks > 3:
+        codes.reshape(rows, blocks, 32)[:, 3], e[:, 3] = 0, -127
+    p, s = O.pack_nibbles(codes).astype(np.uint8), (e + 127).astype(np.uint8)
+    w = O.dequantize(p, s, "mxfp4", 32, None)
+    x = rs.randn(tokens, n)
+    x.reshape(tokens, blocks, 32)[::2, large.any(0)] = 0
+    if large.any(0).all():
+        x[::2, :5] = 1.0
+    x = torch.from_numpy(x).float()
+    y = R.rhtq_matvec(torch.from_numpy(p).cuda(), torch.from_numpy(s).cuda(), x.cuda(), fmt="mxfp4", rotated=True).double().cpu().numpy()
+    x = x.double().numpy()
+    ref = x @ w.T
+    allowed = product_bound(x, w, n) * (1 + 2.0 ** -24) + 2.0 ** -24 * np.abs(ref)
+    bad = ~(np.abs(y - ref) <= allowed)
+    assert not bad.any(), f"{bad.sum()} of {bad.size} off, worst {np.max(np.abs(y - ref) / (allowed + 1e-300)):.3g} x allowed"
