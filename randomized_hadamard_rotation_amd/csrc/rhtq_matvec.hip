@@ -306,10 +306,11 @@ __device__ __forceinline__ void store_y(const MatvecArgs& a, int64_t t, int64_t 
   else static_cast<uint16_t*>(a.y)[at] = (uint16_t)to16<RHTQ_IN_F16>(v);
 }
 
-// Both halves of a token, times its power of two and the tensor scale.
+// Both halves of a token, times the tensor scale and its power of two, in that order: with the power first, x near fp32's largest values
+// would overflow before the tensor scale brings the sum back.
 __device__ __forceinline__ float whole(const MatvecArgs& a, int exponent, float hi, float lo) {
-  const float v = __builtin_amdgcn_ldexpf(__builtin_fmaf(lo, 1.0f / 2048.0f, hi), exponent);
-  return a.tensor_scale ? v * a.tensor_scale[0] : v;
+  const float v = __builtin_fmaf(lo, 1.0f / 2048.0f, hi);
+  return __builtin_amdgcn_ldexpf(a.tensor_scale ? v * a.tensor_scale[0] : v, exponent);
 }
 
 // ---- few tokens: one tile of 16 rows per workgroup, k split over its waves -----------------------------------------------------

@@ -189,3 +189,24 @@ def test_mxfp4_blocks_far_apart(R, n, rows, tokens):
     allowed = product_bound(x, w, n) * (1 + 2.0 ** -24) + 2.0 ** -24 * np.abs(ref)
     bad = ~(np.abs(y - ref) <= allowed)
     assert not bad.any(), f"{bad.sum()} of {bad.size} off, worst {np.max(np.abs(y - ref) / (allowed + 1e-300)):.3g} x allowed"
+
+
+@pytest.mark.parametrize("tokens", [1, 4, 9])
+@pytest.mark.parametrize("size,tensor_scale", [(1e35, 1e-4), (1e37, 1e-5), (1e-34, 1e4), (1.0, 1e-30)])
+def test_nvfp4_tensor_scale_keeps_the_range(R, tokens, size, tensor_scale):
+    """x near the ends of fp32 with a tensor scale that brings the result back: nothing overflows or vanishes on the way."""
+    say("nvfp4 tensor scale", tokens, size, tensor_scale)
+    n, rows = 512, 24
+    rs = np.random.RandomState(tokens)
+    p = O.pack_nibbles(rs.randint(0, 16, (rows, n))).astype(np.uint8)
+    s = O.e4m3_encode(np.exp(2 * rs.rand(rows, n // 16) - 1)).astype(np.uint8)
+    ts = np.float32(tensor_scale)
+    w = O.dequantize(p, s, "nvfp4", 16, ts)
+    x = torch.from_numpy(rs.randn(tokens, n) * size).float()
+    y = R.rhtq_matvec(torch.from_numpy(p).cuda(), torch.from_numpy(s).cuda(), x.cuda(), fmt="nvfp4", rotated=True,
+                      tensor_scale=torch.tensor([float(ts)], device="cuda")).double().cpu().numpy()
+    x = x.double().numpy()
+    ref = x @ w.T
+    # as above, the tensor scale's product and the output besides: 2^-24 each; results are normal fp32 numbers
+    allowed = product_bound(x, w, n) * (1 + 2.0 ** -23) + 2.0 ** -23 * np.abs(ref)
+    assert np.abs(ref).max() < 1e38 and (np.abs(y - ref) <= allowed).all(), f"{np.max(np.abs(y - ref) / allowed):.3g} x allowed"
