@@ -37,7 +37,7 @@ int rhtq_serving_version(void);
  *   y_out      [tokens][rows] in out_dtype (RHTQ_IN_BF16, RHTQ_IN_F16 or RHTQ_IN_F32)
  *   workspace  rhtq_matvec_workspace(...) bytes, 16-byte aligned
  * n: a multiple of 32 up to 2^20 (with rotated == 0 also one that rhtq_rotate or its blocked form takes).
- * rows: any number, tokens up to 2^20 (0: nothing to do).  Sums are in fp32; R x is carried to 22 bits, and to
+ * rows up to 2^31 - 1024, tokens up to 2^20 (0: nothing to do).  Sums are in fp32; R x is carried to 22 bits, and to
  * 2^-35 of the largest value of its row.
  * packed must be 16-byte aligned, x and y_out 16 bytes, scales to their element.
  */

@@ -323,6 +323,7 @@ constexpr int kAhead = 4;          // steps whose codes and operands are in flig
 // for 4096 x 4096 and 24.3 instead of 28.1 for 24576 x 4096 (rotation included); with four, 12.9 instead of 12.1 and 22.1 instead of 19.8.
 constexpr int kOwnTokens = 2;
 constexpr int kOwnWidth = 4096;
+constexpr int64_t kAcross = 1 << 22;   // row tiles in a grid's x, the rest in y: x times its 512 threads stays below 2^32
 
 // OWN: x fp32 is split by every workgroup for itself, in LDS, while its codes are on their way, which saves a launch; otherwise the halves
 // lie ready.
@@ -334,7 +335,8 @@ __global__ __launch_bounds__(64 * kWaves, MODE == MMX ? 4 : 1) void narrow_kerne
   __shared__ __attribute__((aligned(16))) f16x8 own[OWN ? kOwnWidth / 8 : 1][2 * kOwnTokens];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, q = lane >> 4;
-  const int64_t row0 = (int64_t)blockIdx.x * 16;
+  const int64_t row0 = (blockIdx.x + blockIdx.y * kAcross) * 16;
+  if (row0 >= a.rows) return;
   const int64_t row = row0 + m < a.rows ? row0 + m : a.rows - 1;
   const int steps = (a.n + kStep - 1) / kStep;
   const int s0 = steps * wave / kWaves, s1 = steps * (wave + 1) / kWaves;
@@ -595,7 +597,8 @@ constexpr int kNarrowTokens = 4;
 template <int MODE, bool F32>
 hipError_t launch_mode(int x_dtype, const MatvecArgs& a, hipStream_t s) {
   const unsigned padded = (unsigned)matvec_padded(a.tokens);
-  const dim3 tiles16((unsigned)((a.rows + 15) / 16));
+  const int64_t all16 = (a.rows + 15) / 16;
+  const dim3 tiles16((unsigned)(all16 < kAcross ? all16 : kAcross), (unsigned)((all16 + kAcross - 1) / kAcross));
   if (x_dtype == RHTQ_IN_F32 && a.tokens <= kOwnTokens && a.n <= kOwnWidth) {
     hipLaunchKernelGGL((narrow_kernel<MODE, F32, true>), tiles16, dim3(64 * kWaves), 0, s, a);
     return hipGetLastError();

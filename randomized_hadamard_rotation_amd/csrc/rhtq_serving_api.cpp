@@ -117,7 +117,7 @@ int rhtq_serving_version(void) { return RHTQ_SERVING_VERSION; }
 
 // The operands of x, an exponent for each padded token, the sums of split k, and the rotated rows.
 int64_t rhtq_matvec_workspace(int64_t tokens, int32_t n, int64_t rows) {
-  if (tokens <= 0 || n <= 0 || rows <= 0 || tokens > kMostTokens || rows > INT32_MAX || n > (1 << 20)) return 0;
+  if (tokens <= 0 || n <= 0 || rows <= 0 || tokens > kMostTokens || rows > rhtq::kMostWeightRows || n > (1 << 20)) return 0;
   const int64_t parts = rhtq::matvec_splits(tokens, n, rows);
   return rhtq::matvec_halves_bytes(tokens, n) + round16(4 * rhtq::matvec_padded(tokens)) +
          (parts > 1 ? round16(4 * parts * tokens * rows) : 0) + 4 * tokens * n;
@@ -138,7 +138,7 @@ int rhtq_matvec(const void* x, int in_dtype, int64_t tokens, int32_t n, int32_t 
   } else if (group != 32 || scale_dtype != RHTQ_SCALE_E8M0) {
     return RHTQ_EUNSUPPORTED;
   }
-  if (tokens > kMostTokens || rows > (int64_t)INT32_MAX) return RHTQ_EINVAL;
+  if (tokens > kMostTokens || rows > rhtq::kMostWeightRows) return RHTQ_EINVAL;
   if (!rotated) {
     // the rotation's own checks of n and block, with no rows: nothing is enqueued
     const int st = block == n ? rhtq_rotate(x, in_dtype, 0, n, signs, nullptr, stream)

@@ -88,6 +88,7 @@ struct MatvecArgs {
   int32_t k_splits;
 };
 
+constexpr int64_t kMostWeightRows = ((int64_t)1 << 31) - 1024;   // blocks of 256 rows, 512 threads each: below 2^32 threads
 int64_t matvec_padded(int64_t tokens);
 int32_t matvec_splits(int64_t tokens, int32_t n, int64_t rows);
 int64_t matvec_halves_bytes(int64_t tokens, int32_t n);

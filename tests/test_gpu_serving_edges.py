@@ -210,3 +210,21 @@ def test_nvfp4_tensor_scale_keeps_the_range(R, tokens, size, tensor_scale):
     # as above, the tensor scale's product and the output besides: 2^-24 each; results are normal fp32 numbers
     allowed = product_bound(x, w, n) * (1 + 2.0 ** -23) + 2.0 ** -23 * np.abs(ref)
     assert np.abs(ref).max() < 1e38 and (np.abs(y - ref) <= allowed).all(), f"{np.max(np.abs(y - ref) / allowed):.3g} x allowed"
+
+
+@pytest.mark.parametrize("tokens", [1, 3, 5])
+def test_rows_beyond_one_grid_row(R, tokens):
+    """More row tiles than a grid's x takes at 512 threads each (2^27 rows)."""
+    say("matvec rows", tokens)
+    rows, n = 2 ** 27 + 2 ** 20 + 5, 32
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    p = torch.randint(0, 256, (rows, n // 2), dtype=torch.uint8, device="cuda", generator=g)
+    s = torch.ones((rows, 1), dtype=torch.float16, device="cuda")
+    x = torch.randint(-3, 4, (tokens, n), device="cuda", generator=g).to(torch.bfloat16)
+    y = R.rhtq_matvec(p, s, x, scale_dtype="f16", rotated=True, out_dtype=torch.float32)
+    for from_ in (0, 2 ** 26 - 40, 2 ** 27 - 40, 2 ** 27 + 77, rows - 100):
+        c = O.unpack_nibbles(p[from_:from_ + 100].cpu().numpy(), signed=True).astype(np.float64)
+        # whole numbers, exact in fp32
+        assert np.array_equal(y[:, from_:from_ + 100].double().cpu().numpy(), x.double().cpu().numpy() @ c.T), from_
+    del p, s, y
+    torch.cuda.empty_cache()

@@ -45,3 +45,11 @@ def test_most_rows_of_a_call():
         blocks = -(-most // per)
         last = -(-blocks // 32768) * 32768 * per         # blocks in whole columns of 32768
         assert last <= 2 ** 31 - 1
+
+
+def test_most_rows_of_weights():
+    most = 2 ** 31 - 1024
+    call = lambda rows: R.lib.rhtq_matvec(FAKE, 0, 1, 32, 32, NIL, 1, FAKE, FAKE, NIL, rows, 0, 0, 0, FAKE, 0, NIL, 0, NIL)  # noqa: E731
+    assert call(most + 1) == EINVAL and R.lib.rhtq_matvec_workspace(1, 32, most + 1) == 0
+    assert R.lib.rhtq_matvec_workspace(1, 32, most) > 0 and R.lib.rhtq_matvec_workspace(300, 32, most) > 0
+    assert -(-most // 256) * 512 < 2 ** 32               # work items along a grid's x
