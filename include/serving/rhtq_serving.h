@@ -54,8 +54,8 @@ int rhtq_matvec(const void* x, int in_dtype, int64_t tokens, int32_t n, int32_t 
  * power of two, 16 to 256.  Position p of a sequence lies in page table[seq][p / page], slot p % page;
  * `table` is [seqs][width] int32.  An entry outside [0, pages) is no page: its positions are not stored, read as
  * zero and seen by no query.  A length beyond width * page counts as width * page, a negative one as 0.
- * Limits: width * page below 2^31 - 256 and up to 2^31 - 2^23 rows a call (RHTQ_EINVAL beyond); 65535 sequences of a query call, 65535
- * key-value heads (RHTQ_EUNSUPPORTED beyond).
+ * Limits: width * page below 2^31 - 256 and up to 2^31 - 2^23 rows a call (RHTQ_EINVAL beyond); 65535 sequences and 2^26 - 64 query
+ * heads of them all in a query call, 65535 key-value heads (RHTQ_EUNSUPPORTED beyond).
  *
  * The `tokens` new rows belong to sequences by `starts` [seqs+1], ascending from 0: rows starts[s] .. starts[s+1]-1
  * are the last positions of sequence s, up to lengths[s]-1 (lengths count them already).  starts NULL: one row

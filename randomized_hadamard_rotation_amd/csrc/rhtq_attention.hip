@@ -466,9 +466,9 @@ hipError_t launch_te(const AttentionArgs& a, hipStream_t s) {
 }
 
 // No page at all: no position is visible.
+constexpr int64_t kZeroBlocks = 1 << 16;
 __global__ __launch_bounds__(256) void zero_kernel(uint32_t* out, int64_t words) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i < words) out[i] = 0;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < words; i += (int64_t)kZeroBlocks * 256) out[i] = 0;
 }
 
 template <int T>
@@ -506,7 +506,8 @@ int32_t attention_splits(int32_t seqs, int32_t q_heads, int32_t kv_heads, int32_
 hipError_t launch_paged_attention(int dtype, const AttentionArgs& a, hipStream_t s) {
   if (a.pages == 0 || a.width == 0) {
     const int64_t words = (int64_t)a.seqs * a.q_heads * a.head_dim / 2;
-    hipLaunchKernelGGL(zero_kernel, dim3((unsigned)((words + 255) / 256)), dim3(256), 0, s, static_cast<uint32_t*>(a.out), words);
+    const int64_t blocks = (words + 255) / 256 < kZeroBlocks ? (words + 255) / 256 : kZeroBlocks;
+    hipLaunchKernelGGL(zero_kernel, dim3((unsigned)blocks), dim3(256), 0, s, static_cast<uint32_t*>(a.out), words);
     return hipGetLastError();
   }
   if (dtype == RHTQ_IN_BF16) return launch_t<RHTQ_IN_BF16>(a, s);

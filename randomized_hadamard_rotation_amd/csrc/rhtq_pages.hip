@@ -17,6 +17,7 @@ namespace {
 constexpr int kPlan = 1024;
 constexpr int kCopy = 256;
 constexpr int kCopyBlocks = 4096;      // most workgroups of a copy; they stride over the rest
+constexpr int kSeqBlocks = 1 << 20;    // and of a kernel with one workgroup a sequence: a grid holds fewer than 2^32 threads along x
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
 // Sum over the workgroup before this thread (exclusive) and in all; every thread calls it.
@@ -120,18 +121,21 @@ __device__ __forceinline__ void release(const PagesArgs& a, int64_t entry) {
 }
 
 __global__ __launch_bounds__(kCopy) void free_kernel(PagesArgs a) {
-  const int s = a.src[blockIdx.x];
-  if ((uint32_t)s >= (uint32_t)a.seqs) return;
-  for (int i = threadIdx.x; i < a.width; i += kCopy) release(a, (int64_t)s * a.width + i);
-  if (threadIdx.x == 0) a.lengths[s] = 0;
+  for (int64_t k = blockIdx.x; k < a.count; k += kSeqBlocks) {
+    const int s = a.src[k];
+    if ((uint32_t)s >= (uint32_t)a.seqs) continue;
+    for (int i = threadIdx.x; i < a.width; i += kCopy) release(a, (int64_t)s * a.width + i);
+    if (threadIdx.x == 0) a.lengths[s] = 0;
+  }
 }
 
 __global__ __launch_bounds__(kCopy) void trim_kernel(PagesArgs a) {
-  const int s = blockIdx.x;
-  const int64_t len = clamp_length(a.lengths[s], a.width, a.page);   // where attention's window lies
-  for (int i = threadIdx.x; i < a.width; i += kCopy) {
-    const int64_t first = (int64_t)i * a.page;
-    if (first >= a.sinks && first + a.page <= len - a.window) release(a, (int64_t)s * a.width + i);
+  for (int64_t s = blockIdx.x; s < a.seqs; s += kSeqBlocks) {
+    const int64_t len = clamp_length(a.lengths[s], a.width, a.page);   // where attention's window lies
+    for (int i = threadIdx.x; i < a.width; i += kCopy) {
+      const int64_t first = (int64_t)i * a.page;
+      if (first >= a.sinks && first + a.page <= len - a.window) release(a, s * a.width + i);
+    }
   }
 }
 
@@ -314,12 +318,12 @@ hipError_t launch_pages_reserve(const PagesArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_pages_free(const PagesArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(free_kernel, dim3((unsigned)a.count), dim3(kCopy), 0, s, a);
+  hipLaunchKernelGGL(free_kernel, dim3((unsigned)(a.count < kSeqBlocks ? a.count : kSeqBlocks)), dim3(kCopy), 0, s, a);
   return hipGetLastError();
 }
 
 hipError_t launch_pages_trim(const PagesArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(trim_kernel, dim3((unsigned)a.seqs), dim3(kCopy), 0, s, a);
+  hipLaunchKernelGGL(trim_kernel, dim3((unsigned)(a.seqs < kSeqBlocks ? a.seqs : kSeqBlocks)), dim3(kCopy), 0, s, a);
   return hipGetLastError();
 }
 

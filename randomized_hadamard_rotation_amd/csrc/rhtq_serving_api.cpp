@@ -16,6 +16,7 @@ int from_hip(hipError_t e) { return e == hipSuccess ? RHTQ_OK : RHTQ_EHIP; }
 int log2_of(int32_t v) { return 31 - __builtin_clz((unsigned)v); }
 bool in_type(int t) { return t == RHTQ_IN_BF16 || t == RHTQ_IN_F16 || t == RHTQ_IN_F32; }
 constexpr int64_t kMostTokens = 1 << 20;
+constexpr int64_t kMostQueries = ((int64_t)1 << 26) - 64;   // heads of all sequences: a join's 64 threads each stay below 2^32
 int64_t round16(int64_t v) { return (v + 15) & ~(int64_t)15; }
 uintptr_t scale_size(int t) { return t == RHTQ_SCALE_F32 ? 4 : (t == RHTQ_SCALE_F16 ? 2 : 1); }
 
@@ -244,7 +245,7 @@ int rhtq_paged_attention(const void* q, int in_dtype, int32_t seqs, int32_t q_he
   if (seqs == 0) return RHTQ_OK;
   const int32_t splits = rhtq::attention_splits(seqs, q_heads, cache->kv_heads, width, cache->page, window, sinks);
   if (seqs > 65535 || (int64_t)cache->kv_heads * rhtq::attention_head_tiles(q_heads / cache->kv_heads) > 65535 ||
-      (int64_t)seqs * q_heads * splits > INT32_MAX)
+      (int64_t)seqs * q_heads * splits > INT32_MAX || (int64_t)seqs * q_heads > kMostQueries)
     return RHTQ_EUNSUPPORTED;   // a grid's limits
   if (!q || !out || !lengths || !aligned(q, 16) || !aligned(out, 16) || !aligned(lengths, 4) || !aligned(k_signs, 4) ||
       !aligned(v_signs, 4))

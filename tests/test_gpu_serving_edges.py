@@ -228,3 +228,19 @@ def test_rows_beyond_one_grid_row(R, tokens):
         assert np.array_equal(y[:, from_:from_ + 100].double().cpu().numpy(), x.double().cpu().numpy() @ c.T), from_
     del p, s, y
     torch.cuda.empty_cache()
+
+
+def test_more_sequences_than_workgroups(R):
+    """Free and trim over more sequences than a grid has workgroups, the last ones included."""
+    say("more sequences than workgroups")
+    seqs, pages, page = 2 ** 24 + 3, 9, 16
+    table = torch.full((seqs, 2), -1, dtype=torch.int32, device="cuda")
+    lengths, refs = torch.zeros(seqs, dtype=torch.int32, device="cuda"), torch.zeros(pages, dtype=torch.int32, device="cuda")
+    for i, s in enumerate((0, 2 ** 20 + 1, 2 ** 24, seqs - 1)):
+        table[s, 0], table[s, 1], lengths[s] = 2 * i, 2 * i + 1, 32
+    refs[:8] = 1
+    R.rhtq_pages_trim(table, lengths, refs, page, window=16)
+    assert refs.tolist() == [0, 1] * 4 + [0] and held(table, pages).tolist() == refs.tolist()
+    every = torch.arange(seqs, dtype=torch.int32, device="cuda")
+    R.rhtq_pages_free(table, lengths, refs, every)
+    assert refs.tolist() == [0] * 9 and (table == -1).all() and (lengths == 0).all()

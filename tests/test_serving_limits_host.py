@@ -53,3 +53,11 @@ def test_most_rows_of_weights():
     assert call(most + 1) == EINVAL and R.lib.rhtq_matvec_workspace(1, 32, most + 1) == 0
     assert R.lib.rhtq_matvec_workspace(1, 32, most) > 0 and R.lib.rhtq_matvec_workspace(300, 32, most) > 0
     assert -(-most // 256) * 512 < 2 ** 32               # work items along a grid's x
+
+
+def test_most_queries_of_a_call():
+    """2^26 - 64 query heads over all sequences: 64 threads each in the kernel that joins parts."""
+    call = lambda seqs, heads: R.lib.rhtq_paged_attention(NIL, 0, seqs, heads, 8, 8, cache(), FAKE, 3, FAKE, NIL, NIL, 0.1, 0, 0, FAKE, FAKE,  # noqa: E731
+                                                          1 << 40, NIL)
+    assert call(32768, 2048) == EUNS and call(65535, 1026) == EUNS
+    assert call(65535, 1022) == EINVAL                   # in range: refused for q's null pointer only
