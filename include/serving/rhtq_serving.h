@@ -39,7 +39,7 @@ int rhtq_serving_version(void);
  * n: a multiple of 32 up to 2^20 (with rotated == 0 also one that rhtq_rotate or its blocked form takes).
  * rows up to 2^31 - 1024, tokens up to 2^20 (0: nothing to do).  Sums are in fp32; R x is carried to 22 bits, and to
  * 2^-35 of the largest value of its row.
- * packed must be 16-byte aligned, x and y_out 16 bytes, scales to their element.
+ * packed must be 16-byte aligned, x, y_out and signs 16 bytes, scales to their element (NVFP4: 2 bytes).
  */
 int64_t rhtq_matvec_workspace(int64_t tokens, int32_t n, int64_t rows);
 int rhtq_matvec(const void* x, int in_dtype, int64_t tokens, int32_t n, int32_t block, const int8_t* signs,
@@ -49,7 +49,8 @@ int rhtq_matvec(const void* x, int in_dtype, int64_t tokens, int32_t n, int32_t 
 
 /*
  * The cache.  One layer's keys (and, apart, its values) lie as
- *   codes   [pages][kv_heads][page][head_dim/2] bytes, scales [pages][kv_heads][page] fp32 or fp16,
+ *   codes   [pages][kv_heads][page][head_dim/2] bytes (16-byte aligned), scales [pages][kv_heads][page] fp32 or fp16 (aligned to their
+ *           element, for attention to two, for page calls to 16 bytes),
  * each row an INT4 row of rhtq_forward with one scale (group = head_dim).  head_dim 64, 128 or 256; page a
  * power of two, 16 to 256.  Position p of a sequence lies in page table[seq][p / page], slot p % page;
  * `table` is [seqs][width] int32.  An entry outside [0, pages) is no page: its positions are not stored, read as
@@ -111,7 +112,7 @@ int rhtq_paged_attention(const void* q, int in_dtype, int32_t seqs, int32_t q_he
  * Pages.  refs [pages] int32 counts the table entries that hold a page; 0 = free.  A fresh page is always the lowest free one.
  * The calls that take pages are all or nothing: *status (device int32) is 0 when done, the number of pages missing when there
  * were too few (nothing changed), or -1 when an index, an amount or a length was invalid (nothing changed).
- * workspace: rhtq_pages_workspace(pages, seqs, count) bytes, 16-byte aligned.  The cache's scales are 16-byte aligned here.
+ * workspace: rhtq_pages_workspace(pages, seqs, count) bytes, 16-byte aligned.
  */
 int64_t rhtq_pages_workspace(int32_t pages, int32_t seqs, int32_t count);
 

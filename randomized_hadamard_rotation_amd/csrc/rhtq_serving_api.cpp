@@ -148,7 +148,8 @@ int rhtq_matvec(const void* x, int in_dtype, int64_t tokens, int32_t n, int32_t 
   }
   if (tokens == 0 || rows == 0) return RHTQ_OK;
   if (!x || !packed || !scales || !y_out || (fmt == RHTQ_FMT_NVFP4 && !tensor_scale)) return RHTQ_EINVAL;
-  if (!aligned(x, 16) || !aligned(packed, 16) || !aligned(y_out, 16) || !aligned(scales, scale_size(scale_dtype)) ||
+  const uintptr_t scale_alignment = fmt == RHTQ_FMT_NVFP4 ? 2 : scale_size(scale_dtype);   // E4M3 bytes are loaded in pairs
+  if (!aligned(x, 16) || !aligned(packed, 16) || !aligned(y_out, 16) || !aligned(scales, scale_alignment) ||
       !aligned(tensor_scale, 4) || (!rotated && !aligned(signs, 16)))
     return RHTQ_EINVAL;
   if (!workspace_ok(workspace, workspace_bytes, rhtq_matvec_workspace(tokens, n, rows))) return RHTQ_EINVAL;
@@ -251,7 +252,7 @@ int rhtq_paged_attention(const void* q, int in_dtype, int32_t seqs, int32_t q_he
       !aligned(v_signs, 4))
     return RHTQ_EINVAL;
   if (width > 0 && (!table || !aligned(table, 4))) return RHTQ_EINVAL;
-  if (cache->pages > 0 && !cache_pointers(cache, scale_size(cache->scale_dtype))) return RHTQ_EINVAL;
+  if (cache->pages > 0 && !cache_pointers(cache, 2 * scale_size(cache->scale_dtype))) return RHTQ_EINVAL;   // loaded in pairs
   const int64_t need =
       rhtq_paged_attention_workspace(seqs, q_heads, cache->kv_heads, cache->head_dim, width, cache->page, window, sinks);
   if (!workspace_ok(workspace, workspace_bytes, need)) return RHTQ_EINVAL;

@@ -1,12 +1,13 @@
 """CPU: calls at the edges of what the serving header allows, answered or refused on the host before any HIP call."""
 import ctypes
-
-import pytest
-import torch
+import os
+import subprocess
+import sys
 
 import randomized_hadamard_rotation_amd as R
 from randomized_hadamard_rotation_amd import serving
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 FAKE, NIL = 0x100000, None       # never dereferenced: every call below is refused or has nothing to do
 EINVAL, EUNS, OK = R.RHTQ_EINVAL, R.RHTQ_EUNSUPPORTED, R.RHTQ_OK
 
@@ -61,3 +62,28 @@ def test_most_queries_of_a_call():
                                                           1 << 40, NIL)
     assert call(32768, 2048) == EUNS and call(65535, 1026) == EUNS
     assert call(65535, 1022) == EINVAL                   # in range: refused for q's null pointer only
+
+
+def test_scales_that_are_loaded_in_pairs():
+    """NVFP4's bytes and attention's scales are refused at odd places; others are taken one by one.  The launch hook answers RHTQ_EHIP for a
+    call that passes its checks, and enqueues nothing."""
+    code = """
+import sys
+sys.path.insert(0, {tests!r})
+import test_serving_limits_host as T
+R, F, N = T.R, T.FAKE, None
+mv = lambda scales, fmt, group, sd: R.lib.rhtq_matvec(F, 0, 1, 32, 32, N, 1, F, scales, F, 4, fmt, group, sd, F, 0, F, 1 << 40, N)
+assert mv(F + 1, R.RHTQ_FMT_NVFP4, 16, R.RHTQ_SCALE_E4M3) == T.EINVAL
+assert mv(F + 2, R.RHTQ_FMT_NVFP4, 16, R.RHTQ_SCALE_E4M3) == R.RHTQ_EHIP
+assert mv(F + 1, R.RHTQ_FMT_MXFP4, 32, R.RHTQ_SCALE_E8M0) == R.RHTQ_EHIP
+at = lambda **kw: R.lib.rhtq_paged_attention(F, 0, 4, 8, 1024, 128, T.cache(**kw), F, 9, F, N, N, 0.1, 0, 0, F, F, 1 << 40, N)
+f32 = R.RHTQ_SCALE_F32
+for kw in (dict(k_scales=F + 2), dict(v_scales=F + 2), dict(k_scales=F + 4, scale_dtype=f32), dict(v_scales=F + 4, scale_dtype=f32)):
+    assert at(**kw) == T.EINVAL, kw
+    assert T.append(T.cache(**kw)) == R.RHTQ_EHIP, kw
+for kw in (dict(), dict(k_scales=F + 4), dict(v_scales=F + 8, scale_dtype=f32)):
+    assert at(**kw) == R.RHTQ_EHIP, kw
+""".format(tests=os.path.dirname(os.path.abspath(__file__)))
+    env = dict(os.environ, RHTQ_TEST_FAIL_LAUNCH="1", PYTHONPATH=ROOT)
+    r = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr[-2000:]
