@@ -261,13 +261,15 @@ def _rows_of(cache, table, lengths, starts, tokens):
 
 
 def _row_strides(x):
-    """x with rows that start on 16 bytes (a copy where they do not), and its strides in elements."""
+    """x with rows that start on 16 bytes (a copy where they do not), and its strides in elements; 0 along an axis of one entry, whose stride
+    may be anything."""
     per16 = 16 // x.element_size()
-    if x.stride(2) != 1 or x.stride(0) % per16 or x.stride(1) % per16 or x.data_ptr() % 16:
-        x = x.contiguous()
-        if x.data_ptr() % 16:
-            x = x.clone()
-    return x
+    tokens, heads, dim = x.shape
+    of_token = x.stride(0) if tokens > 1 else 0
+    of_head = x.stride(1) if heads > 1 else 0
+    if x.stride(2) != 1 or of_token % per16 or of_head % per16 or x.data_ptr() % 16:
+        return x.clone(memory_format=torch.contiguous_format), heads * dim, dim
+    return x, of_token, of_head
 
 
 def rhtq_cache_append(cache: RhtqCache, k, v, table, lengths, starts=None, k_signs=None, v_signs=None, stream=None):
@@ -289,11 +291,11 @@ def rhtq_cache_append(cache: RhtqCache, k, v, table, lengths, starts=None, k_sig
     on = _On(index)
     try:
         ks, vs = _signs(k_signs, dim, k), _signs(v_signs, dim, k)
-        kc, vc = _row_strides(k), _row_strides(v)
+        (kc, k_token, k_head), (vc, v_token, v_head) = _row_strides(k), _row_strides(v)
         if stream is not None:
             on.follow(stream)
-        _check(lib.rhtq_cache_append(c[0], kc.data_ptr(), vc.data_ptr(), in_type, tokens, kc.stride(0), kc.stride(1),
-                                     vc.stride(0), vc.stride(1), table.data_ptr(), width, lengths.data_ptr(), _p(starts), seqs,
+        _check(lib.rhtq_cache_append(c[0], kc.data_ptr(), vc.data_ptr(), in_type, tokens, k_token, k_head,
+                                     v_token, v_head, table.data_ptr(), width, lengths.data_ptr(), _p(starts), seqs,
                                      _p(ks), _p(vs), on.raw), "rhtq_cache_append")
         on.keep(ks, vs, kc if kc is not k else None, vc if vc is not v else None)
     finally:
@@ -363,7 +365,7 @@ def rhtq_paged_attention(q, cache: RhtqCache, table, lengths, k_signs=None, v_si
     on = _On(index)
     try:
         ks, vs = _signs(k_signs, dim, q), _signs(v_signs, dim, q)
-        qc = _row_strides(q)
+        qc, of_seq, of_head = _row_strides(q)
         own = out is None
         if own:
             out = q.new_empty(q.shape)
@@ -371,7 +373,7 @@ def rhtq_paged_attention(q, cache: RhtqCache, table, lengths, k_signs=None, v_si
         work = q.new_empty(need, dtype=_U8) if need else None
         if stream is not None:
             on.follow(stream)
-        _check(lib.rhtq_paged_attention(qc.data_ptr(), in_type, seqs, q_heads, qc.stride(0), qc.stride(1), c[0],
+        _check(lib.rhtq_paged_attention(qc.data_ptr(), in_type, seqs, q_heads, of_seq, of_head, c[0],
                                         table.data_ptr(), width, lengths.data_ptr(), _p(ks), _p(vs),
                                         1.0 / math.sqrt(dim) if scale is None else scale, window, sinks, out.data_ptr(), _p(work),
                                         need, on.raw), "rhtq_paged_attention")

@@ -244,3 +244,24 @@ def test_more_sequences_than_workgroups(R):
     every = torch.arange(seqs, dtype=torch.int32, device="cuda")
     R.rhtq_pages_free(table, lengths, refs, every)
     assert refs.tolist() == [0] * 9 and (table == -1).all() and (lengths == 0).all()
+
+
+# ------------------------------------------------------------------------------------------------------------- views
+
+def test_one_token_of_a_wider_row(R):
+    """One sequence's token inside a fused projection whose rows are no multiple of 16 bytes apart, and one head alone."""
+    say("one token of a wider row")
+    cache = filled(R, 6, 4, 16, 128, 11)
+    one = filled(R, 6, 1, 16, 128, 12)
+    table, lengths = torch.tensor([[3, 1, 5]], dtype=torch.int32, device="cuda"), ints(37)
+    qkv = torch.randn(2, 16 * 128 + 4, device="cuda", dtype=torch.bfloat16)[:, :2048].unflatten(1, (16, 128))[:1]
+    assert qkv.stride(0) % 8
+    ref = [t.clone() for t in cache]
+    R.rhtq_cache_append(R.RhtqCache(*ref), qkv[:, 8:12].clone(), qkv[:, 12:].clone(), table, lengths)
+    R.rhtq_cache_append(cache, qkv[:, 8:12], qkv[:, 12:], table, lengths)
+    assert all(torch.equal(a, b) for a, b in zip(ref, cache))
+    o = R.rhtq_paged_attention(qkv[:, :8], cache, table, lengths)
+    assert torch.equal(o, R.rhtq_paged_attention(qkv[:, :8].clone(), cache, table, lengths))
+    heads = torch.randn(1, 128, 2, device="cuda", dtype=torch.float16).transpose(1, 2)[:, :1]      # elements two apart
+    R.rhtq_cache_append(one, heads, heads, table, lengths)
+    assert torch.equal(R.rhtq_paged_attention(heads, one, table, lengths), R.rhtq_paged_attention(heads.clone(), one, table, lengths))

@@ -4,6 +4,8 @@ import os
 import subprocess
 import sys
 
+import torch
+
 import randomized_hadamard_rotation_amd as R
 from randomized_hadamard_rotation_amd import serving
 
@@ -87,3 +89,23 @@ for kw in (dict(), dict(k_scales=F + 4), dict(v_scales=F + 8, scale_dtype=f32)):
     env = dict(os.environ, RHTQ_TEST_FAIL_LAUNCH="1", PYTHONPATH=ROOT)
     r = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_row_strides():
+    """Rows that start on 16 bytes are taken where they lie, also where an axis of one entry has an odd stride; others are copied."""
+    from randomized_hadamard_rotation_amd import serving
+    base = torch.arange(6 * 1540, dtype=torch.float32).to(torch.bfloat16).view(6, 1540)
+    heads = base[:, :1536].unflatten(1, (12, 128))
+    assert heads[:1].stride(0) == 1540
+    taken = [(heads[:1], (0, 128)), (heads[::2, 3:4], (3080, 0)), (heads[2:3, 5:6], (0, 0)),
+             (heads[:0], (0, 128)), (torch.zeros(4, 5, 2, 128, dtype=torch.bfloat16)[:, :, 1].transpose(0, 1), (256, 1280)),
+             (torch.zeros(1, 1, 128, dtype=torch.bfloat16).expand(3, 4, 128), (0, 0))]
+    for x, strides in taken:
+        got, *s = serving._row_strides(x)
+        assert got is x and tuple(s) == strides, (x.shape, x.stride(), s)
+    copied = [base[:, 4:1540].unflatten(1, (12, 128)), base[:1, 4:1540].unflatten(1, (12, 128)), torch.ones(2, 128, 4).transpose(1, 2),
+              heads[:2]]                                                # and two rows 1540 apart
+    for x in copied:
+        got, *s = serving._row_strides(x)
+        assert got is not x and torch.equal(got, x)
+        assert got.is_contiguous() and got.data_ptr() % 16 == 0 and tuple(s) == (x.shape[1] * x.shape[2], x.shape[2])
