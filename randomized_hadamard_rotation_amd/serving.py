@@ -166,12 +166,18 @@ def _int32(t, name, shape):
         _expect(t, name, _I32, shape)
 
 
+def _rows16(t):
+    """t contiguous from an address of 16 bytes on: a copy where it is not (views may start anywhere)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _signs(signs, n, x):
     """Device int8 [n] (marshalling only)."""
     if signs is None or (type(signs) is torch.Tensor and signs.dtype is _I8 and signs.dim() == 1 and signs.shape[0] == n
-                         and signs.is_contiguous() and signs.get_device() == x.get_device()):
+                         and signs.is_contiguous() and signs.get_device() == x.get_device() and signs.data_ptr() % 16 == 0):
         return signs
-    return _signs_tensor(signs, n, x.device)
+    return _rows16(_signs_tensor(signs, n, x.device))
 
 
 def _p(t):
@@ -225,7 +231,7 @@ def rhtq_matvec(packed, scales, x, signs=None, fmt: str = "int4", group: int = 0
     _one_device(index, {"x": x, "packed": packed, "scales": scales, "tensor_scale": tensor_scale, "out": out})
     on = _On(index)
     try:
-        xc, pc, sc = x.contiguous(), packed.contiguous(), scales.contiguous()
+        xc, pc, sc = _rows16(x), _rows16(packed), _rows16(scales)
         s = None if rotated else _signs(signs, n, x)
         own = out is None
         if own:

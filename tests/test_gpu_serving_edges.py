@@ -265,3 +265,33 @@ def test_one_token_of_a_wider_row(R):
     heads = torch.randn(1, 128, 2, device="cuda", dtype=torch.float16).transpose(1, 2)[:, :1]      # elements two apart
     R.rhtq_cache_append(one, heads, heads, table, lengths)
     assert torch.equal(R.rhtq_paged_attention(heads, one, table, lengths), R.rhtq_paged_attention(heads.clone(), one, table, lengths))
+
+
+def test_views_that_start_anywhere(R):
+    """x, weights' rows, scales and signs that begin off 16 bytes, as slices of larger buffers do."""
+    say("views that start anywhere")
+    n, rows = 256, 19
+
+    def shifted(t, by):
+        """The same values from element `by` of a buffer on."""
+        buf = torch.empty(t.numel() + by, dtype=t.dtype, device="cuda")
+        buf[by:] = t.flatten()
+        return buf[by:].view(t.shape)
+    sg = torch.from_numpy(np.where(np.random.RandomState(1).rand(n) < 0.5, -1, 1).astype(np.int8)).cuda()
+    w, x = torch.randn(rows, n, device="cuda").bfloat16(), torch.randn(3, n, device="cuda").bfloat16()
+    for fmt, kw in (("int4", dict(group=32, scale_dtype="f16")), ("nvfp4", {}), ("mxfp4", {})):
+        p, s, ts = R.rhtq_forward(w, sg, fmt=fmt, **kw)
+        ref = R.rhtq_matvec(p, s, x, sg, fmt=fmt, tensor_scale=ts, **kw)
+        got = R.rhtq_matvec(shifted(p, 1), shifted(s, 1), shifted(x, 3), shifted(sg, 5), fmt=fmt, tensor_scale=ts, **kw)
+        assert torch.equal(got, ref), fmt
+    a, b = (filled(R, 3, 2, 16, 128, 4) for _ in range(2))
+    table, lengths, sg = torch.tensor([[2, 0], [1, -1]], dtype=torch.int32, device="cuda"), ints(20, 7), sg[:128]
+    kv = torch.randn(2, 2, 128, device="cuda").half()
+    R.rhtq_cache_append(a, kv, kv, table, lengths, None, sg, sg)
+    R.rhtq_cache_append(b, shifted(kv, 1), shifted(kv, 9), table, lengths, None, shifted(sg, 1), shifted(sg, 2))
+    assert all(torch.equal(t, u) for t, u in zip(a, b))
+    for u, v in zip(R.rhtq_cache_read(a, table, lengths, None, 2, sg, sg), R.rhtq_cache_read(a, table, lengths, None, 2, shifted(sg, 3), shifted(sg, 1))):
+        assert torch.equal(u, v)
+    q = torch.randn(2, 4, 128, device="cuda").half()
+    assert torch.equal(R.rhtq_paged_attention(shifted(q, 2), a, table, lengths, shifted(sg, 1), shifted(sg, 7)),
+                       R.rhtq_paged_attention(q, a, table, lengths, sg, sg))
