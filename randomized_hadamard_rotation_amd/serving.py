@@ -180,6 +180,11 @@ def _signs(signs, n, x):
     return _rows16(_signs_tensor(signs, n, x.device))
 
 
+def _bounded(v):
+    """A count as int32, which ctypes would cut to its low 32 bits: beyond 2^31 - 1 positions there are none."""
+    return max(-1, min(v, 0x7FFFFFFF))
+
+
 def _p(t):
     return None if t is None else t.data_ptr()
 
@@ -363,6 +368,7 @@ def rhtq_paged_attention(q, cache: RhtqCache, table, lengths, k_signs=None, v_si
         raise ValueError(f"q: {tuple(q.shape)} does not fit {kv_heads} key-value heads of {c[4]}")
     if window < 0 or sinks < 0:
         raise ValueError("window and sinks must not be negative")
+    window, sinks = _bounded(window), _bounded(sinks)
     if out is not None:
         _expect(out, "out", q.dtype, q.shape)
     index = q.get_device()
@@ -448,7 +454,7 @@ def rhtq_pages_reserve(table, lengths, refs, add, page: int, stream=None):
     pages = refs.shape[0]
     return _page_call("rhtq_pages_reserve", {"table": table, "lengths": lengths, "refs": refs, "add": add}, stream,
                       lambda raw, word, work, size: lib.rhtq_pages_reserve(table.data_ptr(), width, lengths.data_ptr(), seqs, refs.data_ptr(),
-                                                                           pages, page, add.data_ptr(), word, work, size, raw),
+                                                                           pages, _bounded(page), add.data_ptr(), word, work, size, raw),
                       pages, seqs, 0, True)
 
 
@@ -466,7 +472,7 @@ def rhtq_pages_trim(table, lengths, refs, page: int, window: int, sinks: int = 0
     seqs, width = _paging(table, lengths, refs)
     _page_call("rhtq_pages_trim", {"table": table, "lengths": lengths, "refs": refs}, stream,
                lambda raw, word, work, size: lib.rhtq_pages_trim(table.data_ptr(), width, lengths.data_ptr(), seqs, refs.data_ptr(),
-                                                                 refs.shape[0], page, window, sinks, raw))
+                                                                 refs.shape[0], _bounded(page), _bounded(window), _bounded(sinks), raw))
 
 
 def rhtq_pages_fork(cache: RhtqCache, table, lengths, refs, src, dst, stream=None):

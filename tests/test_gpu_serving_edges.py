@@ -295,3 +295,26 @@ def test_views_that_start_anywhere(R):
     q = torch.randn(2, 4, 128, device="cuda").half()
     assert torch.equal(R.rhtq_paged_attention(shifted(q, 2), a, table, lengths, shifted(sg, 1), shifted(sg, 7)),
                        R.rhtq_paged_attention(q, a, table, lengths, sg, sg))
+
+
+# ----------------------------------------------------------------------------------------------------------- numbers
+
+@pytest.mark.parametrize("huge", [2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 40])
+def test_windows_beyond_32_bits(R, huge):
+    """A window or a count of first positions larger than any sequence leaves everything visible."""
+    say("windows beyond 32 bits", huge)
+    cache = filled(R, 8, 1, 16, 64, 9)
+    table, lengths, refs = torch.tensor([[4, 7, 1, 2]], dtype=torch.int32, device="cuda"), ints(60), ints(0, 1, 1, 0, 1, 0, 0, 1)
+    q = torch.randn(1, 2, 64, device="cuda", dtype=torch.float16)
+    every = R.rhtq_paged_attention(q, cache, table, lengths)
+    assert torch.equal(R.rhtq_paged_attention(q, cache, table, lengths, window=huge), every)
+    assert torch.equal(R.rhtq_paged_attention(q, cache, table, lengths, window=5, sinks=huge), every)
+    R.rhtq_pages_trim(table, lengths, refs, 16, window=huge)
+    R.rhtq_pages_trim(table, lengths, refs, 16, window=5, sinks=huge)
+    assert table.tolist() == [[4, 7, 1, 2]] and refs.tolist() == [0, 1, 1, 0, 1, 0, 0, 1]
+    with pytest.raises(R.RhtqError):
+        R.rhtq_pages_trim(table, lengths, refs, 2 ** 32 + 16, window=5)
+    with pytest.raises(R.RhtqError):
+        R.rhtq_pages_trim(table, lengths, refs, 16, window=-2 ** 32 + 5)
+    with pytest.raises(R.RhtqError):
+        R.rhtq_pages_reserve(table, lengths, refs, ints(1), 2 ** 32 + 16)
