@@ -97,9 +97,9 @@ int rhtq_cache_read(const rhtq_cache_t* cache, void* k_out, void* v_out, int out
  *   q   [seqs][q_heads][head_dim] bf16 or fp16, strides in elements (rows 16-byte aligned); q_heads a multiple of kv_heads
  *   out [seqs][q_heads][head_dim] contiguous, q's type
  *   workspace  rhtq_paged_attention_workspace(...) bytes, 16-byte aligned
- * Scores, softmax and sums are in fp32.  q enters the products as whole numbers to 2^-16 of a head's largest rotated value, the weights
- * p_j * (scale of v_j) to 2^-16 of the largest among 64 positions; below 2^-110 they count as 0.  scale is finite, and scores
- * stay finite in fp32.  The new token's own row has to be appended first.
+ * Scores, softmax and sums are in fp32.  q enters the products as whole numbers, off by at most 2^-22 of a head's largest rotated value,
+ * the weights p_j * (scale of v_j) likewise, of the largest among 64 positions.  scale is finite, and scores stay finite in fp32.  The new
+ * token's own row has to be appended first.  8 query heads of a key-value head read the cache once; more read it once for every 8.
  */
 int64_t rhtq_paged_attention_workspace(int32_t seqs, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t width,
                                        int32_t page, int32_t window, int32_t sinks);

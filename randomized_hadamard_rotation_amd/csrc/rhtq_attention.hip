@@ -5,17 +5,20 @@
 // The rotation is orthonormal, so q is rotated once, the codes are used as they lie, and the sum is rotated back once.
 // The bytes of the codes and scales bound it, so nothing else may take long:
 //  - Both products run on the int8 matrix cores on the codes themselves, 16 c as a byte (a mask, or a shift and a mask, for four
-//    codes), exactly.  q and the weights p_j s^v_j go in as two bytes, v = 256 hi + lo, of a 16-bit fixed point relative to the largest of
-//    their row: q over its head, the weights over a chunk of 64 positions.
-//  - S^T = K Q^T has positions as rows and, as its 16 columns, 8 query heads of one key-value head in hi and in lo bytes: lane (n, g) gets
-//    positions 4 g + i of each tile for column n.  Lanes n and n + 8 swap halves (a DPP rotation by 8) so that the lower one finishes
-//    positions 4 g, 4 g + 1 and the upper one 4 g + 2, 4 g + 3, and swap the finished weights back as bytes: the lane then holds the 16
-//    weights that it supplies as an operand of O^T = V^T P^T.
+//    codes), exactly.  q and the weights p_j s^v_j go in as three signed bytes, v = 65536 a + 256 b + c, whole numbers of up to 2^22 for
+//    the power of two above the largest of their row (q over its head, the weights over a chunk of 64 positions): off by at most 2^-22 of it.
+//  - S^T = K Q^T has positions as rows and query heads of one key-value head as its 16 columns; lane (n, g) gets positions 4 g + i of each
+//    tile for column n.  Up to 4 heads: column 4 h + r is head h's byte r (0: c, 1: b, 2: a, 3: nothing).  The four lanes of a head add up
+//    65536 a + 256 b + c as they divide the positions among them, one each, and turn the finished weights' bytes (a 4 x 4 transposition by
+//    DPP moves and byte permutes) into the operand of O^T = V^T P^T.  5 to 8 heads: columns h and 8 + h are bytes a and b, and a second
+//    product adds c to the upper ones, as 256 b + c.  Lanes n and n + 8 swap halves, finish two positions each and swap the bytes back.
 //  - A lane loads one dword (at head_dim 128) of 16 rows of V; 4 x 4 byte transposes in registers make operands of four positions.
 //  - One pass: each wave keeps the running maximum m, sum l and the weighted sum o in fp32.  Parts (m, l, o) of waves and of
 //    splits join as m = max m_i, l = sum l_i 2^(m_i - m), o likewise, in a fixed order.
 // Scores are in units of log2, so a weight is one v_exp_f32.
 //
+// Two bytes (16 bits) of q and of the weights took the same time with up to 4 heads and 29.7 us where 64 / 8 heads x 4096 positions now take
+// 31.7, but one fp16 output in 5 was then another number than the rounded result, for 1 in 200 now.
 // Measured: 32 x 32 heads x 4096 positions 98 us (554 MB, 5.6 TB/s; a copy moves 5.1); one sequence of 131072 with 8 key-value heads 27 us
 // and 4 us to join (4.3 TB/s); 515 positions of 32 heads 7.8 us, a chain of length, table, codes and the end's exchange.
 #include <type_traits>
@@ -29,14 +32,13 @@ namespace {
 
 constexpr int kWaves = 8;
 constexpr int kJoinWaves = 4;           // heads of a join's workgroup
-constexpr int kHeads = 8;               // query heads of a tile
+constexpr int kHeads = 8;               // most query heads of a tile
 constexpr int kChunk = 4;               // tiles that a wave takes at once: 64 positions, the depth of one product
 constexpr int kLeastTiles = kWaves * kChunk;   // tiles of a part worth a workgroup: 512 positions
 constexpr int kMostTiles = 320;         // and at most, where the whole is enough for the chip: 5120 positions
 constexpr int kEnough = 256;            // workgroups that fill the chip: one of 8 waves on each CU
 constexpr float kNone = -INFINITY;
-constexpr float kTiny = 7.7037197775489434e-34f;   // 2^-110
-constexpr float kLargest = 32639.0f;    // 127 * 256 + 127: the largest two-byte value
+constexpr int kBits = 22;               // of q and the weights as whole numbers
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
@@ -62,8 +64,28 @@ __device__ __forceinline__ float max_over_groups(float v) {
   return fmaxf(__uint_as_float(h[0]), __uint_as_float(h[1]));
 }
 
-// Largest over the lanes that share a query head: 8 apart (in a row of 16) and 16 and 32 apart.
-__device__ __forceinline__ float max_over_head(float v) { return max_over_groups(fmaxf(v, lane_xor16<3>(v))); }
+// Over the lanes of a row of 16 that share a query head: 4 neighbours, or two 8 apart.
+template <int HT>
+__device__ __forceinline__ float add_over_columns(float v) {
+  if constexpr (HT == 4) {
+    v += lane_xor16<0>(v);
+    return v + lane_xor16<1>(v);
+  } else {
+    return v + lane_xor16<3>(v);
+  }
+}
+
+// Largest over all lanes that share a query head: these, and those 16 and 32 apart.
+template <int HT>
+__device__ __forceinline__ float max_over_head(float v) {
+  if constexpr (HT == 4) {
+    v = fmaxf(v, lane_xor16<0>(v));
+    v = fmaxf(v, lane_xor16<1>(v));
+  } else {
+    v = fmaxf(v, lane_xor16<3>(v));
+  }
+  return max_over_groups(v);
+}
 
 // Where a chunk's tiles lie: first position (-1: none) and page.  The same in all lanes.
 struct Place {
@@ -87,13 +109,13 @@ __device__ __forceinline__ void locate(const AttentionArgs& a, const Visible& vi
   }
 }
 
-// What a wave has loaded of a chunk.
-template <int D, bool F32>
+// What a wave has loaded of a chunk.  PER: positions of a tile that a lane finishes, whose scales it has.
+template <int D, bool F32, int PER>
 struct Loaded {
   static constexpr int H = D >= 128 ? D / 128 : 1;
   u32x4 k[kChunk][H];                           // D 64: two dwords used
   uint32_t v[kChunk][4][H];
-  uint32_t ks[kChunk][F32 ? 2 : 1], vs[kChunk][F32 ? 2 : 1];   // this lane's two scales: fp32, or two fp16 in a word
+  uint32_t ks[kChunk][F32 ? PER : 1], vs[kChunk][F32 ? PER : 1];   // its scales: fp32, or one or two fp16 in a word
 };
 
 // First slot of a tile, counted in rows.  A tile of no page takes page 0, which its weights of 0 make harmless, so that its loads need no
@@ -103,19 +125,32 @@ __device__ __forceinline__ int64_t slot_of(const AttentionArgs& a, int kv, const
   return (((int64_t)at.page[t] * a.kv_heads + kv) << a.page_log) + (pos >= 0 ? pos & ((1 << a.page_log) - 1) : 0);
 }
 
-template <bool F32, int N>
+template <bool F32, int PER, int N>
 __device__ __forceinline__ void load_scales(const void* p, int64_t slot, uint32_t (&s)[N]) {
   if constexpr (F32) {
-    const u32x2 x = *reinterpret_cast<const u32x2*>(static_cast<const float*>(p) + slot);
-    s[0] = x.x;
-    s[1] = x.y;
+    const float* q = static_cast<const float*>(p) + slot;
+    if constexpr (PER == 2) {
+      const u32x2 x = *reinterpret_cast<const u32x2*>(q);
+      s[0] = x.x;
+      s[1] = x.y;
+    } else {
+      s[0] = *reinterpret_cast<const uint32_t*>(q);
+    }
   } else {
-    s[0] = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + slot);
+    const uint16_t* q = static_cast<const uint16_t*>(p) + slot;
+    if constexpr (PER == 2) s[0] = *reinterpret_cast<const uint32_t*>(q);
+    else s[0] = *q;
   }
 }
 
-template <int D, bool F32>
-__device__ __forceinline__ void load_keys(const AttentionArgs& a, int kv, const Place& at, Loaded<D, F32>& c) {
+// First of the PER positions of a tile that lane (n, g) finishes.
+template <int PER>
+__device__ __forceinline__ int own_position(int n, int g) {
+  return PER == 1 ? 4 * g + (n & 3) : 4 * g + 2 * (n >> 3);
+}
+
+template <int D, bool F32, int PER>
+__device__ __forceinline__ void load_keys(const AttentionArgs& a, int kv, const Place& at, Loaded<D, F32, PER>& c) {
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int t = 0; t < kChunk; ++t) {
@@ -129,12 +164,12 @@ __device__ __forceinline__ void load_keys(const AttentionArgs& a, int kv, const 
       for (int h = 0; h < D / 128; ++h)
         c.k[t][h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(k + 64 * h + 16 * g));
     }
-    load_scales<F32>(a.k_scales, slot + 4 * g + 2 * (n >> 3), c.ks[t]);
+    load_scales<F32, PER>(a.k_scales, slot + own_position<PER>(n, g), c.ks[t]);
   }
 }
 
-template <int D, bool F32>
-__device__ __forceinline__ void load_values(const AttentionArgs& a, int kv, const Place& at, Loaded<D, F32>& c) {
+template <int D, bool F32, int PER>
+__device__ __forceinline__ void load_values(const AttentionArgs& a, int kv, const Place& at, Loaded<D, F32, PER>& c) {
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int t = 0; t < kChunk; ++t) {
@@ -150,7 +185,7 @@ __device__ __forceinline__ void load_values(const AttentionArgs& a, int kv, cons
         c.v[t][i][1] = w.y;
       }
     }
-    load_scales<F32>(a.v_scales, slot + 4 * g + 2 * (n >> 3), c.vs[t]);
+    load_scales<F32, PER>(a.v_scales, slot + own_position<PER>(n, g), c.vs[t]);
   }
 }
 
@@ -174,23 +209,30 @@ __device__ __forceinline__ int operand_byte(int d) {
   else return ((2 * (d >> 7) + (d & 1)) * 4 + ((d & 127) >> 5)) * 16 + ((d & 31) >> 1);
 }
 
-// One workgroup: a part of one sequence's positions for up to 8 query heads of one key-value head; its waves take the chunks
+// Waves a SIMD; a workgroup is two.  Four: 32 x 32 heads x 4096 positions 96 us, with three 106 (fp32 scales 98 and 106).  Three: 48 x 8
+// heads, ragged, with a window 20.4 us for 22.6 (both types), and 64 / 8 heads 31.4 us for 36.6, where four spill.  head_dim 256 needs the
+// registers of two.
+constexpr int waves_of(int E, bool F32, int HT) { return E == 16 ? 2 : (F32 || HT == 8 ? 3 : 4); }
+
+// One workgroup: a part of one sequence's positions for up to HT = 4 or 8 query heads of one key-value head; its waves take the chunks
 // in turn.
-template <int T, int E, bool F32>
-__global__ __launch_bounds__(64 * kWaves, E == 16 || F32 ? 2 : 4) void attention_kernel(AttentionArgs a) {
+template <int T, int E, bool F32, int HT>
+__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(waves_of(E, F32, HT), waves_of(E, F32, HT))))
+void attention_kernel(AttentionArgs a) {
+  constexpr int PER = HT == 8 ? 2 : 1;    // positions of a tile that a lane finishes
   constexpr int D = 16 * E;
   constexpr int NK = D / 64;              // products of a score
   constexpr int H = D >= 128 ? D / 128 : 1;
-  __shared__ __attribute__((aligned(16))) uint8_t sq[16][D];
-  __shared__ float sf[kHeads];
-  __shared__ float sm[kWaves][kHeads], sl[kWaves][kHeads];
-  __shared__ __attribute__((aligned(16))) float so[kWaves][kHeads][D + 4];   // + 4: columns start in other banks
+  __shared__ __attribute__((aligned(16))) uint8_t sq[3 * HT + 1][D];   // bytes a, b, c of each head, and zeros
+  __shared__ float sf[HT];
+  __shared__ float sm[kWaves][HT], sl[kWaves][HT];
+  __shared__ __attribute__((aligned(16))) float so[kWaves][HT][D + 4];   // + 4: columns start in other banks
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int group = threadIdx.x >> 4, j = threadIdx.x & 15;
   const int split = blockIdx.x, s = blockIdx.z;
-  const int kv = blockIdx.y / a.head_tiles, head0 = (blockIdx.y - kv * a.head_tiles) * kHeads;
-  const int heads = a.each - head0 < kHeads ? a.each - head0 : kHeads;
+  const int kv = blockIdx.y / a.head_tiles, head0 = (blockIdx.y - kv * a.head_tiles) * HT;
+  const int heads = a.each - head0 < HT ? a.each - head0 : HT;
   // loads in the order of their use: q's rotation then runs while the first chunk's codes are on their way
   const int length = load_uniform(a.lengths + s);
   uint32_t signs[E / 4];
@@ -206,41 +248,51 @@ __global__ __launch_bounds__(64 * kWaves, E == 16 || F32 ? 2 : 4) void attention
 
   int at = t0 + wave * kChunk;
   Place next;
-  Loaded<D, F32> c;
+  Loaded<D, F32, PER> c;
   // a wave without a chunk loads too (page 0): the number of loads before the first wait is then known
   locate(a, vis, table, at, t1, next);
-  load_keys<D, F32>(a, kv, next, c);
-  load_values<D, F32>(a, kv, next, c);
+  load_keys<D, F32, PER>(a, kv, next, c);
+  load_values<D, F32, PER>(a, kv, next, c);
 
-  // q: 16 lanes rotate a head and leave its bytes as operand rows h (hi) and 8 + h (lo)
-  if (group < kHeads) {
+  if (threadIdx.x < D / 4) reinterpret_cast<uint32_t*>(sq[3 * HT])[threadIdx.x] = 0;
+  // q: 16 lanes rotate a head and leave its bytes as operand rows h (a), HT + h (b) and 2 HT + h (c)
+  if (group < HT) {
     apply_signs<E>(signs, x0);
     fwht16<E>(x0);
     float amax = 0.0f;
 #pragma unroll
     for (int i = 0; i < E; ++i) amax = fmaxf(amax, __builtin_fabsf(x0[i]));
     amax = max16(amax);
-    const float inv = amax > kTiny ? kLargest / amax : 0.0f;   // a quotient: the reciprocal of the largest values is subnormal
+    const int e = __builtin_amdgcn_frexp_expf(amax);   // amax < 2^e; 0 for 0
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const int v = (int)__builtin_rintf(x0[i] * inv);
-      sq[group][operand_byte<D>(j * E + i)] = (uint8_t)((v + 128) >> 8);
-      sq[8 + group][operand_byte<D>(j * E + i)] = (uint8_t)v;
+      const int v = (int)__builtin_rintf(__builtin_amdgcn_ldexpf(x0[i], kBits - e));
+      const int high = (v + 128) >> 8;   // 256 a + b
+      sq[group][operand_byte<D>(j * E + i)] = (uint8_t)((high + 128) >> 8);
+      sq[HT + group][operand_byte<D>(j * E + i)] = (uint8_t)high;
+      sq[2 * HT + group][operand_byte<D>(j * E + i)] = (uint8_t)v;
     }
     // what a product of 16 c and the fixed point counts for in a score, log2
     const float cnorm = E == 4 ? 0.125f : (E == 8 ? 0.088388347648318447f : 0.0625f);
-    if (j == 0) sf[group] = amax / (16.0f * kLargest) * (cnorm * 1.4426950408889634f) * a.scale;
+    if (j == 0) sf[group] = __builtin_amdgcn_ldexpf(cnorm * 1.4426950408889634f, e - kBits - 4) * a.scale;
   }
   __syncthreads();
-  i32x4 q[NK];
-#pragma unroll
-  for (int i = 0; i < NK; ++i) q[i] = *reinterpret_cast<const i32x4*>(&sq[n][(4 * i + g) * 16]);
-  const float factor = sf[n & 7];
-  // the weights' bytes: 1.5 * 2^23 in front makes the sum's low bits the whole number, + 128 its second byte hi; the first is then
-  // lo + 128.  Of the lane's own two weights and its partner's, the lower lane supplies the hi bytes, the upper one the lo bytes.
-  const float magic = 12582912.0f + 128.0f;
-  const uint32_t pick = n < 8 ? 0x07050301u : 0x02000604u, flip = n < 8 ? 0u : 0x80808080u;
-  const int upper = n >= 8 ? -1 : 0;
+  // this lane's head, what its column counts for in a sum, and its operand rows
+  const int h = HT == 4 ? n >> 2 : n & 7, r = HT == 4 ? n & 3 : n >> 3;
+  const float counts = HT == 4 ? (r == 0 ? 1.0f : (r == 1 ? 256.0f : (r == 2 ? 65536.0f : 0.0f))) : (r ? 1.0f : 256.0f);
+  const float partner_counts = HT == 4 ? (r == 0 ? 65536.0f : (r == 1 ? 0.0f : (r == 2 ? 1.0f : 256.0f))) : 0.0f;   // two columns on
+  int q_row = (HT == 4 ? (r == 3 ? 3 * HT : (2 - r) * HT + h) : n) * D + 16 * g;
+  int c_row = (r ? 2 * HT + h : 3 * HT) * D + 16 * g;   // 8 heads
+  const float factor = sf[h];
+  // The weights' bytes: 2^23 in front makes the sum's low 23 bits the whole number, + 128 * 257 its third byte a; the others are then
+  // b + 128 and c + 128.  Byte selections (12 stands for 0).  4 heads: both stages of the transposition.  8 heads: what the partner gets
+  // of the lane's two weights, what the lane keeps, and from the kept and the partner's bytes the operands of both products.
+  const float magic = 8388608.0f + 32896.0f;
+  const uint32_t near = r & 1 ? 0x03070105u : 0x06020400u, across = r & 2 ? 0x03020706u : 0x05040100u;
+  const uint32_t give = r ? 0x0C0C0602u : 0x05040100u, keep = r ? 0x05040100u : 0x0C0C0602u;
+  const uint32_t pick = r ? 0x03010705u : 0x05040100u, pick_c = r ? 0x02000604u : 0x0C0C0C0Cu;
+  const uint32_t flip = (HT == 4 ? r < 2 : r == 1) ? 0x80808080u : 0u;
+  const int odd_column = r & 1 ? -1 : 0, upper = (HT == 4 ? r & 2 : r) ? -1 : 0;
 
   float m = kNone, l = 0.0f;
   float o[E][4] = {};                     // element E (4 g + i) + e of column n
@@ -252,43 +304,70 @@ __global__ __launch_bounds__(64 * kWaves, E == 16 || F32 ? 2 : 4) void attention
     for (int t = 0; t < kChunk; ++t) positions[t] = next.pos[t];
     at += kWaves * kChunk;
     if constexpr (more) locate(a, vis, table, at, t1, next);
-    float x[kChunk][2], top = kNone;
+    // q is read again for every chunk: held, it would take the registers of loads in flight
+    i32x4 q[NK], qc[NK];             // qc: 8 heads
+    asm("" : "+v"(q_row), "+v"(c_row));
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      q[i] = *reinterpret_cast<const i32x4*>(&sq[0][0] + q_row + 64 * i);
+      qc[i] = *reinterpret_cast<const i32x4*>(&sq[0][0] + c_row + 64 * i);
+    }
+    float x[kChunk][PER], top = kNone;
 #pragma unroll
     for (int t = 0; t < kChunk; ++t) {
-      i32x4 d = {0, 0, 0, 0};
+      i32x4 d = {0, 0, 0, 0}, k[NK];
       if constexpr (D == 64) {
-        const i32x4 k = {even_codes(c.k[t][0].x), even_codes(c.k[t][0].y), odd_codes(c.k[t][0].x), odd_codes(c.k[t][0].y)};
-        d = __builtin_amdgcn_mfma_i32_16x16x64_i8(k, q[0], d, 0, 0, 0);
+        const u32x4 w = c.k[t][0];
+        k[0] = i32x4{even_codes(w.x), even_codes(w.y), odd_codes(w.x), odd_codes(w.y)};
       } else {
 #pragma unroll
-        for (int h = 0; h < H; ++h) {
-          const u32x4 w = c.k[t][h];
-          const i32x4 k0 = {even_codes(w.x), even_codes(w.y), even_codes(w.z), even_codes(w.w)};
-          const i32x4 k1 = {odd_codes(w.x), odd_codes(w.y), odd_codes(w.z), odd_codes(w.w)};
-          d = __builtin_amdgcn_mfma_i32_16x16x64_i8(k0, q[2 * h], d, 0, 0, 0);
-          d = __builtin_amdgcn_mfma_i32_16x16x64_i8(k1, q[2 * h + 1], d, 0, 0, 0);
+        for (int i = 0; i < H; ++i) {
+          const u32x4 w = c.k[t][i];
+          k[2 * i] = i32x4{even_codes(w.x), even_codes(w.y), even_codes(w.z), even_codes(w.w)};
+          k[2 * i + 1] = i32x4{odd_codes(w.x), odd_codes(w.y), odd_codes(w.z), odd_codes(w.w)};
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NK; ++i) d = __builtin_amdgcn_mfma_i32_16x16x64_i8(k[i], q[i], d, 0, 0, 0);
+      if constexpr (HT == 8) {
+        d = d << 8;
+#pragma unroll
+        for (int i = 0; i < NK; ++i) d = __builtin_amdgcn_mfma_i32_16x16x64_i8(k[i], qc[i], d, 0, 0, 0);
+      }
+      float sum[PER];
+      if constexpr (HT == 4) {
+        // the lower two columns go on with positions 0 and 1, the upper two with 2 and 3; then each with one
+        float two[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int own = select(upper, d[2 + i], d[i]), other = lane_xor16<1>(select(upper, d[i], d[2 + i]));
+          two[i] = __builtin_fmaf((float)own, counts, (float)other * partner_counts);
+        }
+        const float own = __int_as_float(select(odd_column, __float_as_int(two[1]), __float_as_int(two[0])));
+        sum[0] = own + lane_xor16<0>(__int_as_float(select(odd_column, __float_as_int(two[0]), __float_as_int(two[1]))));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int own = select(upper, d[2 + i], d[i]), other = lane_xor16<3>(select(upper, d[i], d[2 + i]));
+          sum[i] = __builtin_fmaf((float)select(upper, other, own), 256.0f, (float)select(upper, own, other));   // of 256 a, of 256 b + c
         }
       }
       const int pos = positions[t];
       const bool cut = pos < 0 || pos + kTile > vis.len || (pos < vis.start && pos + kTile > vis.sinks);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int own = select(upper, d[2 + i], d[i]), other = lane_xor16<3>(select(upper, d[i], d[2 + i]));
-        const int hi = select(upper, other, own), lo = select(upper, own, other);
-        x[t][i] = (float)(256 * hi + lo) * (scale_of<F32>(c.ks[t], i) * factor);
-      }
+      for (int i = 0; i < PER; ++i) x[t][i] = sum[i] * (scale_of<F32>(c.ks[t], i) * factor);
       if (cut) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int at_pos = pos + 4 * g + 2 * (n >> 3) + i;
+        for (int i = 0; i < PER; ++i) {
+          const int at_pos = pos + own_position<PER>(n, g) + i;
           const bool seen = (at_pos < vis.len) & (pos >= 0) & ((at_pos >= vis.start) | (at_pos < vis.sinks));
           x[t][i] = seen ? x[t][i] : kNone;
         }
       }
-      top = fmaxf(top, fmaxf(x[t][0], x[t][1]));
+      top = fmaxf(top, PER == 2 ? fmaxf(x[t][0], x[t][PER - 1]) : x[t][0]);
     }
-    if constexpr (more) load_keys<D, F32>(a, kv, next, c);
-    const float mn = fmaxf(m, max_over_head(top));
+    if constexpr (more) load_keys<D, F32, PER>(a, kv, next, c);
+    const float mn = fmaxf(m, max_over_head<HT>(top));
     const float base = mn == kNone ? 0.0f : mn;
     const float fade = m == kNone ? 0.0f : __builtin_amdgcn_exp2f(m - base);
     if (__any(mn != m)) {
@@ -306,7 +385,7 @@ __global__ __launch_bounds__(64 * kWaves, E == 16 || F32 ? 2 : 4) void attention
 #pragma unroll
       for (int t = 0; t < kChunk; ++t)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < PER; ++i) {
           const float p = __builtin_amdgcn_exp2f(x[t][i] - base);
           l += p;
           // what lies behind the last position may hold anything: it has weight 0 whatever its scale
@@ -315,19 +394,25 @@ __global__ __launch_bounds__(64 * kWaves, E == 16 || F32 ? 2 : 4) void attention
           top = fmaxf(top, x[t][i]);
         }
     }
-    top = max_over_head(top);
-    // weights below 2^-110 are none: their reciprocal stays finite
-    const float unit = top > kTiny ? kLargest * __builtin_amdgcn_rcpf(top) : 0.0f;
-    i32x4 p;
+    top = max_over_head<HT>(top);
+    const int e_top = __builtin_amdgcn_frexp_expf(top);
+    i32x4 p, pc;
 #pragma unroll
     for (int t = 0; t < kChunk; ++t) {
-      const uint32_t w0 = __float_as_uint(__builtin_fmaf(x[t][0], unit, magic));
-      const uint32_t w1 = __float_as_uint(__builtin_fmaf(x[t][1], unit, magic));
-      const uint32_t own = __builtin_amdgcn_perm(w1, w0, 0x05040100u);
-      const uint32_t other = (uint32_t)lane_xor16<3>((int)own);
-      p[t] = (int)(__builtin_amdgcn_perm(other, own, pick) ^ flip);
+      uint32_t w[PER];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) w[i] = __float_as_uint(__builtin_amdgcn_ldexpf(x[t][i], kBits - e_top) + magic);
+      if constexpr (HT == 4) {
+        const uint32_t pair = __builtin_amdgcn_perm((uint32_t)lane_xor16<0>((int)w[0]), w[0], near);
+        p[t] = (int)(__builtin_amdgcn_perm((uint32_t)lane_xor16<1>((int)pair), pair, across) ^ flip);
+      } else {
+        const uint32_t own = __builtin_amdgcn_perm(w[1], w[0], keep);
+        const uint32_t other = (uint32_t)lane_xor16<3>((int)__builtin_amdgcn_perm(w[1], w[0], give));
+        p[t] = (int)(__builtin_amdgcn_perm(other, own, pick) ^ flip);
+        pc[t] = (int)(__builtin_amdgcn_perm(other, own, pick_c) ^ flip);
+      }
     }
-    const float back = top * (1.0f / (16.0f * kLargest)) * (n < 8 ? 256.0f : 1.0f);
+    const float back = __builtin_amdgcn_ldexpf(counts, e_top - kBits - 4);
     // V: byte r of the four rows of a lane's tile, transposed; its low nibbles are element 2 r, its high ones 2 r + 1
     constexpr int R = D / 32;
     uint32_t col[R][kChunk];
@@ -345,7 +430,7 @@ __global__ __launch_bounds__(64 * kWaves, E == 16 || F32 ? 2 : 4) void attention
           col[4 * h + 3][t] = __builtin_amdgcn_perm(y1, x1, 0x07060302u);
         }
       }
-    if constexpr (more) load_values<D, F32>(a, kv, next, c);
+    if constexpr (more) load_values<D, F32, PER>(a, kv, next, c);
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -354,6 +439,7 @@ __global__ __launch_bounds__(64 * kWaves, E == 16 || F32 ? 2 : 4) void attention
 #pragma unroll
         for (int t = 0; t < kChunk; ++t) v[t] = odd ? odd_codes(col[r][t]) : even_codes(col[r][t]);
         d = __builtin_amdgcn_mfma_i32_16x16x64_i8(v, p, d, 0, 0, 0);
+        if constexpr (HT == 8) d = __builtin_amdgcn_mfma_i32_16x16x64_i8(v, pc, d << 8, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[2 * r + odd][i] = __builtin_fmaf((float)d[i], back, o[2 * r + odd][i]);
       }
@@ -362,24 +448,24 @@ __global__ __launch_bounds__(64 * kWaves, E == 16 || F32 ? 2 : 4) void attention
     while (at + kWaves * kChunk < t1) chunk(std::true_type{});
     chunk(std::false_type{});
   }
-  // both halves of a column's sum; l over the lanes that share it
-  l += lane_xor16<3>(l);
+  // l over the lanes that share a head, o over its columns
+  l = add_over_columns<HT>(l);
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
 #pragma unroll
   for (int e = 0; e < E; ++e)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[e][i] += lane_xor16<3>(o[e][i]);
-  if (n < kHeads) {
+    for (int i = 0; i < 4; ++i) o[e][i] = add_over_columns<HT>(o[e][i]);
+  if (r == 0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int e = 0; e < E; e += 4)
-        *reinterpret_cast<f32x4*>(&so[wave][n][E * (4 * g + i) + e]) = f32x4{o[e][i], o[e + 1][i], o[e + 2][i], o[e + 3][i]};
-  }
-  if (lane < kHeads) {
-    sm[wave][lane] = m;
-    sl[wave][lane] = l;
+        *reinterpret_cast<f32x4*>(&so[wave][h][E * (4 * g + i) + e]) = f32x4{o[e][i], o[e + 1][i], o[e + 2][i], o[e + 3][i]};
+    if (g == 0) {
+      sm[wave][h] = m;
+      sl[wave][h] = l;
+    }
   }
   __syncthreads();
   if (group >= heads) return;
@@ -387,21 +473,21 @@ __global__ __launch_bounds__(64 * kWaves, E == 16 || F32 ? 2 : 4) void attention
 #pragma unroll
   for (int k = 0; k < kWaves; ++k) m = fmaxf(m, sm[k][group]);
   l = 0.0f;
-  float r[E] = {};
+  float res[E] = {};
 #pragma unroll
   for (int k = 0; k < kWaves; ++k) {
     const float f = sm[k][group] == kNone ? 0.0f : __builtin_amdgcn_exp2f(sm[k][group] - m);
     l += sl[k][group] * f;
 #pragma unroll
-    for (int i = 0; i < E; ++i) r[i] = __builtin_fmaf(f, so[k][group][j * E + i], r[i]);
+    for (int i = 0; i < E; ++i) res[i] = __builtin_fmaf(f, so[k][group][j * E + i], res[i]);
   }
   const int64_t row = row0 + group;
   if (a.splits == 1) {
-    finish<T, E>(a, row, l, r);
+    finish<T, E>(a, row, l, res);
     return;
   }
   float* part = a.partial + (row * a.splits + split) * D;
-  store_row<RHTQ_IN_F32, E>(part, j * E, r);
+  store_row<RHTQ_IN_F32, E>(part, j * E, res);
   if (j == 0) {
     float* ml = a.partial + (int64_t)a.seqs * a.q_heads * a.splits * D + 2 * (row * a.splits + split);
     ml[0] = m;
@@ -456,9 +542,15 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(AttentionArgs a) 
 
 template <int T, int E>
 hipError_t launch_te(const AttentionArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)a.splits, (unsigned)(a.kv_heads * a.head_tiles), (unsigned)a.seqs);
-  if (a.scale_dtype == RHTQ_SCALE_F32) hipLaunchKernelGGL((attention_kernel<T, E, true>), grid, dim3(64 * kWaves), 0, s, a);
-  else hipLaunchKernelGGL((attention_kernel<T, E, false>), grid, dim3(64 * kWaves), 0, s, a);
+  const dim3 grid((unsigned)a.splits, (unsigned)(a.kv_heads * a.head_tiles), (unsigned)a.seqs), block(64 * kWaves);
+  const bool f32 = a.scale_dtype == RHTQ_SCALE_F32;
+  if (a.each <= 4) {
+    if (f32) hipLaunchKernelGGL((attention_kernel<T, E, true, 4>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((attention_kernel<T, E, false, 4>), grid, block, 0, s, a);
+  } else {
+    if (f32) hipLaunchKernelGGL((attention_kernel<T, E, true, 8>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((attention_kernel<T, E, false, 8>), grid, block, 0, s, a);
+  }
   const int64_t rows = (int64_t)a.seqs * a.q_heads;
   if (a.splits > 1)
     hipLaunchKernelGGL((join_kernel<T, E>), dim3((unsigned)((rows + kJoinWaves - 1) / kJoinWaves)), dim3(64 * kJoinWaves), 0, s, a);
