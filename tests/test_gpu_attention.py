@@ -1,10 +1,12 @@
-"""GPU: paged attention's rounding against the output type's own."""
+"""GPU: paged attention held to a bound that a lost chunk of positions exceeds (tests/test_attention_bound.py), at the lengths that are
+split over workgroups and joined; and its rounding against the output type's own."""
 import math
 import sys
 
 import numpy as np
 import pytest
 
+import oracle as O
 from tests import attention_model as A
 
 pytestmark = pytest.mark.gpu
@@ -36,9 +38,52 @@ def ints(*v):
     return torch.tensor(v, dtype=torch.int32, device="cuda")
 
 
+def signs_of(n, seed):
+    return np.where(np.random.RandomState(seed).rand(n) < 0.5, -1, 1).astype(np.int8)
+
+
 def check(o, ref, bound, qt):
     bad = A.off(o.double().cpu().numpy(), ref, bound, torch.finfo(DT[qt]).eps / 2, SUBNORMAL[qt])
     assert not bad.any(), f"heads off: {np.argwhere(bad).tolist()[:10]}"
+
+
+@pytest.mark.parametrize("lens,heads,kv,dim,page,sd,qt,window,sinks", A.LONG)
+def test_long_sequences(R, lens, heads, kv, dim, page, sd, qt, window, sinks):
+    say("attention, long", lens, heads, kv, dim, page, sd, qt, window, sinks)
+    cache = A.make(lens, kv, dim, page, sd, seed=heads + dim)
+    c, table = device(R, cache)
+    q = torch.from_numpy(np.random.RandomState(7).randn(len(lens), heads, dim)).to(DT[qt])
+    ks, vs = signs_of(dim, 3), signs_of(dim, 4)
+    o = R.rhtq_paged_attention(q.cuda(), c, table, ints(*lens), ks, vs, window=window, sinks=sinks)
+    ref, bound = A.reference(q.double().numpy(), cache, lens, ks, vs, 1 / math.sqrt(dim), window, sinks)
+    check(o, ref, bound, qt)
+
+
+@pytest.mark.parametrize("n,dim,page", [(700, 128, 16), (4097, 64, 32), (12000, 128, 64), (6000, 256, 16)])
+def test_one_position_outweighs_the_rest(R, n, dim, page):
+    """Each query's weight lies on one position: the first, the last, and those on both sides of a tile's, a chunk's, a workgroup's round
+    and a part's end.  All queries look at the same pages."""
+    say("attention, one position", n, dim, page)
+    at = sorted({p for p in (0, 1, 15, 16, 63, 64, 511, 512, 1023, 1024, 2560, 4095, 4096, 5119, 5120, n // 2, n - 65, n - 17, n - 2, n - 1)
+                 if 0 <= p < n})
+    kc, ks, vc, vs, table = A.make([n], 1, dim, page, "f16", seed=n)
+    rs = np.random.RandomState(n)
+    u = rs.choice([-7, 7], (len(at), dim))
+    for i, p in enumerate(at):
+        kc[table[0, p // page], 0, p % page] = O.pack_nibbles(u[i][None].astype(np.int64))[0]
+        ks[table[0, p // page], 0, p % page] = 0.5
+    q = torch.from_numpy(O.inverse_rotate(u / 7.0, None)).to(torch.bfloat16)[:, None]
+    table = np.repeat(table, len(at), 0)
+    cache = (kc, ks, vc, vs, table)
+    c, tb = device(R, cache)
+    lens = [n] * len(at)
+    o = R.rhtq_paged_attention(q.cuda(), c, tb, ints(*lens), scale=1.0)
+    ref, bound = A.reference(q.double().numpy(), cache, lens, None, None, 1.0)
+    for i, p in enumerate(at):                                     # the case is what it says
+        v, sv = A.rows_of(vc, vs, table[0], 0, [p], page)
+        row = O.inverse_rotate(v * sv[:, None], None)[0]
+        assert np.linalg.norm(ref[i, 0] - row) < 1e-3 * np.linalg.norm(row)
+    check(o, ref, bound, "bf16")
 
 
 @pytest.mark.parametrize("heads", [16, 28])
