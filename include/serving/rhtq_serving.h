@@ -38,7 +38,7 @@ int rhtq_serving_version(void);
  *   workspace  rhtq_matvec_workspace(...) bytes, 16-byte aligned
  * n: a multiple of 32 up to 2^20 (with rotated == 0 also one that rhtq_rotate or its blocked form takes).
  * rows up to 2^31 - 1024, tokens up to 2^20 (0: nothing to do).  Sums are in fp32; R x is carried to 22 bits, and to
- * 2^-35 of the largest value of its row.
+ * 2^-35 of the largest value of its row.  A value of R x that is not finite gives NaN for its token.
  * packed must be 16-byte aligned, x, y_out and signs 16 bytes, scales to their element (NVFP4: 2 bytes).
  */
 int64_t rhtq_matvec_workspace(int64_t tokens, int32_t n, int64_t rows);
@@ -98,8 +98,9 @@ int rhtq_cache_read(const rhtq_cache_t* cache, void* k_out, void* v_out, int out
  *   out [seqs][q_heads][head_dim] contiguous, q's type
  *   workspace  rhtq_paged_attention_workspace(...) bytes, 16-byte aligned
  * Scores, softmax and sums are in fp32.  q enters the products as whole numbers, off by at most 2^-22 of a head's largest rotated value,
- * the weights p_j * (scale of v_j) likewise, of the largest among 64 positions.  scale is finite, and scores stay finite in fp32.  The new
- * token's own row has to be appended first.  8 query heads of a key-value head read the cache once; more read it once for every 8.
+ * the weights p_j * (scale of v_j) likewise, of the largest among 64 positions.  scale is finite, and scores stay finite in fp32.  A
+ * query or a visible value's scale that is not finite, or a visible key's scale that is NaN, gives NaN for the heads that it takes part in.
+ * The new token's own row has to be appended first.  8 query heads of a key-value head read the cache once; more read it once for every 8.
  */
 int64_t rhtq_paged_attention_workspace(int32_t seqs, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t width,
                                        int32_t page, int32_t window, int32_t sinks);

@@ -47,7 +47,7 @@ template <int T, int E>
 __device__ __forceinline__ void finish(const AttentionArgs& a, int64_t row, float l, float (&o)[E]) {
   const int j = threadIdx.x & 15;
   const float cnorm = E == 4 ? 0.125f : (E == 8 ? 0.088388347648318447f : 0.0625f);
-  const float f = l > 0.0f ? cnorm * __builtin_amdgcn_rcpf(l) : 0.0f;
+  const float f = l == 0.0f ? 0.0f : cnorm * __builtin_amdgcn_rcpf(l);   // NaN where l is
   fwht16<E>(o);
 #pragma unroll
   for (int i = 0; i < E; ++i) o[i] *= f;
@@ -259,14 +259,19 @@ void attention_kernel(AttentionArgs a) {
   if (group < HT) {
     apply_signs<E>(signs, x0);
     fwht16<E>(x0);
-    float amax = 0.0f;
+    float amax = 0.0f, none = 0.0f;      // NaN where a value is not finite, which neither a maximum nor a whole number would show
 #pragma unroll
-    for (int i = 0; i < E; ++i) amax = fmaxf(amax, __builtin_fabsf(x0[i]));
+    for (int i = 0; i < E; ++i) {
+      amax = fmaxf(amax, __builtin_fabsf(x0[i]));
+      none = __builtin_fmaf(x0[i], 0.0f, none);
+    }
     amax = max16(amax);
+    none = sum16(none);
     const int e = __builtin_amdgcn_frexp_expf(amax);   // amax < 2^e; 0 for 0
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const int v = (int)__builtin_rintf(__builtin_amdgcn_ldexpf(x0[i], kBits - e));
+      const float whole = __builtin_rintf(__builtin_amdgcn_ldexpf(x0[i], kBits - e));
+      const int v = (int)fminf(fmaxf(whole, -0x1p22f), 0x1p22f);
       const int high = (v + 128) >> 8;   // 256 a + b
       sq[group][operand_byte<D>(j * E + i)] = (uint8_t)((high + 128) >> 8);
       sq[HT + group][operand_byte<D>(j * E + i)] = (uint8_t)high;
@@ -274,7 +279,7 @@ void attention_kernel(AttentionArgs a) {
     }
     // what a product of 16 c and the fixed point counts for in a score, log2
     const float cnorm = E == 4 ? 0.125f : (E == 8 ? 0.088388347648318447f : 0.0625f);
-    if (j == 0) sf[group] = __builtin_amdgcn_ldexpf(cnorm * 1.4426950408889634f, e - kBits - 4) * a.scale;
+    if (j == 0) sf[group] = __builtin_amdgcn_ldexpf(cnorm * 1.4426950408889634f, e - kBits - 4) * a.scale + none;
   }
   __syncthreads();
   // this lane's head, what its column counts for in a sum, and its operand rows
@@ -391,6 +396,7 @@ void attention_kernel(AttentionArgs a) {
           // what lies behind the last position may hold anything: it has weight 0 whatever its scale
           const float weight = p * scale_of<F32>(c.vs[t], i);
           x[t][i] = x[t][i] == kNone ? 0.0f : weight;
+          l = __builtin_fmaf(x[t][i], 0.0f, l);      // NaN for a weight that is not finite
           top = fmaxf(top, x[t][i]);
         }
     }

@@ -108,3 +108,35 @@ def test_outputs_are_the_rounded_ones(R, heads, dim, size, spread):
     check(torch.from_numpy(o), ref, bound, "f16")
     other = (o != torch.from_numpy(ref).half().numpy()).mean()
     assert other <= 0.02, f"{other:.3g} of the outputs are another number than the rounded result"
+
+
+@pytest.mark.parametrize("heads", [8, 14])                    # 4 and 7 query heads of a key-value head
+@pytest.mark.parametrize("sd", ["f16", "f32"])
+def test_what_is_not_finite_shows(R, sd, heads):
+    """A NaN or infinity in one query, or in a scale that a query sees, gives NaN for the heads that it takes part in, and those alone; also
+    where the sequence is split and only one part holds it."""
+    say("attention, not finite", sd, heads)
+    lens, each = [40, 3000, 1], heads // 2
+    cache = A.make(lens, 2, 128, 16, sd, seed=3)
+    c, table = device(R, cache)
+    n = ints(*lens)
+    q = torch.randn(3, heads, 128, device="cuda").half()
+    ref = R.rhtq_paged_attention(q, c, table, n)
+    assert torch.isfinite(ref).all()
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        for s, h, e in ((0, 0, 0), (1, heads - 1, 77), (2, each, 127)):
+            broken = q.clone()
+            broken[s, h, e] = bad
+            o = R.rhtq_paged_attention(broken, c, table, n)
+            assert torch.isnan(o[s, h]).all()
+            o[s, h] = ref[s, h]
+            assert torch.equal(o, ref)
+        for s, p, kv in ((0, 39, 0), (1, 5, 1), (1, 2999, 0), (1, 1500, 1)):
+            for which in (1, 3):
+                t = [x.clone() for x in c]
+                t[which][table[s, p // 16], kv, p % 16] = bad
+                o = R.rhtq_paged_attention(q, R.RhtqCache(*t), table, n)
+                if which == 3 or bad != bad:        # a key's scale of +-inf: scores of +-inf, NaN only where the largest is +inf
+                    assert torch.isnan(o[s, kv * each:(kv + 1) * each]).all(), (bad, s, p, kv, which)
+                o[s, kv * each:(kv + 1) * each] = ref[s, kv * each:(kv + 1) * each]
+                assert torch.equal(o, ref)

@@ -318,3 +318,22 @@ def test_windows_beyond_32_bits(R, huge):
         R.rhtq_pages_trim(table, lengths, refs, 16, window=-2 ** 32 + 5)
     with pytest.raises(R.RhtqError):
         R.rhtq_pages_reserve(table, lengths, refs, ints(1), 2 ** 32 + 16)
+
+
+@pytest.mark.parametrize("tokens", [1, 2, 3, 9, 61])
+@pytest.mark.parametrize("fmt,group", [("int4", 64), ("nvfp4", 16), ("mxfp4", 32)])
+def test_products_with_what_is_not_finite(R, fmt, group, tokens):
+    """A rotated value that is not finite gives NaN for its token, and for no other."""
+    say("matvec, not finite", fmt, tokens)
+    w = torch.randn(40, 512, device="cuda").bfloat16()
+    p, s, ts = R.rhtq_forward(w, None, fmt=fmt, group=group)
+    x = torch.randn(tokens, 512, device="cuda")
+    kw = dict(fmt=fmt, group=group, tensor_scale=ts, rotated=True)
+    ref = R.rhtq_matvec(p, s, x, **kw)
+    for bad, t, k in ((float("nan"), 0, 0), (float("inf"), tokens - 1, 511), (-float("inf"), tokens // 2, 100)):
+        b = x.clone()
+        b[t, k] = bad
+        y = R.rhtq_matvec(p, s, b, **kw)
+        assert torch.isnan(y[t]).all()
+        y[t] = ref[t]
+        assert torch.equal(y, ref)
