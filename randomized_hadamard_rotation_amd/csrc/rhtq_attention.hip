@@ -48,9 +48,9 @@ __device__ __forceinline__ void finish(const AttentionArgs& a, int64_t row, floa
   const int j = threadIdx.x & 15;
   const float cnorm = E == 4 ? 0.125f : (E == 8 ? 0.088388347648318447f : 0.0625f);
   const float f = l == 0.0f ? 0.0f : cnorm * __builtin_amdgcn_rcpf(l);   // NaN where l is
-  fwht16<E>(o);
 #pragma unroll
-  for (int i = 0; i < E; ++i) o[i] *= f;
+  for (int i = 0; i < E; ++i) o[i] *= f;   // before the transform, whose sums could overflow without it
+  fwht16<E>(o);
   apply_signs<E>(a.v_signs, j * E, o);
   store_row<T, E>(a.out, row * (16 * E) + j * E, o);
 }
@@ -258,6 +258,8 @@ void attention_kernel(AttentionArgs a) {
   // q: 16 lanes rotate a head and leave its bytes as operand rows h (a), HT + h (b) and 2 HT + h (c)
   if (group < HT) {
     apply_signs<E>(signs, x0);
+#pragma unroll
+    for (int i = 0; i < E; ++i) x0[i] *= 0.0625f;   // about 1 / sqrt(D), exactly: the transform's sums stay as small as the result
     fwht16<E>(x0);
     float amax = 0.0f, none = 0.0f;      // NaN where a value is not finite, which neither a maximum nor a whole number would show
 #pragma unroll
@@ -279,7 +281,7 @@ void attention_kernel(AttentionArgs a) {
     }
     // what a product of 16 c and the fixed point counts for in a score, log2
     const float cnorm = E == 4 ? 0.125f : (E == 8 ? 0.088388347648318447f : 0.0625f);
-    if (j == 0) sf[group] = __builtin_amdgcn_ldexpf(cnorm * 1.4426950408889634f, e - kBits - 4) * a.scale + none;
+    if (j == 0) sf[group] = __builtin_amdgcn_ldexpf(cnorm * 1.4426950408889634f, e - kBits) * a.scale + none;   // 16 / 16
   }
   __syncthreads();
   // this lane's head, what its column counts for in a sum, and its operand rows

@@ -140,3 +140,23 @@ def test_what_is_not_finite_shows(R, sd, heads):
                     assert torch.isnan(o[s, kv * each:(kv + 1) * each]).all(), (bad, s, p, kv, which)
                 o[s, kv * each:(kv + 1) * each] = ref[s, kv * each:(kv + 1) * each]
                 assert torch.equal(o, ref)
+
+
+@pytest.mark.parametrize("heads", [3, 6])
+@pytest.mark.parametrize("q_size,k_scale,scale,v_scale", [(1e37, 1e-30, 1e-7, 1.0), (1e-29, 1e25, 1e3, 1.0), (1.0, 1.0, 0.05, 1e35),
+                                                          (1.0, 1.0, 0.05, 1e-33), (1e36, 1e-36, 1.0, 1e-30)])
+def test_ends_of_the_types(R, heads, q_size, k_scale, scale, v_scale):
+    """Queries and scales near the ends of bf16 and fp32, scores of ordinary size: the result is as exact as for ordinary ones."""
+    say("attention, ends of the types", heads, q_size, k_scale, scale, v_scale)
+    n = 300
+    kc, ks, vc, vs, table = A.make([n], 1, 128, 16, "f32", seed=2)
+    vc[:, :, :, :] = 0x77                                       # every code 7: the rotated sum has all its weight in one element
+    vc[table[0, 3], 0, 5] = 0x99                                # but one row of -7
+    ks, vs = (ks * k_scale).astype(np.float32), (vs * v_scale).astype(np.float32)
+    cache = (kc, ks, vc, vs, table)
+    c, tb = device(R, cache)
+    q = torch.from_numpy(np.random.RandomState(1).randn(1, heads, 128) * q_size).to(torch.bfloat16)
+    o = R.rhtq_paged_attention(q.cuda(), c, tb, ints(n), scale=scale)
+    ref, bound = A.reference(q.double().numpy(), cache, [n], None, None, scale)
+    # elements that cancel to 0: fp32 sums of 128 values of the largest one's size
+    check(o, ref, bound + 2.0 ** -20 * np.abs(ref).max(-1), "bf16")
