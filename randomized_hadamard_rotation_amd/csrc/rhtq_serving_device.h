@@ -163,8 +163,4 @@ __device__ __forceinline__ int32_t load_uniform(const int32_t* p) {
   return *reinterpret_cast<const __attribute__((address_space(4))) int32_t*>(reinterpret_cast<uintptr_t>(p));
 }
 
-__device__ __forceinline__ float load_scale(const void* p, int64_t at, int dtype) {
-  return dtype == RHTQ_SCALE_F32 ? static_cast<const float*>(p)[at] : __half2float(static_cast<const __half*>(p)[at]);
-}
-
 }  // namespace rhtq

@@ -37,7 +37,7 @@ struct AttentionArgs {
   int64_t q_seq_stride;
   int64_t q_head_stride;
   void* out;
-  float* partial;             // [seqs][q_heads][splits][2 + head_dim]
+  float* partial;             // sums [seqs][q_heads][splits][head_dim], then maximum and sum of weights [seqs][q_heads][splits][2]
   const uint8_t* k_codes;
   const uint8_t* v_codes;
   const void* k_scales;
