@@ -303,7 +303,8 @@ int rhtq_pages_reserve(int32_t* table, int32_t width, int32_t* lengths, int32_t 
   const int st = page_args(table, width, lengths, seqs, refs, pages, page, a);
   if (st != RHTQ_OK) return st;
   if (!status || !aligned(status, 4)) return RHTQ_EINVAL;
-  if (seqs > 0 && (!lengths || !add || !aligned(add, 4) || (width > 0 && !table) || (pages > 0 && !refs))) return RHTQ_EINVAL;
+  if (pages > 0 && !refs) return RHTQ_EINVAL;      // free pages are counted whatever the sequences
+  if (seqs > 0 && (!lengths || !add || !aligned(add, 4) || (width > 0 && !table))) return RHTQ_EINVAL;
   if (!workspace_ok(workspace, workspace_bytes, rhtq_pages_workspace(pages, seqs, 0))) return RHTQ_EINVAL;
   a.add = add;
   a.status = status;
@@ -349,7 +350,8 @@ int rhtq_pages_fork(const rhtq_cache_t* cache, int32_t* table, int32_t width, in
   if (st != RHTQ_OK) return st;
   if (count < 0 || !status || !aligned(status, 4)) return RHTQ_EINVAL;
   if (count > 0 && (!src || !dst || !aligned(src, 4) || !aligned(dst, 4))) return RHTQ_EINVAL;
-  if (seqs > 0 && (!lengths || (width > 0 && !table) || (a.pages > 0 && !refs))) return RHTQ_EINVAL;
+  if (a.pages > 0 && !refs) return RHTQ_EINVAL;
+  if (seqs > 0 && (!lengths || (width > 0 && !table))) return RHTQ_EINVAL;
   if (!workspace_ok(workspace, workspace_bytes, rhtq_pages_workspace(a.pages, seqs, count))) return RHTQ_EINVAL;
   a.src = src;
   a.dst = dst;

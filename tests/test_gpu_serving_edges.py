@@ -337,3 +337,17 @@ def test_products_with_what_is_not_finite(R, fmt, group, tokens):
         assert torch.isnan(y[t]).all()
         y[t] = ref[t]
         assert torch.equal(y, ref)
+
+
+def test_page_calls_without_sequences(R):
+    """No sequence: nothing to do, and the calls say so."""
+    say("page calls without sequences")
+    cache = filled(R, 5, 2, 16, 64, 8)
+    before = [t.clone() for t in cache]
+    table, none, refs = torch.zeros((0, 3), dtype=torch.int32, device="cuda"), ints(), ints(0, 0, 2, 0, 0)
+    assert R.rhtq_pages_reserve(table, none, refs, none, 16).item() == 0
+    assert R.rhtq_pages_fork(cache, table, none, refs, none, none).item() == 0
+    R.rhtq_pages_free(table, none, refs, ints(0, 1))
+    R.rhtq_pages_trim(table, none, refs, 16, 4)
+    assert refs.tolist() == [0, 0, 2, 0, 0] and all(torch.equal(a, b) for a, b in zip(before, cache))
+    assert R.rhtq_pages_compact(cache, table, refs).item() == 1 and refs.tolist() == [2, 0, 0, 0, 0]

@@ -109,3 +109,10 @@ def test_row_strides():
         got, *s = serving._row_strides(x)
         assert got is not x and torch.equal(got, x)
         assert got.is_contiguous() and got.data_ptr() % 16 == 0 and tuple(s) == (x.shape[1] * x.shape[2], x.shape[2])
+
+
+def test_reference_counts_are_needed_without_sequences_too():
+    """Reserve and fork count the free pages whether or not there are sequences."""
+    L = R.lib
+    assert L.rhtq_pages_reserve(NIL, 3, NIL, 0, NIL, 10, 16, NIL, FAKE, FAKE, 1 << 30, NIL) == EINVAL
+    assert L.rhtq_pages_fork(cache(), NIL, 3, NIL, 0, NIL, NIL, NIL, 0, FAKE, FAKE, 1 << 30, NIL) == EINVAL
