@@ -46,7 +46,7 @@ __device__ __forceinline__ int64_t scan(int64_t v, int64_t& total) {
 __device__ __forceinline__ void stretch(int n, int& from, int& to) {
   const int per = (n + kPlan - 1) / kPlan;
   from = min((int)threadIdx.x * per, n);
-  to = min(from + per, n);
+  to = n - from < per ? n : from + per;
 }
 
 // Writes the lowest `want` free pages, in order, to list[0 ..]; returns how many free pages there are.

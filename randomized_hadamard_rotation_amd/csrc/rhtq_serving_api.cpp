@@ -94,6 +94,7 @@ int page_args(int32_t* table, int32_t width, int32_t* lengths, int32_t seqs, int
 int page_data(const rhtq_cache_t* c, rhtq::PagesArgs& a) {
   const int st = check_cache(c);
   if (st != RHTQ_OK) return st;
+  if (c->kv_heads > 65535) return RHTQ_EUNSUPPORTED;   // 16-byte words of a page's slots are counted in 32 bits
   if (c->pages > 0 && !cache_pointers(c, 16)) return RHTQ_EINVAL;
   a.data[0] = c->k_codes;
   a.data[1] = static_cast<uint8_t*>(c->k_scales);

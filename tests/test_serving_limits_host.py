@@ -116,3 +116,13 @@ def test_reference_counts_are_needed_without_sequences_too():
     L = R.lib
     assert L.rhtq_pages_reserve(NIL, 3, NIL, 0, NIL, 10, 16, NIL, FAKE, FAKE, 1 << 30, NIL) == EINVAL
     assert L.rhtq_pages_fork(cache(), NIL, 3, NIL, 0, NIL, NIL, NIL, 0, FAKE, FAKE, 1 << 30, NIL) == EINVAL
+
+
+def test_most_heads_of_a_page():
+    """65535 key-value heads, for page calls as for the others."""
+    L, many = R.lib, cache(kv_heads=65536)
+    assert L.rhtq_pages_copy(many, FAKE, FAKE, 2, NIL) == EUNS
+    assert L.rhtq_pages_fork(many, FAKE, 3, FAKE, 4, FAKE, FAKE, FAKE, 2, FAKE, FAKE, 1 << 30, NIL) == EUNS
+    assert L.rhtq_pages_compact(many, FAKE, 3, 4, FAKE, FAKE, FAKE, 1 << 30, NIL) == EUNS
+    assert L.rhtq_pages_copy(cache(kv_heads=65535), NIL, NIL, 0, NIL) == OK
+    assert append(many) == EUNS and read(many) == EUNS
