@@ -77,7 +77,7 @@ typedef struct {
 
 /* Rotate, quantise and store k, v [tokens][kv_heads][head_dim] (row strides in elements; head_dim contiguous, every row
  * 16-byte aligned).  signs: int8 [head_dim] +-1 or NULL.  Two rows of one call must not fall on the same slot, nor any on a page that
- * sequences share (rhtq_pages_reserve refuses room there). */
+ * sequences share (rhtq_pages_reserve refuses room there).  A row with a value that is not finite gets a NaN scale: it is read as NaN. */
 int rhtq_cache_append(const rhtq_cache_t* cache, const void* k, const void* v, int in_dtype, int64_t tokens,
                       int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
                       const int32_t* table, int32_t width, const int32_t* lengths, const int32_t* starts, int32_t seqs,

@@ -107,8 +107,9 @@ __device__ __forceinline__ void store_codes(const CacheArgs& a, int which, int64
   else if constexpr (E == 8) *reinterpret_cast<uint32_t*>(out) = w[0];
   else *reinterpret_cast<u32x2*>(out) = u32x2{w[0], w[1]};
   if (j == 0) {
-    if (a.scale_dtype == RHTQ_SCALE_F32) static_cast<float*>(a.scales[which])[slot] = sc.s;
-    else static_cast<__half*>(a.scales[which])[slot] = __float2half_rn(fminf(sc.s, 65504.0f));
+    // every element of a rotated row holds each of the row's values, so that the first one is not finite where one of them is not: a NaN scale
+    if (a.scale_dtype == RHTQ_SCALE_F32) static_cast<float*>(a.scales[which])[slot] = __builtin_fmaf(v[0], 0.0f, sc.s);
+    else static_cast<__half*>(a.scales[which])[slot] = __float2half_rn(__builtin_fmaf(v[0], 0.0f, fminf(sc.s, 65504.0f)));
   }
 }
 

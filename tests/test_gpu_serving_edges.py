@@ -351,3 +351,26 @@ def test_page_calls_without_sequences(R):
     R.rhtq_pages_trim(table, none, refs, 16, 4)
     assert refs.tolist() == [0, 0, 2, 0, 0] and all(torch.equal(a, b) for a, b in zip(before, cache))
     assert R.rhtq_pages_compact(cache, table, refs).item() == 1 and refs.tolist() == [2, 0, 0, 0, 0]
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("sd", ["f16", "f32"])
+def test_rows_that_are_not_finite(R, dim, dtype, sd):
+    """A NaN or an infinity anywhere in a row: the row's scale is NaN, and it is read as NaN; the other rows are as they were."""
+    say("rows that are not finite", dim, dtype, sd)
+    x = torch.randn(40, 2, dim, device="cuda").to(dtype)
+    table, lengths, starts = torch.tensor([[3, 0, 5]], dtype=torch.int32, device="cuda"), ints(40), ints(0, 40)
+    good, bad = (filled(R, 6, 2, 16, dim, 6, scale_dtype=sd) for _ in range(2))
+    R.rhtq_cache_append(good, x, x, table, lengths, starts)
+    broken = x.clone()
+    rows = [(0, 0, 0, float("nan")), (17, 1, dim - 1, float("inf")), (39, 0, dim // 2 + 3, -float("inf")), (39, 1, 5, float("nan"))]
+    for t, h, e, value in rows:
+        broken[t, h, e] = value
+    R.rhtq_cache_append(bad, broken, x, table, lengths, starts)
+    k, v = R.rhtq_cache_read(bad, table, lengths, starts, 40, dtype=dtype)
+    ref = R.rhtq_cache_read(good, table, lengths, starts, 40, dtype=dtype)
+    for t, h, _, _ in rows:
+        assert torch.isnan(k[t, h]).all(), (t, h)
+        k[t, h] = ref[0][t, h]
+    assert torch.equal(k, ref[0]) and torch.equal(v, ref[1])
