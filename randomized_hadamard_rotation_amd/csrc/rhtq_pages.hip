@@ -20,26 +20,36 @@ constexpr int kCopyBlocks = 4096;      // most workgroups of a copy; they stride
 constexpr int kSeqBlocks = 1 << 20;    // and of a kernel with one workgroup a sequence: a grid holds fewer than 2^32 threads along x
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
-// Sum over the workgroup before this thread (exclusive) and in all; every thread calls it.
-__device__ __forceinline__ int64_t scan(int64_t v, int64_t& total) {
-  __shared__ int64_t wave_sum[kPlan / 64];
+// N sums over the workgroup at once: v becomes the sum before this thread, total that of all; every thread calls it.
+template <int N>
+__device__ __forceinline__ void scan(int64_t (&v)[N], int64_t (&total)[N]) {
+  __shared__ int64_t wave_sum[N][kPlan / 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int64_t x = v;
+  int64_t x[N];
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t o = __shfl_up(x, d);
-    if (lane >= d) x += o;
-  }
-  if (lane == 63) wave_sum[wave] = x;
+  for (int k = 0; k < N; ++k) x[k] = v[k];
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int64_t o = __shfl_up(x[k], d);
+      if (lane >= d) x[k] += o;
+    }
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    if (lane == 63) wave_sum[k][wave] = x[k];
   __syncthreads();
-  int64_t before = 0;
-  total = 0;
-  for (int i = 0; i < kPlan / 64; ++i) {
-    if (i < wave) before += wave_sum[i];
-    total += wave_sum[i];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    int64_t before = 0;
+    total[k] = 0;
+    for (int i = 0; i < kPlan / 64; ++i) {
+      if (i < wave) before += wave_sum[k][i];
+      total[k] += wave_sum[k][i];
+    }
+    v[k] = before + x[k] - v[k];
   }
   __syncthreads();
-  return before + x - v;
 }
 
 // Stretch of `n` items that this thread looks after: neighbouring ones, so that its rank is the items' own order.
@@ -49,19 +59,22 @@ __device__ __forceinline__ void stretch(int n, int& from, int& to) {
   to = n - from < per ? n : from + per;
 }
 
-// Writes the lowest `want` free pages, in order, to list[0 ..]; returns how many free pages there are.
-__device__ __forceinline__ int64_t list_free(const PagesArgs& a, int32_t* list, int64_t want) {
+// Free pages of this thread's stretch.
+__device__ __forceinline__ int count_free(const PagesArgs& a) {
   int from, to;
   stretch(a.pages, from, to);
   int mine = 0;
   for (int p = from; p < to; ++p) mine += a.refs[p] <= 0;
-  int64_t total;
-  int64_t at = scan(mine, total);
-  if (total >= want)
-    for (int p = from; p < to && at < want; ++p)
-      if (a.refs[p] <= 0) list[at++] = p;
+  return mine;
+}
+
+// Writes the lowest `want` free pages, in order, to list[0 ..]; `at` free ones lie before this thread's stretch.
+__device__ __forceinline__ void list_free(const PagesArgs& a, int32_t* list, int64_t at, int64_t want) {
+  int from, to;
+  stretch(a.pages, from, to);
+  for (int p = from; p < to && at < want; ++p)
+    if (a.refs[p] <= 0) list[at++] = p;
   __syncthreads();
-  return total;
 }
 
 // An entry that names no page, whatever it holds.
@@ -93,14 +106,14 @@ __global__ __launch_bounds__(kPlan) void reserve_kernel(PagesArgs a) {
         else if (a.refs[e] > 1) bad = 1;     // new rows would overwrite another sequence's
       }
   }
-  int64_t wanted, over;
-  int64_t at = scan(mine, wanted);
-  scan(beyond, over);
-  const int64_t have = list_free(a, a.work, wanted);
-  int64_t short_of = over + (wanted > have ? wanted - have : 0);
+  int64_t sums[3] = {mine, beyond, count_free(a)}, all[3];
+  scan(sums, all);
+  const int64_t wanted = all[0], have = all[2];
+  int64_t at = sums[0], short_of = all[1] + (wanted > have ? wanted - have : 0);
   if (short_of > INT32_MAX) short_of = INT32_MAX;
   if (threadIdx.x == 0) a.status[0] = bad ? -1 : (int32_t)short_of;
   if (bad || short_of) return;
+  list_free(a, a.work, sums[2], wanted);
   for (int s = from; s < to; ++s) {
     if (a.add[s] == 0) continue;
     const int64_t len = a.lengths[s], need = slots_of(len + a.add[s], a.page);
@@ -176,11 +189,13 @@ __global__ __launch_bounds__(kPlan) void fork_kernel(PagesArgs a) {
     const int32_t len = a.lengths[a.src[i]];
     mine += len % a.page && page_at(a.table + (int64_t)a.src[i] * a.width, a.width, a.pages, len / a.page) >= 0;
   }
-  int64_t wanted;
-  int64_t at = scan(mine, wanted);
-  const int64_t have = list_free(a, a.work, wanted);
+  int64_t sums[2] = {mine, count_free(a)}, all[2];
+  scan(sums, all);
+  const int64_t wanted = all[0], have = all[1];
+  int64_t at = sums[0];
   if (threadIdx.x == 0) a.status[0] = wanted > have ? (int32_t)(wanted - have) : 0;
   if (wanted > have) return;
+  list_free(a, a.work, sums[1], wanted);
   for (int i = from; i < to; ++i) {
     const int32_t len = a.lengths[a.src[i]];
     const int last = page_at(a.table + (int64_t)a.src[i] * a.width, a.width, a.pages, len / a.page);
@@ -261,16 +276,19 @@ __global__ __launch_bounds__(kPlan) void compact_kernel(PagesArgs a) {
   stretch(a.pages, from, to);
   int mine = 0;
   for (int p = from; p < to; ++p) mine += a.refs[p] > 0;
-  int64_t live;
-  scan(mine, live);
+  int64_t used_before[1] = {mine}, used_in_all[1];
+  scan(used_before, used_in_all);
+  const int64_t live = used_in_all[0];
   int holes = 0, movers = 0;
   for (int p = from; p < to; ++p) {
     const bool used = a.refs[p] > 0;
     holes += !used && p < live;
     movers += used && p >= live;
   }
-  int64_t moves, same;
-  int64_t h = scan(holes, same), m = scan(movers, moves);
+  int64_t sums[2] = {holes, movers}, all[2];
+  scan(sums, all);
+  int64_t h = sums[0], m = sums[1];
+  const int64_t moves = all[1];
   int32_t* pairs = a.work + 1;
   int32_t* place = pairs + 2 * (a.pages / 2 + 1);
   for (int p = from; p < to; ++p) {
