@@ -19,7 +19,7 @@
 //
 // Two bytes (16 bits) of q and of the weights took the same time with up to 4 heads and 29.7 us where 64 / 8 heads x 4096 positions now take
 // 31.7, but one fp16 output in 5 was then another number than the rounded result, for 1 in 200 now.
-// Measured: 32 x 32 heads x 4096 positions 98 us (554 MB, 5.6 TB/s; a copy moves 5.1); one sequence of 131072 with 8 key-value heads 27 us
+// Measured: 32 x 32 heads x 4096 positions 98 us (554 MB, 5.6 TB/s; a sum reads 5.7); one sequence of 131072 with 8 key-value heads 27 us
 // and 4 us to join (4.3 TB/s); 515 positions of 32 heads 7.8 us, a chain of length, table, codes and the end's exchange.
 #include <type_traits>
 

@@ -15,7 +15,7 @@
 //  r and h in int32.  The scale leaves the transform, which is exact; it and the signs are applied to the result.
 //
 // The 16 tokens' slots lie side by side in a page, so that a page's lines are written whole by one XCD's cache.
-// Now 189 us to store and 168 us to read those rows: bounded by the vector instructions (about 630 for 16 rows stored) and by the chain of
+// Now 190 us to store and 162 us to read those rows: bounded by the vector instructions (about 630 for 16 rows stored) and by the chain of
 // lookups, which two tiles a wave share.  32 tokens x 8 heads: 6.3 and 5.8 us, that chain.
 #include "rhtq_internal.h"
 #include "rhtq_serving_device.h"

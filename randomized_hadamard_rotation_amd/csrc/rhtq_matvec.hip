@@ -314,8 +314,8 @@ __device__ __forceinline__ float whole(const MatvecArgs& a, int exponent, float 
 }
 
 // ---- few tokens: one tile of 16 rows per workgroup, k split over its waves -----------------------------------------------------
-// 4096 x 4096, 1 token 5.4 us; 24576 x 4096 20 us (2.5 TB/s); 12288 x 4096 NVFP4, 4 tokens 12.8 us: the life of a workgroup is one wait for
-// its loads, of which x's operands are four for each of the codes'.
+// 4096 x 4096, 1 token 5.7 us; 24576 x 4096 20 us (2.5 TB/s); 12288 x 4096, 4 tokens NVFP4 12.4 us, MXFP4 20.8: the life of a workgroup is
+// one wait for its loads, of which x's operands are four for each of the codes'.
 
 constexpr int kWaves = 8;
 constexpr int kAhead = 4;          // steps whose codes and operands are in flight
@@ -326,7 +326,8 @@ constexpr int kOwnWidth = 4096;
 constexpr int64_t kAcross = 1 << 22;   // row tiles in a grid's x, the rest in y: x times its 512 threads stays below 2^32
 
 // OWN: x fp32 is split by every workgroup for itself, in LDS, while its codes are on their way, which saves a launch; otherwise the halves
-// lie ready.
+// lie ready.  MXFP4's steps over far blocks would take 139 registers; four waves a SIMD, with four values spilled there, took 27.2 us for
+// the call at 12288 x 4096, 4 tokens, three waves 28.0.
 template <int MODE, bool F32, bool OWN>
 __global__ __launch_bounds__(64 * kWaves, MODE == MMX ? 4 : 1) void narrow_kernel(MatvecArgs a) {
   __shared__ f32x4 part[kWaves][64];

@@ -374,3 +374,72 @@ def test_rows_that_are_not_finite(R, dim, dtype, sd):
         assert torch.isnan(k[t, h]).all(), (t, h)
         k[t, h] = ref[0][t, h]
     assert torch.equal(k, ref[0]) and torch.equal(v, ref[1])
+
+
+def test_lengths_near_31_bits(R):
+    """The longest sequence there can be, every page of it the same one but for the last: attention, with and without a window, is that of
+    a few pages; rows are stored and read at its end."""
+    say("lengths near 31 bits")
+    page, dim, width = 256, 64, 2 ** 23 - 1               # 2^31 - 256 positions
+    cache = filled(R, 5, 1, page, dim, 14)
+    table = torch.full((1, width), 3, dtype=torch.int32, device="cuda")
+    n = width * page
+    lengths = torch.tensor([n], dtype=torch.int64).to(torch.int32).cuda()
+    with pytest.raises(R.RhtqError):                      # width * page = 2^31 - 256 is one too many
+        R.rhtq_paged_attention(torch.zeros(1, 2, dim, device="cuda", dtype=torch.bfloat16), cache, table, lengths)
+    table, n = table[:, :-1].contiguous(), n - page
+    lengths = ints(n)
+    q = torch.randn(1, 2, dim, device="cuda", dtype=torch.bfloat16)
+    one = torch.tensor([[3]], dtype=torch.int32, device="cuda")
+    o, ref = R.rhtq_paged_attention(q, cache, table, lengths).float(), R.rhtq_paged_attention(q, cache, one, ints(page)).float()
+    # a wave adds up 4096 equal chunks in fp32: 2^-12 of the result's size before the rounding of both to bf16
+    assert ((o - ref).abs() <= 2.0 ** -7 * ref.abs() + 2.0 ** -10 * ref.norm(dim=-1, keepdim=True)).all()
+    table[0, -1] = 1
+    x = torch.randn(2, 1, 1, dim, device="cuda", dtype=torch.bfloat16)
+    R.rhtq_cache_append(cache, x[0], x[1], table, lengths)
+    near = torch.tensor([[3, 3, 1]], dtype=torch.int32, device="cuda")
+    for got, want in zip(R.rhtq_cache_read(cache, table, lengths, None, 1), R.rhtq_cache_read(cache, near, ints(3 * page), None, 1)):
+        assert (got != 0).any() and torch.equal(got, want)
+    for window, sinks in ((300, 0), (17, 40), (513, 256)):
+        o = R.rhtq_paged_attention(q, cache, table, lengths, window=window, sinks=sinks)
+        few = torch.tensor([[3, 3, 3, 3, 1]], dtype=torch.int32, device="cuda")
+        want = R.rhtq_paged_attention(q, cache, few, ints(5 * page), window=window, sinks=sinks)
+        # the same positions in other chunks: one bf16 step at most, and 2^-14 where a value cancels to next to nothing
+        assert ((o - want).float().abs() <= 2.0 ** -7 * want.float().abs() + 2.0 ** -14).all(), (window, sinks)
+
+
+def test_most_sequences_of_a_query_call(R):
+    say("65535 sequences")
+    cache = filled(R, 4, 1, 16, 64, 15)
+    seqs = 65535
+    table = torch.randint(0, 4, (seqs, 1), dtype=torch.int32, device="cuda")
+    lengths = torch.randint(0, 17, (seqs,), dtype=torch.int32, device="cuda")
+    q = torch.randn(3, 64, device="cuda", dtype=torch.float16).expand(seqs, 3, 64)
+    o = R.rhtq_paged_attention(q, cache, table, lengths)
+    t, n = (torch.arange(68, device="cuda") // 17).int(), (torch.arange(68, device="cuda") % 17).int()
+    every = R.rhtq_paged_attention(q[:68], cache, t[:, None].contiguous(), n)
+    assert torch.equal(o, every[(table[:, 0] * 17 + lengths).long()])
+    with pytest.raises(R.RhtqError):
+        R.rhtq_paged_attention(q[:1].expand(seqs + 1, 3, 64), cache, table[:1].expand(seqs + 1, 1).contiguous(), lengths[:1].expand(seqs + 1).contiguous())
+
+
+@pytest.mark.parametrize("tokens", [1, 4, 9])
+@pytest.mark.parametrize("fmt,group", [("int4", 0), ("nvfp4", 16), ("mxfp4", 32)])
+def test_widest_rows(R, fmt, group, tokens):
+    """n = 2^20, taken rotated."""
+    say("widest rows", fmt, tokens)
+    n, rows = 2 ** 20, 3
+    rs = np.random.RandomState(tokens)
+    p = O.pack_nibbles(rs.randint(0, 16, (rows, n))).astype(np.uint8)
+    ts = np.float32(0.5) if fmt == "nvfp4" else None
+    s = {"int4": lambda: np.array([[0.5], [2.0], [0.125]], dtype=np.float32), "nvfp4": lambda: O.e4m3_encode(1 + rs.rand(rows, n // 16)).astype(np.uint8),
+         "mxfp4": lambda: rs.randint(120, 132, (rows, n // 32)).astype(np.uint8)}[fmt]()
+    w = O.dequantize(p, s, fmt, group, ts)
+    x = torch.from_numpy(rs.randn(tokens, n)).float()
+    y = R.rhtq_matvec(torch.from_numpy(p).cuda(), torch.from_numpy(s).cuda(), x.cuda(), fmt=fmt, rotated=True,
+                      tensor_scale=None if ts is None else torch.tensor([float(ts)], device="cuda")).double().cpu().numpy()
+    x = x.double().numpy()
+    ref = x @ w.T
+    allowed = product_bound(x, w, n) * (1 + 2.0 ** -23) + 2.0 ** -23 * np.abs(ref)
+    # that bound grows with n; the roundings of up to 2^13 steps add up as a random walk does: 2^-24 * 2^6.5, with a factor of 3 for chance
+    assert (np.abs(y - ref) <= allowed).all() and np.linalg.norm(y - ref) <= 2.0 ** -16 * np.linalg.norm(ref)
