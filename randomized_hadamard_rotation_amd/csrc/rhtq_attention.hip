@@ -209,8 +209,9 @@ __device__ __forceinline__ int operand_byte(int d) {
   else return ((2 * (d >> 7) + (d & 1)) * 4 + ((d & 127) >> 5)) * 16 + ((d & 31) >> 1);
 }
 
-// Waves a SIMD; a workgroup is two.  Four: 32 x 32 heads x 4096 positions 96 us, with three 106 (fp32 scales 98 and 106).  Three: 48 x 8
-// heads, ragged, with a window 20.4 us for 22.6 (both types), and 64 / 8 heads 31.4 us for 36.6, where four spill.  head_dim 256 needs the
+// Waves a SIMD; a workgroup is two.  Four against three: 32 x 32 heads x 4096 positions 96 us against 106 (fp32 scales 98 against 106);
+// 48 x 8 heads, ragged, with a window 22.6 against 20.4 (both types of scales); 64 / 8 heads, where four spill, 36.6 against 31.4.  So 8
+// heads take three; of up to 4, fp16 scales take four for the batch, fp32 ones three for the ragged lengths.  head_dim 256 needs the
 // registers of two.
 constexpr int waves_of(int E, bool F32, int HT) { return E == 16 ? 2 : (F32 || HT == 8 ? 3 : 4); }
 

@@ -160,3 +160,31 @@ def test_ends_of_the_types(R, heads, q_size, k_scale, scale, v_scale):
     ref, bound = A.reference(q.double().numpy(), cache, [n], None, None, scale)
     # elements that cancel to 0: fp32 sums of 128 values of the largest one's size
     check(o, ref, bound + 2.0 ** -20 * np.abs(ref).max(-1), "bf16")
+
+
+@pytest.mark.parametrize("heads", [6, 14])
+def test_captured_calls_replay_as_eager(R, heads):
+    """Split and joined, captured into two graphs, replayed in turn with eager calls and other lengths between."""
+    say("attention, captured", heads)
+    lens = [6000, 70, 0]
+    cache = A.make(lens, 2, 128, 16, "f16", seed=4)
+    c, table = device(R, cache)
+    sets = [(torch.randn(3, heads, 128, device="cuda").half(), ints(*lens)) for _ in range(2)]
+    graphs, outs = [], []
+    for q, n in sets:
+        R.rhtq_paged_attention(q, c, table, n)
+    torch.cuda.synchronize()
+    for q, n in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(R.rhtq_paged_attention(q, c, table, n))
+        graphs.append(g)
+    for turn in range(4):
+        for q, n in sets:
+            q.mul_(0.5 + turn)
+            n.copy_(ints(6000 - 777 * turn, 70 - turn, turn))
+        for g in graphs:
+            g.replay()
+        want = [R.rhtq_paged_attention(q, c, table, n) for q, n in sets]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)), turn
