@@ -168,14 +168,16 @@ def _int32(t, name, shape):
 
 def _rows16(t):
     """t contiguous from an address of 16 bytes on: a copy where it is not (views may start anywhere)."""
+    if t.is_contiguous() and not t.data_ptr() & 15:
+        return t
     t = t.contiguous()
-    return t if t.data_ptr() % 16 == 0 else t.clone()
+    return t.clone() if t.data_ptr() & 15 else t
 
 
 def _signs(signs, n, x):
     """Device int8 [n] (marshalling only)."""
     if signs is None or (type(signs) is torch.Tensor and signs.dtype is _I8 and signs.dim() == 1 and signs.shape[0] == n
-                         and signs.is_contiguous() and signs.get_device() == x.get_device() and signs.data_ptr() % 16 == 0):
+                         and signs.is_contiguous() and signs.get_device() == x.get_device() and not signs.data_ptr() & 15):
         return signs
     return _rows16(_signs_tensor(signs, n, x.device))
 
@@ -236,7 +238,12 @@ def rhtq_matvec(packed, scales, x, signs=None, fmt: str = "int4", group: int = 0
     _one_device(index, {"x": x, "packed": packed, "scales": scales, "tensor_scale": tensor_scale, "out": out})
     on = _On(index)
     try:
-        xc, pc, sc = _rows16(x), _rows16(packed), _rows16(scales)
+        xc, pc, sc = x, packed, scales
+        xp, pp, sp = x.data_ptr(), packed.data_ptr(), scales.data_ptr()
+        if (xp | pp) & 15 or sp & 1 or not (x.is_contiguous() and packed.is_contiguous() and scales.is_contiguous()):
+            xc, pc = _rows16(x), _rows16(packed)
+            sc = _rows16(scales) if sp & 1 else scales.contiguous()          # E4M3 bytes are loaded in pairs, others one by one
+            xp, pp, sp = xc.data_ptr(), pc.data_ptr(), sc.data_ptr()
         s = None if rotated else _signs(signs, n, x)
         own = out is None
         if own:
@@ -245,8 +252,8 @@ def rhtq_matvec(packed, scales, x, signs=None, fmt: str = "int4", group: int = 0
         work = x.new_empty(need, dtype=_U8)
         if stream is not None:
             on.follow(stream)
-        _check(lib.rhtq_matvec(xc.data_ptr(), in_type, tokens, n, n if block is None else block, _p(s), rotated,
-                               pc.data_ptr(), sc.data_ptr(), _p(tensor_scale), rows, _FMT[fmt], group, _SCALE[scale_dtype],
+        _check(lib.rhtq_matvec(xp, in_type, tokens, n, n if block is None else block, _p(s), rotated,
+                               pp, sp, _p(tensor_scale), rows, _FMT[fmt], group, _SCALE[scale_dtype],
                                out.data_ptr(), out_type, work.data_ptr(), need, on.raw), "rhtq_matvec")
         on.keep(xc if xc is not x else None, pc if pc is not packed else None, sc if sc is not scales else None, s, work,
                 out if own else None)
@@ -276,9 +283,12 @@ def _row_strides(x):
     may be anything."""
     per16 = 16 // x.element_size()
     tokens, heads, dim = x.shape
-    of_token = x.stride(0) if tokens > 1 else 0
-    of_head = x.stride(1) if heads > 1 else 0
-    if x.stride(2) != 1 or of_token % per16 or of_head % per16 or x.data_ptr() % 16:
+    of_token, of_head, of_value = x.stride()
+    if tokens < 2:
+        of_token = 0
+    if heads < 2:
+        of_head = 0
+    if of_value != 1 or of_token % per16 or of_head % per16 or x.data_ptr() & 15:
         return x.clone(memory_format=torch.contiguous_format), heads * dim, dim
     return x, of_token, of_head
 
