@@ -1,0 +1,94 @@
+/*
+ * rhtq_products.h -- products of rows that are quantised on both sides, dense and grouped by expert, and the norm in front
+ * of them that makes such rows (gfx950).
+ *
+ * The calls ship in librhtq.so beside those of rhtq.h and serving/rhtq_serving.h and share their status codes, type codes and
+ * conventions: device pointers owned by the caller, nothing allocated or kept, only kernels enqueued on `stream` (so every call can be
+ * captured into a HIP graph), arguments checked on the host before any HIP call.  Scratch memory is the caller's too; its contents need
+ * not be kept between calls and are undefined afterwards.  Two calls that may run at the same time need workspaces of their own.
+ *
+ * Rows rotated by the same R can be multiplied as they lie: (R x) . (R w) = x . w (QuaRot reviews page, review 1 Summary: weights,
+ * activations and cache in 4 bits; reviewer 2 follow-up: activations are quantised with nearest rounding).
+ */
+#ifndef RHTQ_PRODUCTS_H
+#define RHTQ_PRODUCTS_H
+
+#include <stdint.h>
+
+#include "../rhtq.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define RHTQ_PRODUCTS_VERSION 1
+int rhtq_products_version(void);
+
+/* 8-bit formats, besides the 4-bit ones of rhtq.h. */
+#define RHTQ_FMT_INT8  3      /* symmetric absmax INT8, codes int8, scales as INT4's (max|y|/127)              */
+#define RHTQ_FMT_MXFP8 4      /* E4M3 codes, E8M0 block-32 scales (OCP MX v1.0): e = floor(log2 max|y|) - 8    */
+
+/*
+ * Quantised rows.
+ *   codes         [rows][n/2] bytes as rhtq_forward packs them (INT4, NVFP4, MXFP4), or [rows][n] bytes (INT8, MXFP8); 16-byte aligned
+ *   scales        [rows][n/group] of scale_dtype, aligned to its element
+ *   tensor_scale  NVFP4: one fp32 (grouped weights: one for each expert)
+ *   fmt, group, scale_dtype  INT4, INT8: group 0 (one a row) or a power of two >= 16 dividing n, fp32 or fp16; NVFP4 16, E4M3; MXFP4 and
+ *                 MXFP8 32, E8M0
+ */
+typedef struct {
+  const void* codes;
+  const void* scales;
+  const float* tensor_scale;
+  int32_t fmt;
+  int32_t group;
+  int32_t scale_dtype;
+} rhtq_rows_t;
+
+/*
+ * y[t][r] = sum_k a[t][k] w[r][k] of the values that the codes stand for: with both sides rotated alike, x W^T.
+ *   a          [tokens] rows: INT4 or INT8 with INT4 weights, NVFP4 with NVFP4, MXFP4 or MXFP8 with MXFP4; groups of a and w may differ
+ *   w          [rows] rows
+ *   y_out      [tokens][rows] in out_dtype (RHTQ_IN_BF16, RHTQ_IN_F16 or RHTQ_IN_F32), 16-byte aligned
+ *   workspace  rhtq_matmul_workspace(...) bytes, 16-byte aligned
+ * n: a multiple of 32 up to 2^20; tokens up to 2^20, rows up to 2^24, tokens * rows up to 2^36 (0: nothing to do).  Products of codes are exact, sums are in fp32 (of
+ * INT4 and INT8 within a group: in 32-bit integers); a tensor scale is applied to the sum.  A scale that is not finite shows in the
+ * results that it takes part in.
+ */
+int64_t rhtq_matmul_workspace(int64_t tokens, int32_t n, int64_t rows, int a_fmt);
+int rhtq_matmul(const rhtq_rows_t* a, int64_t tokens, int32_t n, const rhtq_rows_t* w, int64_t rows, void* y_out, int out_dtype,
+                void* workspace, int64_t workspace_bytes, rhtq_stream_t stream);
+
+/*
+ * The same product with weights by expert:  y[i][r] = sum_k a[index[i]][k] w[e][r][k]  for starts[e] <= i < starts[e + 1].
+ *   a          [a_rows] rows; index int32 [tokens] names the row of a for each row of y (NULL: row i, a_rows >= tokens).  An index outside
+ *              [0, a_rows) is no row: its results are zeros
+ *   w          [experts][rows] rows, an expert's after the other's
+ *   starts     int32 [experts + 1], ascending; what lies outside [0, tokens] counts as its nearer end.  Read on the device only
+ *   y_out      [tokens][rows]; rows before starts[0] and from starts[experts] on are left as they were
+ * experts 1 to 32767, the rest as in rhtq_matmul.  No workspace.
+ */
+int rhtq_grouped_matmul(const rhtq_rows_t* a, int64_t a_rows, int64_t tokens, int32_t n, const rhtq_rows_t* w, int32_t experts, int64_t rows,
+                        const int32_t* starts, const int32_t* index, void* y_out, int out_dtype, rhtq_stream_t stream);
+
+/*
+ * Residual, norm, rotation and quantisation in one pass, row by row:
+ *   h = x + residual, rounded to their type and stored to residual_out (residual NULL: h = x, residual_out unused)
+ *   y = h * weight / sqrt(mean(h^2) + eps)        (weight [n] of x's type, or NULL: folded into what follows)
+ *   block > 0:  y <- (I (x) H_block) diag(signs) y / sqrt(block);  block 0: no rotation, signs unused
+ *   codes_out, scales_out: y in `fmt` (INT4, NVFP4, MXFP4 as rhtq_forward, INT8, MXFP8 as above; a zero group: scale 0, E8M0 byte 0,
+ *   codes 0).  tensor_scale (NVFP4) is read: a scale over all rows would need them twice.
+ *   x, residual, residual_out  [tokens][n] bf16, fp16 or fp32, rows contiguous, 16-byte aligned; residual_out may be residual or x
+ * n: a multiple of 32 up to 32768; block a power of two, 16 to n, dividing n; groups lie inside a block (INT4 and INT8 group 0, one a
+ * row: any block) and, where they are not one a row, hold up to 32768 values.  eps is finite and not negative.  The mean, the norm and
+ * the rotation are in fp32.  A row of zeros with eps 0, or with a value that is not finite, has unspecified codes.
+ */
+int rhtq_norm_forward(const void* x, const void* residual, void* residual_out, int in_dtype, int64_t tokens, int32_t n, const void* weight,
+                      float eps, const int8_t* signs, int32_t block, int fmt, int32_t group, int scale_dtype, void* codes_out,
+                      void* scales_out, const float* tensor_scale, rhtq_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* RHTQ_PRODUCTS_H */

@@ -384,6 +384,8 @@ try:   # the serving calls are typed by torch; without torch the host helpers ab
     from .serving import (EXPORTED_SERVING, RhtqCache, rhtq_cache_append, rhtq_cache_new, rhtq_cache_read,  # noqa: F401
                           rhtq_matvec, rhtq_paged_attention, rhtq_pages_compact, rhtq_pages_copy, rhtq_pages_fork,
                           rhtq_pages_free, rhtq_pages_reserve, rhtq_pages_trim, rhtq_serving_version)
+    from .products import (EXPORTED_PRODUCTS, RHTQ_FMT_INT8, RHTQ_FMT_MXFP8, RhtqRows, rhtq_grouped_matmul,  # noqa: F401
+                           rhtq_matmul, rhtq_norm_forward, rhtq_products_version)
 except ImportError as _e:
     if _e.name != "torch":
         raise

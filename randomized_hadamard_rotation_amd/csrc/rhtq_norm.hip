@@ -1,0 +1,298 @@
+// Residual, root-mean-square norm, rotation and quantisation of one row per workgroup, in one pass:
+//   h = round(x + residual),  y = h w / sqrt(mean(h^2) + eps),  y <- (I (x) H_b) diag(s) y / sqrt(b),  codes and scales of y.
+// The row stays in registers between its load and its codes, so that the bytes of x, residual and codes bound the call.
+//
+// Thread t holds values 8 (i NT + t) .. + 7 of chunk i, NT threads: bits 0-2 of a value's place are a register, 3-8 the lane, the next ones
+// the wave and the highest the chunk.  A stage of the Walsh-Hadamard transform is an addition in registers, one across lanes (DPP, or for
+// lane bits 4 and 5 a swap of half rows between two registers and back), or one across waves through LDS.
+#include "rhtq_internal.h"
+#include "rhtq_products_internal.h"
+#include "rhtq_serving_device.h"
+
+namespace rhtq {
+namespace {
+
+constexpr int kMostWaves = 16;
+
+__device__ __forceinline__ void lane_stage4(float& a, float& b) {
+  auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  const float s = __uint_as_float(p[0]) + __uint_as_float(p[1]), d = __uint_as_float(p[0]) - __uint_as_float(p[1]);
+  p = __builtin_amdgcn_permlane16_swap(__float_as_uint(s), __float_as_uint(d), false, false);
+  a = __uint_as_float(p[0]);
+  b = __uint_as_float(p[1]);
+}
+__device__ __forceinline__ void lane_stage5(float& a, float& b) {
+  auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  const float s = __uint_as_float(p[0]) + __uint_as_float(p[1]), d = __uint_as_float(p[0]) - __uint_as_float(p[1]);
+  p = __builtin_amdgcn_permlane32_swap(__float_as_uint(s), __float_as_uint(d), false, false);
+  a = __uint_as_float(p[0]);
+  b = __uint_as_float(p[1]);
+}
+
+// Largest (or sum) of a wave's values in every lane, in one order.
+template <bool SUM>
+__device__ __forceinline__ float wave_all(float v) {
+  auto put = [](float a, float b) { return SUM ? a + b : fmaxf(a, b); };
+  v = put(v, lane_xor16<0>(v));
+  v = put(v, lane_xor16<1>(v));
+  v = put(v, lane_xor16<2>(v));
+  v = put(v, lane_xor16<3>(v));
+  auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = put(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return put(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+
+__device__ __forceinline__ uint32_t pack_int4(const float (&c)[8]) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w |= ((uint32_t)(int)c[j] & 15u) << (4 * j);
+  return w;
+}
+
+template <int T, int HELD>
+__global__ __launch_bounds__(64 * kMostWaves) void norm_kernel(NormArgs a) {
+  extern __shared__ __attribute__((aligned(16))) float exchange[];     // the row, where a stage crosses waves
+  __shared__ float wave_sum[kMostWaves];
+  __shared__ float granule[HELD * kMostWaves];                         // largest of 512 values
+  const int nt = blockDim.x, t = threadIdx.x, waves = nt >> 6, wave = t >> 6, lane = t & 63;
+  const int64_t row = blockIdx.x, base = row * a.n;
+  float v[HELD][8];
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < HELD; ++i) {
+    const int e = 8 * (i * nt + t);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+    if (e < a.n) {
+      load_row<T, 8>(a.x, base + e, v[i]);
+      if (a.residual) {
+        float u[8];
+        load_row<T, 8>(a.residual, base + e, u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v[i][j] += u[j];
+          if constexpr (T == RHTQ_IN_BF16) v[i][j] = __uint_as_float(to16<T>(v[i][j]) << 16);
+          if constexpr (T == RHTQ_IN_F16) v[i][j] = __half2float(__ushort_as_half((uint16_t)to16<T>(v[i][j])));
+        }
+        store_row<T, 8>(a.residual_out, base + e, v[i]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(v[i][j], v[i][j], sum);
+  }
+  sum = wave_all<true>(sum);
+  if (waves > 1) {
+    if (lane == 0) wave_sum[wave] = sum;
+    __syncthreads();
+    sum = 0.0f;
+    for (int w = 0; w < waves; ++w) sum += wave_sum[w];
+  }
+  const bool lost = !(sum < __builtin_inff());                         // an infinity or NaN in the row: its scales are NaN
+  float r = 1.0f / __builtin_sqrtf(sum / (float)a.n + a.eps);
+  if (a.block_log >= 0) r *= a.block_log & 1 ? __builtin_ldexpf(0.70710678118654752f, -(a.block_log >> 1)) : __builtin_ldexpf(1.0f, -(a.block_log >> 1));
+#pragma unroll
+  for (int i = 0; i < HELD; ++i) {
+    const int e = 8 * (i * nt + t);
+    if (e >= a.n) continue;
+    float w[8];
+    if (a.weight) load_row<T, 8>(a.weight, e, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] *= a.weight ? r * w[j] : r;
+    if (a.block_log >= 0 && a.signs) apply_signs<8>(a.signs, e, v[i]);
+  }
+
+  if (a.block_log >= 0) {
+    const int wave_bits = 31 - __builtin_clz(waves);
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+#pragma unroll
+      for (int h = 1; h < 8; h *= 2)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if ((j & h) == 0) bfly(v[i][j], v[i][j | h]);
+      lane_stage16<0>(v[i]);                                           // blocks are of 16 values at least
+      if (a.block_log > 4) lane_stage16<1>(v[i]);
+      if (a.block_log > 5) lane_stage16<2>(v[i]);
+      if (a.block_log > 6) lane_stage16<3>(v[i]);
+      if (a.block_log > 7)
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) lane_stage4(v[i][j], v[i][j + 1]);
+      if (a.block_log > 8)
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) lane_stage5(v[i][j], v[i][j + 1]);
+    }
+    // two wave bits at a time: everybody's values to LDS, and the sums of four partners back
+    const int crossed = a.block_log - 9 < wave_bits ? a.block_log - 9 : wave_bits;
+    for (int bit = 0; bit < crossed; bit += 2) {
+      const bool two = bit + 1 < crossed;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < HELD; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; j += 4)
+          *reinterpret_cast<f32x4*>(exchange + 4 * ((2 * i + j / 4) * nt + t)) = f32x4{v[i][j], v[i][j + 1], v[i][j + 2], v[i][j + 3]};
+      __syncthreads();
+      const int step = 64 << bit;
+      const float s1 = t & step ? -1.0f : 1.0f, s2 = t & (2 * step) ? -1.0f : 1.0f;
+#pragma unroll
+      for (int i = 0; i < HELD; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+          const float* from = exchange + 4 * ((2 * i + j / 4) * nt);
+          const f32x4 p = *reinterpret_cast<const f32x4*>(from + 4 * (t ^ step));
+          f32x4 u, w = {0.0f, 0.0f, 0.0f, 0.0f};
+          if (two) {
+            const f32x4 p0 = *reinterpret_cast<const f32x4*>(from + 4 * (t ^ (2 * step))), p1 = *reinterpret_cast<const f32x4*>(from + 4 * (t ^ (3 * step)));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = __builtin_fmaf(s1, p0[k], p1[k]);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            u[k] = __builtin_fmaf(s1, v[i][j + k], p[k]);              // this thread's half: own + other, or other - own
+            v[i][j + k] = two ? __builtin_fmaf(s2, u[k], w[k]) : u[k];
+          }
+        }
+    }
+#pragma unroll
+    for (int h = 1; h < HELD; h *= 2)
+      if (a.block_log > 9 + wave_bits + (h > 1))
+#pragma unroll
+        for (int i = 0; i < HELD; ++i)
+          if ((i & h) == 0)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) bfly(v[i][j], v[i | h][j]);
+  }
+
+  // largest of every group, in all of its lanes
+  float top[HELD];
+#pragma unroll
+  for (int i = 0; i < HELD; ++i) {
+    float m = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, __builtin_fabsf(v[i][j]));
+    if (a.group_log < 0 || a.group_log >= 9) {
+      m = wave_all<false>(m);
+    } else {
+      m = fmaxf(m, lane_xor16<0>(m));
+      if (a.group_log > 4) m = fmaxf(m, lane_xor16<1>(m));
+      if (a.group_log > 5) m = fmaxf(m, lane_xor16<2>(m));
+      if (a.group_log > 6) m = fmaxf(m, lane_xor16<3>(m));
+      if (a.group_log > 7) {
+        auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(m), __float_as_uint(m), false, false);
+        m = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+      }
+    }
+    top[i] = m;
+  }
+  if (a.group_log < 0 || a.group_log > 9) {
+#pragma unroll
+    for (int i = 0; i < HELD; ++i)
+      if (lane == 0) granule[i * waves + wave] = top[i];
+    __syncthreads();
+    const int span = a.group_log < 0 ? HELD * waves : 1 << (a.group_log - 9);
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+      const int first = a.group_log < 0 ? 0 : (i * waves + wave) & -span;
+      float m = 0.0f;
+      for (int g = 0; g < span && first + g < HELD * waves; ++g) m = fmaxf(m, granule[first + g]);
+      top[i] = m;
+    }
+  }
+
+  const int groups = a.group_log < 0 ? 1 : a.n >> a.group_log;
+  const int mask = a.group_log < 0 ? -1 : (1 << a.group_log) - 1;
+#pragma unroll
+  for (int i = 0; i < HELD; ++i) {
+    const int e = 8 * (i * nt + t);
+    if (e >= a.n) continue;
+    const bool first = (e & mask) == 0;                                // this thread stores the group's scale
+    const int64_t at = row * groups + (a.group_log < 0 ? 0 : e >> a.group_log);
+    if (a.fmt == RHTQ_FMT_INT4 || a.fmt == RHTQ_FMT_INT8) {
+      const bool four = a.fmt == RHTQ_FMT_INT4;
+      const float s = lost ? __builtin_nanf("") : top[i] / (four ? 7.0f : 127.0f);
+      const __half h = __float2half_rn(s > 65504.0f ? 65504.0f : s);
+      const float kept = a.f32 ? s : __half2float(h);
+      if (first) {
+        if (a.f32) reinterpret_cast<float*>(a.scales)[at] = s;
+        else reinterpret_cast<__half*>(a.scales)[at] = h;
+      }
+      const float inv = kept > 0.0f ? 1.0f / kept : 0.0f, most = four ? 7.0f : 127.0f;
+      float c[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) c[j] = __builtin_rintf(__builtin_amdgcn_fmed3f(v[i][j] * inv, -most - 1.0f, most));
+      if (four) {
+        *reinterpret_cast<uint32_t*>(a.codes + (base + e) / 2) = pack_int4(c);
+      } else {
+        u32x2 w = {0u, 0u};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j / 4] |= ((uint32_t)(int)c[j] & 255u) << (8 * (j % 4));
+        *reinterpret_cast<u32x2*>(a.codes + base + e) = w;
+      }
+    } else if (a.fmt == RHTQ_FMT_MXFP8) {
+      const int x = top[i] > 0.0f ? (int)(__float_as_uint(top[i]) >> 23) - 127 - 8 : -127;
+      const int ex = x < -127 ? -127 : x;
+      if (first) reinterpret_cast<uint8_t*>(a.scales)[at] = lost ? 0xFF : (uint8_t)(ex + 127);
+      u32x2 w;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float c[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[j] = __builtin_amdgcn_fmed3f(__builtin_amdgcn_ldexpf(v[i][4 * k + j], -ex), -448.0f, 448.0f);
+        int u = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
+        w[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], u, true);
+      }
+      *reinterpret_cast<u32x2*>(a.codes + base + e) = w;
+    } else {
+      float inv;
+      if (a.fmt == RHTQ_FMT_MXFP4) {
+        const int ex = mx_exponent(top[i]);
+        inv = top[i] > 0.0f ? __builtin_ldexpf(1.0f, -ex) : 0.0f;
+        if (first) reinterpret_cast<uint8_t*>(a.scales)[at] = lost ? 0xFF : (uint8_t)(ex + 127);
+      } else {
+        const float g = a.tensor[0];
+        const uint32_t code = g > 0.0f ? e4m3_code(top[i] / (6.0f * g)) : 0u;
+        const float s = e4m3_value(code) * g;
+        inv = s > 0.0f ? 1.0f / s : 0.0f;
+        if (first) reinterpret_cast<uint8_t*>(a.scales)[at] = lost ? 0x7F : (uint8_t)code;
+      }
+      uint32_t w = 0;
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[i][0] * inv, v[i][1] * inv, 1.0f, 0);
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[i][2] * inv, v[i][3] * inv, 1.0f, 1);
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[i][4] * inv, v[i][5] * inv, 1.0f, 2);
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[i][6] * inv, v[i][7] * inv, 1.0f, 3);
+      *reinterpret_cast<uint32_t*>(a.codes + (base + e) / 2) = inv > 0.0f ? w : 0u;
+    }
+  }
+}
+
+template <int T, int HELD>
+hipError_t go(const NormArgs& a, int threads, hipStream_t s) {
+  const int wave_bits = 31 - __builtin_clz(threads / 64);
+  const size_t lds = a.block_log > 9 && wave_bits > 0 ? sizeof(float) * 8 * HELD * threads : 0;
+  if (lds > 65536) {
+    const hipError_t e = hipFuncSetAttribute((const void*)norm_kernel<T, HELD>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((norm_kernel<T, HELD>), dim3((unsigned)a.tokens), dim3(threads), lds, s, a);
+  return hipGetLastError();
+}
+
+template <int T>
+hipError_t by_width(const NormArgs& a, hipStream_t s) {
+  if (a.n <= 512) return go<T, 1>(a, 64, s);
+  if (a.n <= 1024) return go<T, 2>(a, 64, s);
+  int threads = 64;
+  while (32 * threads < a.n) threads *= 2;
+  return go<T, 4>(a, threads, s);
+}
+
+}  // namespace
+
+hipError_t launch_norm(int dtype, const NormArgs& a, hipStream_t s) {
+  if (dtype == RHTQ_IN_BF16) return by_width<RHTQ_IN_BF16>(a, s);
+  if (dtype == RHTQ_IN_F16) return by_width<RHTQ_IN_F16>(a, s);
+  return by_width<RHTQ_IN_F32>(a, s);
+}
+
+}  // namespace rhtq

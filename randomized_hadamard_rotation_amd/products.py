@@ -1,0 +1,269 @@
+"""Products of rows that are quantised on both sides, dense and grouped by expert, and the norm in front of them.
+
+The functions carry the names of the C entry points in include/serving/rhtq_products.h and, like the others, only marshal arguments:
+torch provides device memory and the current HIP stream, every step runs in the library's kernels, and nothing is read back to the
+host.  They are exported by the package itself.
+"""
+from __future__ import annotations
+
+import ctypes
+import struct
+from typing import NamedTuple
+
+import torch
+
+from . import _FMT, _SCALE, _check, _expect, lib
+from .serving import _I32, _IN, _U8, _On, _int32, _one_device, _p, _rows16, _signs
+
+EXPORTED_PRODUCTS = ["rhtq_products_version", "rhtq_matmul_workspace", "rhtq_matmul", "rhtq_grouped_matmul", "rhtq_norm_forward"]
+
+RHTQ_FMT_INT8, RHTQ_FMT_MXFP8 = 3, 4
+_FMT8 = {**_FMT, "int8": RHTQ_FMT_INT8, "mxfp8": RHTQ_FMT_MXFP8}
+_GROUP = {"nvfp4": 16, "mxfp4": 32, "mxfp8": 32}
+_SCALE_NAME = {"nvfp4": "e4m3", "mxfp4": "e8m0", "mxfp8": "e8m0"}
+_SCALE_DTYPE = {"f32": torch.float32, "f16": torch.float16, "e4m3": torch.uint8, "e8m0": torch.uint8}
+_SCALE_CODE = {torch.float32: _SCALE["f32"], torch.float16: _SCALE["f16"]}
+_WHOLE = ("int4", "int8")
+_PAIR = {"int4": "int4", "int8": "int4", "nvfp4": "nvfp4", "mxfp4": "mxfp4", "mxfp8": "mxfp4"}
+
+# rhtq_rows_t as bytes, which a pointer argument takes as they are
+_pack_rows = struct.Struct("@3P3i").pack
+
+
+class _RowsStruct(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("tensor_scale", ctypes.c_void_p), ("fmt", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("scale_dtype", ctypes.c_int32)]
+
+
+def _declare():
+    vp, i32, i64, ci, fl = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+    args = {
+        "rhtq_products_version": (ci, []),
+        "rhtq_matmul_workspace": (i64, [i64, i32, i64, ci]),
+        "rhtq_matmul": (ci, [vp, i64, i32, vp, i64, vp, ci, vp, i64, vp]),
+        "rhtq_grouped_matmul": (ci, [vp, i64, i64, i32, vp, i32, i64, vp, vp, vp, ci, vp]),
+        "rhtq_norm_forward": (ci, [vp, vp, vp, ci, i64, i32, vp, fl, vp, i32, ci, i32, ci, vp, vp, vp, vp]),
+    }
+    for name, (res, types) in args.items():
+        f = getattr(lib, name)
+        f.restype, f.argtypes = res, types
+
+
+_declare()
+
+
+class RhtqRows(NamedTuple):
+    """Quantised rows, as rhtq_forward or rhtq_norm_forward gives them: codes uint8 [.., rows, n/2] (INT4, NVFP4, MXFP4), int8 (INT8) or
+    uint8 (MXFP8) [.., rows, n]; scales [.., rows, n/group]; tensor_scale float32 for NVFP4.  With a leading axis: an expert's weights after
+    the other's (tensor_scale [experts])."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    tensor_scale: torch.Tensor | None = None
+    fmt: str = "int4"
+    group: int = 0
+
+
+class _Side:
+    """Rows after their checks: sizes and what keeps the memory alive."""
+    __slots__ = ("rows", "lead", "n", "group", "scale", "codes", "scales", "tensor", "fmt")
+
+    def __init__(self, r, name, dims):
+        codes, scales, tensor, fmt, group = r
+        code = _FMT8.get(fmt)
+        if code is None:
+            raise ValueError(f"{name}: unknown fmt {fmt!r}")
+        shape = codes.shape
+        if len(shape) != dims:
+            raise ValueError(f"{name}.codes must be {dims}-D")
+        if codes.dtype is not (torch.int8 if fmt == "int8" else _U8):
+            raise ValueError(f"{name}.codes: {codes.dtype}, expected {'int8' if fmt == 'int8' else 'uint8'}")
+        n = shape[-1] if code >= RHTQ_FMT_INT8 else 2 * shape[-1]
+        group = group or _GROUP.get(fmt, 0)
+        each = group or n
+        if group < 0 or each == 0 or n % each:
+            raise ValueError(f"{name}: group {group} does not divide n = {n}")
+        want = (*shape[:-1], n // each)
+        if fmt in _WHOLE:
+            self.scale = _SCALE_CODE.get(scales.dtype)
+            if self.scale is None:
+                raise ValueError(f"{name}.scales: {scales.dtype}, expected float16 or float32")
+        else:
+            self.scale = _SCALE[_SCALE_NAME[fmt]]
+            if scales.dtype is not _U8:
+                raise ValueError(f"{name}.scales: {scales.dtype}, expected uint8")
+        if scales.shape != want:
+            raise ValueError(f"{name}.scales: {tuple(scales.shape)}, expected {want}")
+        self.lead = shape[0] if dims == 3 else 1
+        if fmt == "nvfp4":
+            if tensor is None:
+                raise ValueError(f"{name}: NVFP4 needs its tensor_scale")
+            if tensor.dtype != torch.float32 or tensor.numel() != self.lead:
+                raise ValueError(f"{name}.tensor_scale must be float32 with {self.lead} entries")
+        else:
+            tensor = None
+        self.rows, self.n, self.group, self.fmt = shape[-2], n, group, fmt
+        self.codes, self.scales, self.tensor = codes, scales, tensor
+
+    def packed(self):
+        """rhtq_rows_t as bytes; codes from 16 bytes on, scales and the tensor scale contiguous (copies where they are not)."""
+        if not self.codes.is_contiguous() or self.codes.data_ptr() & 15:
+            self.codes = _rows16(self.codes)
+        if not self.scales.is_contiguous():
+            self.scales = self.scales.contiguous()
+        if self.tensor is not None and not self.tensor.is_contiguous():
+            self.tensor = self.tensor.contiguous()
+        return _pack_rows(self.codes.data_ptr(), self.scales.data_ptr(), _p(self.tensor) or 0, _FMT8[self.fmt], self.group, self.scale)
+
+    def held(self, r):
+        """What packed() copied."""
+        return [t for t, u in ((self.codes, r.codes), (self.scales, r.scales), (self.tensor, r.tensor_scale)) if t is not None and t is not u]
+
+
+def _product(a, w, out, out_dtype, tokens, dims):
+    sa, sw = _Side(a, "a", 2), _Side(w, "w", dims)
+    if sa.n != sw.n:
+        raise ValueError(f"a has rows of {sa.n} values, w of {sw.n}")
+    if _PAIR[sa.fmt] != sw.fmt:
+        raise ValueError(f"{sa.fmt} rows are multiplied with {_PAIR[sa.fmt]} weights: got {sw.fmt}")
+    if tokens is None:
+        tokens = sa.rows
+    if out is not None:
+        out_dtype = out.dtype
+    kind = _IN.get(out_dtype)
+    if kind is None:
+        raise ValueError("out_dtype must be bfloat16, float16 or float32")
+    if out is not None:
+        _expect(out, "out", out_dtype, (tokens, sw.rows))
+    return sa, sw, kind, out_dtype
+
+
+def _tensors(a, w):
+    return {"a.codes": a.codes, "a.scales": a.scales, "a.tensor_scale": a.tensor_scale if a.fmt == "nvfp4" else None, "w.codes": w.codes,
+            "w.scales": w.scales, "w.tensor_scale": w.tensor_scale if w.fmt == "nvfp4" else None}
+
+
+def rhtq_products_version() -> int:
+    return lib.rhtq_products_version()
+
+
+def rhtq_matmul(a: RhtqRows, w: RhtqRows, out=None, out_dtype=torch.bfloat16, stream=None):
+    """y [tokens][rows] = a [tokens] rows times the transpose of w [rows] rows, both quantised and rotated alike (or not): INT4 or INT8 with
+    INT4 weights, NVFP4 with NVFP4, MXFP4 or MXFP8 with MXFP4.  Groups of a and w may differ.  y has out's type, or out_dtype."""
+    sa, sw, kind, out_dtype = _product(a, w, out, out_dtype, None, 2)
+    tokens, rows, n = sa.rows, sw.rows, sa.n
+    index = a.codes.get_device()
+    _one_device(index, {**_tensors(a, w), "out": out})
+    on = _On(index)
+    try:
+        pa, pw = sa.packed(), sw.packed()
+        own = out is None
+        if own:
+            out = a.codes.new_empty((tokens, rows), dtype=out_dtype)
+        need = lib.rhtq_matmul_workspace(tokens, n, rows, _FMT8[sa.fmt])
+        work = a.codes.new_empty(need, dtype=_U8) if need else None
+        if stream is not None:
+            on.follow(stream)
+        _check(lib.rhtq_matmul(pa, tokens, n, pw, rows, out.data_ptr(), kind, _p(work), need, on.raw), "rhtq_matmul")
+        if on.stream is not None:
+            on.keep(*sa.held(a), *sw.held(w), work, out if own else None)
+    finally:
+        on.leave()
+    return out
+
+
+def rhtq_grouped_matmul(a: RhtqRows, w: RhtqRows, starts, index=None, out=None, out_dtype=torch.bfloat16, stream=None):
+    """y [tokens][rows], y[i] = a[index[i]] times the transpose of w[e], for starts[e] <= i < starts[e + 1]: w holds [experts][rows] rows,
+    starts is int32 [experts + 1], ascending, index int32 [tokens] (None: row i of a).  An index outside a's rows gives zeros.  Rows of y before
+    starts[0] or from starts[experts] on are left as they were (without `out`: unspecified).  Formats as in rhtq_matmul."""
+    if starts.dim() != 1 or (index is not None and index.dim() != 1):
+        raise ValueError("starts and index must be 1-D")
+    tokens = a.codes.shape[0] if index is None else index.shape[0]
+    sa, sw, kind, out_dtype = _product(a, w, out, out_dtype, tokens, 3)
+    rows, experts = sw.rows, sw.lead
+    _int32(starts, "starts", (experts + 1,))
+    if index is not None:
+        _int32(index, "index", (tokens,))
+    where = a.codes.get_device()
+    _one_device(where, {**_tensors(a, w), "starts": starts, "index": index, "out": out})
+    on = _On(where)
+    try:
+        pa, pw = sa.packed(), sw.packed()
+        own = out is None
+        if own:
+            out = a.codes.new_empty((tokens, rows), dtype=out_dtype)
+        if stream is not None:
+            on.follow(stream)
+        _check(lib.rhtq_grouped_matmul(pa, sa.rows, tokens, sa.n, pw, experts, rows, starts.data_ptr(), _p(index), out.data_ptr(), kind,
+                                       on.raw), "rhtq_grouped_matmul")
+        if on.stream is not None:
+            on.keep(*sa.held(a), *sw.held(w), out if own else None)
+    finally:
+        on.leave()
+    return out
+
+
+def rhtq_norm_forward(x, weight=None, residual=None, eps: float = 1e-5, signs=None, block: int = 0, fmt: str = "int8", group: int = 0,
+                      scale_dtype: str | None = None, tensor_scale=None, residual_out=None, stream=None):
+    """(rows, h): h = x + residual (of their type; None without a residual), and RhtqRows of h * weight / sqrt(mean(h^2) + eps), rotated
+    block by block if block > 0 ((I (x) H_block) diag(signs) / sqrt(block); block = n: the whole row, a power of two).  x, residual [tokens][n]
+    and weight [n] (None: ones) are all bfloat16, float16 or float32.  fmt 'int4', 'int8' (group 0: one scale a row; scale_dtype 'f32' or
+    'f16'), 'nvfp4' (tensor_scale is given, float32 [1]), 'mxfp4' or 'mxfp8'.  residual_out may be residual or x."""
+    code = _FMT8.get(fmt)
+    if code is None:
+        raise ValueError(f"unknown fmt {fmt!r}")
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D [tokens][n]")
+    kind = _IN.get(x.dtype)
+    if kind is None:
+        raise ValueError("x must be bfloat16, float16 or float32")
+    tokens, n = shape = x.shape
+    group = group or _GROUP.get(fmt, 0)
+    if scale_dtype is None:
+        scale_dtype = _SCALE_NAME.get(fmt, "f32")
+    scale_type = _SCALE_DTYPE.get(scale_dtype)
+    if scale_type is None:
+        raise ValueError(f"unknown scale_dtype {scale_dtype!r}")
+    each = group or n
+    if group < 0 or each == 0 or n % each:
+        raise ValueError(f"group {group} does not divide n = {n}")
+    if fmt == "nvfp4":
+        if tensor_scale is None:
+            raise ValueError("NVFP4 needs its tensor_scale: it is not computed here")
+        if tensor_scale.dtype != torch.float32 or tensor_scale.numel() != 1:
+            raise ValueError("tensor_scale must be one float32")
+    else:
+        tensor_scale = None
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out without a residual")
+    elif residual.dtype is not x.dtype or residual.shape != shape:
+        raise ValueError(f"residual: {residual.dtype} {tuple(residual.shape)}, expected {x.dtype} {tuple(shape)}")
+    if residual_out is not None:
+        _expect(residual_out, "residual_out", x.dtype, shape)
+        if residual_out.data_ptr() & 15:
+            raise ValueError("residual_out must be 16-byte aligned")
+    if weight is not None and (weight.dtype is not x.dtype or weight.shape != shape[1:]):
+        raise ValueError(f"weight: {weight.dtype} {tuple(weight.shape)}, expected {x.dtype} {(n,)}")
+    index = x.get_device()
+    _one_device(index, {"x": x, "weight": weight, "residual": residual, "tensor_scale": tensor_scale, "residual_out": residual_out})
+    on = _On(index)
+    try:
+        xc, rc = _rows16(x), residual if residual is None else _rows16(residual)
+        wc = weight if weight is None else _rows16(weight)
+        s = _signs(signs, n, x) if block else None
+        h = residual_out
+        if residual is not None and h is None:
+            h = x.new_empty(shape)
+        wide = code >= RHTQ_FMT_INT8
+        codes = x.new_empty((tokens, n if wide else n // 2), dtype=torch.int8 if fmt == "int8" else _U8)
+        scales = x.new_empty((tokens, n // each), dtype=scale_type)
+        if stream is not None:
+            on.follow(stream)
+        _check(lib.rhtq_norm_forward(xc.data_ptr(), _p(rc), _p(h), kind, tokens, n, _p(wc), eps, _p(s), block, code, group,
+                                     _SCALE[scale_dtype], codes.data_ptr(), scales.data_ptr(), _p(tensor_scale), on.raw), "rhtq_norm_forward")
+        if on.stream is not None:
+            on.keep(xc if xc is not x else None, rc if rc is not residual else None, wc if wc is not weight else None, s, codes, scales,
+                    h if residual_out is None else None)
+    finally:
+        on.leave()
+    return RhtqRows(codes, scales, tensor_scale, fmt, group), h
