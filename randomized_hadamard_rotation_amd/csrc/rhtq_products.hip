@@ -38,7 +38,8 @@ constexpr bool kWhole = K == KI4 || K == KI8;
 template <int K>
 constexpr int kActBytes = K == KI8 || K == KM8 ? kStep : kStepBytes;   // of a row of activations in a step
 
-// How INT scales apply.  SUB: parts of a step with scales of their own; 0: one scale a row on both sides, applied at the end.
+// How INT scales apply.  SUB: parts of a step with scales of their own; 0: one scale a row on both sides, applied at the end.  ONE: one scale a
+// row of the activations, applied at the end, and groups of at least 128 for the weights (SUB 1).
 template <int K, int SUB>
 constexpr int kScaleWords = kWhole<K> ? (SUB ? SUB : 1) : (K == KNV ? 2 : 1);   // dwords of a row's scales in a step, as LDS holds them
 
@@ -210,7 +211,8 @@ __device__ __forceinline__ i32x4 whole_sum(const X& x, const Y& y, i32x4 c, int 
 template <int K>
 constexpr float kWholeUnit = K == KI4 ? 1.0f / 256.0f : 1.0f / 16.0f;
 
-// Values of the last step that lie behind the row's end: out of the activations' operand.
+// Values that lie behind the row's end, of whose last step `left` are there: out of the activations' operand.  In every step, without a branch:
+// behind a branch round such a block the compiler does not count the wait states of the instruction before it.
 template <int K, bool ACT>
 __device__ __forceinline__ void cut_tail(u32x4* raw, int left) {
   const int q = (threadIdx.x & 63) >> 4;
@@ -273,8 +275,8 @@ __device__ __forceinline__ bool find_span(const ProductArgs& p, int slot, int si
 }
 
 // Row of a for row t of y, -1: none.
-__device__ __forceinline__ int64_t row_of(const ProductArgs& p, int64_t t) {
-  if (!p.index) return t;
+__device__ __forceinline__ int32_t row_of(const ProductArgs& p, int64_t t) {
+  if (!p.index) return (int32_t)t;
   const int32_t i = p.index[t];
   return i >= 0 && i < p.a_rows ? i : -1;
 }
@@ -287,23 +289,23 @@ __device__ __forceinline__ void store_one(const ProductArgs& p, int64_t t, int64
 }
 
 // Four results next to each other; r a multiple of 4.
+template <int T>
 __device__ __forceinline__ void store_four(const ProductArgs& p, int64_t t, int64_t r, f32x4 v) {
-  if ((p.rows & 3) != 0) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (r + i < p.rows) store_one(p, t, r + i, v[i]);
+  const int64_t at = t * p.rows + r;
+  if ((p.rows & 3) == 0) {
+    if constexpr (T == RHTQ_IN_F32) {
+      *reinterpret_cast<f32x4*>(static_cast<float*>(p.y) + at) = v;
+    } else {
+      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.y) + at) = u32x2{to16<T>(v[0]) | to16<T>(v[1]) << 16, to16<T>(v[2]) | to16<T>(v[3]) << 16};
+    }
     return;
   }
-  const int64_t at = t * p.rows + r;
-  if (p.out_dtype == RHTQ_IN_F32) {
-    *reinterpret_cast<f32x4*>(static_cast<float*>(p.y) + at) = v;
-  } else {
-    const bool bf = p.out_dtype == RHTQ_IN_BF16;
-    uint32_t h[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = bf ? to16<RHTQ_IN_BF16>(v[i]) : to16<RHTQ_IN_F16>(v[i]);
-    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.y) + at) = u32x2{h[0] | h[1] << 16, h[2] | h[3] << 16};
-  }
+  for (int i = 0; i < 4; ++i)
+    if (r + i < p.rows) {
+      if constexpr (T == RHTQ_IN_F32) static_cast<float*>(p.y)[at + i] = v[i];
+      else static_cast<uint16_t*>(p.y)[at + i] = (uint16_t)to16<T>(v[i]);
+    }
 }
 
 // ---- tiles: codes through LDS ----------------------------------------------------------------------------------------------------
@@ -319,225 +321,398 @@ __device__ __forceinline__ void fetch16(const void* from, void* to) {
 // Where 16-byte piece c of row r stands in its row: 16 lanes that read the same piece of 16 rows meet 64 different banks.
 template <int BYTES>
 __device__ __forceinline__ int placed(int r, int c) {
-  return BYTES == 64 ? c ^ ((r >> 2) & 3) : c ^ ((r >> 1) & 7);
+  return BYTES == 64 ? c ^ ((r >> 2) & 3) : (BYTES == 128 ? c ^ ((r >> 1) & 7) : c ^ (r & 15));
 }
 
 // Block id to tile: blocks of one XCD (every eighth) take neighbouring tiles, in bands of token tiles, so that an XCD's L2 serves each row of
 // codes to several of its workgroups.
-__device__ __forceinline__ void tile_of(int64_t id, int64_t all, int row_tiles, int token_tiles, int& rt, int& tt) {
-  constexpr int XCDS = 8, BAND = 8;
-  const int64_t each = all / XCDS, more = all % XCDS, xcd = id % XCDS;
-  const int64_t at = xcd * each + (xcd < more ? xcd : more) + id / XCDS;
-  const int64_t band_size = (int64_t)BAND * row_tiles;
+__device__ __forceinline__ void tile_of(uint32_t id, uint32_t all, int row_tiles, int token_tiles, int& rt, int& tt) {
+  constexpr uint32_t XCDS = 8, BAND = 8;
+  const uint32_t each = all / XCDS, more = all % XCDS, xcd = id % XCDS;
+  const uint32_t at = xcd * each + (xcd < more ? xcd : more) + id / XCDS;
+  const uint32_t band_size = BAND * row_tiles;
   const int band = (int)(at / band_size), in = (int)(at % band_size);
-  const int first = band * BAND, height = token_tiles - first < BAND ? token_tiles - first : BAND;
+  const int first = band * (int)BAND, height = token_tiles - first < (int)BAND ? token_tiles - first : (int)BAND;
   tt = first + in % height;
   rt = in / height;
 }
 
-// FR x FT tiles of 16 weight rows x 16 tokens a wave, WR x WT waves.
-template <int K, int SUB, int FR, int FT, int WR, int WT>
-__global__ __launch_bounds__(64 * WR * WT) void tile_kernel(ProductArgs p, int row_tiles, int token_tiles) {
-  constexpr int WAVES = WR * WT, TR = 16 * FR * WR, TT = 16 * FT * WT;
-  constexpr int AB = kActBytes<K>, WORDS = kScaleWords<K, SUB>;
-  constexpr int CODES = TR * kStepBytes + TT * AB;                 // bytes of a step's codes
-  constexpr int PIECES_W = TR * kStepBytes / 1024, PIECES = CODES / 1024;   // of a wave's 64 x 16 bytes
-  constexpr int MINE = (PIECES + WAVES - 1) / WAVES;
+// FR x FT tiles of 16 weight rows x 16 tokens a wave, WR x WT waves.  A stage is KS steps (two where a row's 128 bytes fit: whole cache lines);
+// BUFS stages' codes lie in LDS, one being worked on, the next ones there or on their way.  Scales come for BS steps at a time, so that a
+// row's are one request, a block ahead.  WA row tiles' codes are read from LDS ahead of their products.
+template <int K, int SUB, bool ONE, int KS, int BUFS, int BS, int FR, int FT, int WR, int WT, int WA>
+__global__ __launch_bounds__(64 * WR * WT, 2) void tile_kernel(ProductArgs p, int row_tiles, int token_tiles) {
+  constexpr int WAVES = WR * WT, THREADS = 64 * WAVES, TR = 16 * FR * WR, TT = 16 * FT * WT, ROWS = TR + TT;
+  constexpr int WB = KS * kStepBytes, AB = KS * kActBytes<K>, WORDS = kScaleWords<K, SUB>;
+  constexpr bool WIDE_A = kActBytes<K> == kStep;                   // 8-bit activations
+  constexpr int CODES = TR * WB + TT * AB;                         // bytes of a stage's codes
+  constexpr int PIECES_W = TR * WB / 1024, PIECES = CODES / 1024;  // of a wave's 64 x 16 bytes
+  constexpr int MINE = PIECES / WAVES;
+  static_assert(PIECES % WAVES == 0, "");
+  constexpr int SLOTS = KS * FR / 2, EACH = (MINE + SLOTS - 1) / SLOTS;   // pieces asked for after one row tile's products, in the first half
   constexpr bool SCALES = !(kWhole<K> && SUB == 0);
-  __shared__ __attribute__((aligned(16))) uint8_t codes[2][CODES];
-  __shared__ __attribute__((aligned(16))) uint32_t scales[2][SCALES ? (TR + TT) * WORDS : 4];
+  constexpr int BLOCK = BS / KS;                                   // stages of a block of scales
+  constexpr int SCALED = ONE ? TR : ROWS;                          // rows whose scales are needed on the way
+  // INT: thread u has step u % BS of rows u / BS + i * SCALE_ROWS, through registers; a step's scales stand STRIDE dwords after the one's before,
+  // in other banks.  Blocks: a wave's 64 dwords are those of CHUNK rows, [row][step], fetched as the codes are.
+  constexpr int SCALE_ROWS = THREADS / BS, SCALE_LOADS = kWhole<K> ? (SCALED + SCALE_ROWS - 1) / SCALE_ROWS : 1;
+  constexpr int STRIDE = SCALED * WORDS + 16, PER_ROW = BS * WORDS, CHUNK = 64 / PER_ROW, CHUNKS = ROWS / CHUNK;
+  constexpr int SCALE_PIECES = kWhole<K> ? 0 : (CHUNKS + WAVES - 1) / WAVES;
+  static_assert(kWhole<K> || (ROWS % CHUNK == 0 && TR % CHUNK == 0), "");
+  // objects of their own, so that a read of one does not wait for what is on its way to the other
+  __shared__ __attribute__((aligned(16))) uint8_t codes0[CODES], codes1[CODES], codes2[BUFS > 2 ? CODES : 16], codes3[BUFS > 3 ? CODES : 16];
+  __shared__ __attribute__((aligned(16))) uint32_t scales[2][SCALES ? (kWhole<K> ? BS * STRIDE : ROWS * PER_ROW) : 4];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, q = lane >> 4;
   const int wr = wave % WR, wt = wave / WR;
   int rt, tt;
-  tile_of(blockIdx.x, (int64_t)row_tiles * token_tiles, row_tiles, token_tiles, rt, tt);
+  tile_of(blockIdx.x, gridDim.x, row_tiles, token_tiles, rt, tt);
   Span span;
   if (!find_span(p, tt, TT, span)) return;
   const int64_t row0 = (int64_t)rt * TR, tok0 = span.first;
   const int64_t expert_row = span.expert * p.rows;
+  const int rows_here = (int)(p.rows - row0 < TR ? p.rows - row0 : TR), tokens_here = (int)(span.end - tok0 < TT ? span.end - tok0 : TT);
 
-  const int steps = (p.n + kStep - 1) / kStep;
-  const int s0 = (int)((int64_t)steps * blockIdx.y / p.k_splits), s1 = (int)((int64_t)steps * (blockIdx.y + 1) / p.k_splits);
-  const int left = p.n - (steps - 1) * kStep;                      // values in the last step
+  constexpr int STAGE = KS * kStep;
+  const int stages = (p.n + STAGE - 1) / STAGE, steps = (p.n + kStep - 1) / kStep;
+  const int s0 = stages * (int)blockIdx.y / p.k_splits, s1 = stages * ((int)blockIdx.y + 1) / p.k_splits;
+  const int left = p.n - (stages - 1) * STAGE;                     // values in the last stage
 
-  // this lane's pieces: where they begin in their rows, and which part of the step's bytes
+  // row of a for token r of the tile: those behind the last take its row
+  auto act_row = [&](int r) -> uint32_t {
+    const int32_t row = row_of(p, tok0 + (r < tokens_here ? r : tokens_here - 1));
+    return row < 0 ? 0 : row;
+  };
+  // this lane's pieces of the stage that is fetched last
+  static_assert(PIECES_W % WAVES == 0, "");
+  constexpr int MINE_W = PIECES_W / WAVES;
   const uint8_t* from[MINE];
-  int part[MINE];
+  const uint8_t* const w_from = p.w.codes + (expert_row + row0) * (p.n / 2);
+  const uint32_t a_bytes = WIDE_A ? p.n : p.n / 2;
 #pragma unroll
   for (int i = 0; i < MINE; ++i) {
-    const int piece = i * WAVES + wave;
-    if (piece < PIECES_W) {
-      const int r = 16 * piece + (lane >> 2);
-      part[i] = 16 * placed<64>(r, lane & 3);
-      const int64_t row = row0 + r < p.rows ? row0 + r : p.rows - 1;
-      from[i] = p.w.codes + (expert_row + row) * (p.n / 2);
+    if (i < MINE_W) {
+      constexpr int PER = WB / 16;
+      const int r = (64 * (i * WAVES + wave) + lane) / PER;
+      from[i] = w_from + ((uint32_t)(r < rows_here ? r : rows_here - 1) * (uint32_t)(p.n / 2) + 16 * placed<WB>(r, lane % PER)) + s0 * WB;
     } else {
       constexpr int PER = AB / 16;
-      const int r = (64 * (piece - PIECES_W) + lane) / PER;
-      part[i] = 16 * placed<AB>(r, lane % PER);
-      const int64_t t = tok0 + r < span.end ? tok0 + r : span.end - 1;
-      const int64_t row = row_of(p, t);
-      from[i] = p.a.codes + (row < 0 ? 0 : row) * (AB == kStep ? p.n : p.n / 2);
+      const int r = (64 * (i * WAVES + wave - PIECES_W) + lane) / PER;
+      from[i] = p.a.codes + ((uint64_t)act_row(r) * a_bytes + 16 * placed<AB>(r, lane % PER)) + (int64_t)s0 * AB;
     }
   }
-  auto fetch = [&](int s, int b) {
-#pragma unroll
-    for (int i = 0; i < MINE; ++i) {
-      const int piece = i * WAVES + wave;
-      if (piece >= PIECES) break;
-      const bool weights = piece < PIECES_W;
-      const int bytes = weights || AB == kStepBytes ? kStepBytes : kStep;
-      int at = part[i];
-      if (s == steps - 1) {
-        const int end = bytes == kStep ? left : left / 2;          // a multiple of 16: its last piece for those behind it
-        at = at < end ? at : end - 16;
-      }
-      fetch16(from[i] + (int64_t)s * bytes + at, &codes[b][1024 * piece]);
-    }
+  // piece i of the stage `on` stages further
+  auto fetch = [&](int i, int on, uint8_t* to) {
+    from[i] += on * (WIDE_A && i >= MINE_W ? STAGE : STAGE / 2);
+    fetch16(from[i], to + 1024 * (i * WAVES + wave));
   };
-  // a row's scales are one thread's
-  constexpr int ROWS_EACH = (TR + TT + 64 * WAVES - 1) / (64 * WAVES);
-  uint32_t held[ROWS_EACH][WORDS];
-  int64_t scale_row[ROWS_EACH];
-#pragma unroll
-  for (int i = 0; i < ROWS_EACH; ++i) {
-    const int r = threadIdx.x + i * 64 * WAVES;
-    if (r < TR) {
-      scale_row[i] = expert_row + (row0 + r < p.rows ? row0 + r : p.rows - 1);
-    } else {
-      const int64_t t = tok0 + r - TR < span.end ? tok0 + r - TR : span.end - 1;
-      const int64_t row = row_of(p, t);
-      scale_row[i] = row < 0 ? 0 : row;
-    }
-  }
-  auto fetch_scales = [&](int s) {
-    if constexpr (SCALES)
-#pragma unroll
-      for (int i = 0; i < ROWS_EACH; ++i) {
-        const int r = threadIdx.x + i * 64 * WAVES;
-        if (r < TR) load_scales<K, SUB>(p.w, scale_row[i], s, held[i]);
-        else if (r < TR + TT) load_scales<K, SUB>(p.a, scale_row[i], s, held[i]);
-      }
+  // A last stage that the row does not fill: in the place of pieces behind the row's end its last one, which zeros replace for the activations
+  // before anybody reads them.
+  const bool has_cut = s1 == stages && left < STAGE;
+  auto byte_of = [&](int i) {
+    int l = lane;
+    asm volatile("" : "+v"(l));                                      // computed where it is used, once, and not held in registers until then
+    return 16 * (i < MINE_W ? placed<WB>((64 * (i * WAVES + wave) + l) / (WB / 16), l % (WB / 16))
+                            : placed<AB>((64 * (i * WAVES + wave - PIECES_W) + l) / (AB / 16), l % (AB / 16)));
   };
-  auto put_scales = [&](int b) {
-    if constexpr (SCALES)
+  auto behind = [&](int i) {                                         // how far behind the last piece
+    const int over = byte_of(i) + 16 - (WIDE_A && i >= MINE_W ? left : left / 2);
+    return over > 0 ? over : 0;
+  };
+  auto fetch_cut = [&](uint8_t* to) {
 #pragma unroll
-      for (int i = 0; i < ROWS_EACH; ++i) {
-        const int r = threadIdx.x + i * 64 * WAVES;
-        if (r >= TR + TT) continue;
+    for (int i = 0; i < MINE; ++i)
+      fetch16(from[i] + (WIDE_A && i >= MINE_W ? STAGE : STAGE / 2) - behind(i), to + 1024 * (i * WAVES + wave));
+  };
+  auto clear_cut = [&](uint8_t* codes) {
 #pragma unroll
-        for (int j = 0; j < WORDS; ++j) {
-          const uint32_t v = r < TR ? scale_value<K>(p.w, held[i][j]) : scale_value<K>(p.a, held[i][j]);
-          if constexpr (kWhole<K>) scales[b][j * (TR + TT) + r] = v;
-          else scales[b][r * WORDS + j] = v;
+    for (int i = MINE_W; i < MINE; ++i)
+      if (byte_of(i) >= (WIDE_A ? left : left / 2)) *reinterpret_cast<u32x4*>(codes + 1024 * (i * WAVES + wave) + 16 * lane) = u32x4{0u, 0u, 0u, 0u};
+  };
+  const int scale_step = kWhole<K> ? threadIdx.x % BS : lane % PER_ROW;   // blocks: dword of the row's in a block
+  uint32_t held[SCALE_LOADS][WORDS], scale_row[SCALE_LOADS];       // rows: of w from row0 on, or of a
+  const uint8_t* scale_from[SCALE_PIECES ? SCALE_PIECES : 1];
+  if constexpr (SCALES && kWhole<K>)
+#pragma unroll
+    for (int i = 0; i < SCALE_LOADS; ++i) {
+      const int r = threadIdx.x / BS + i * SCALE_ROWS;
+      scale_row[i] = r < TR ? (uint32_t)(r < rows_here ? r : rows_here - 1) : act_row(r - TR);
+    }
+  if constexpr (!kWhole<K>)
+#pragma unroll
+    for (int i = 0; i < SCALE_PIECES; ++i) {
+      const int c = i * WAVES + wave, r = (c < CHUNKS ? c : 0) * CHUNK + lane / PER_ROW;
+      scale_from[i] = r < TR ? static_cast<const uint8_t*>(p.w.scales) + (expert_row + row0 + (r < rows_here ? r : rows_here - 1)) * p.w.groups
+                             : static_cast<const uint8_t*>(p.a.scales) + (uint64_t)act_row(r - TR) * (uint32_t)p.a.groups;
+    }
+  const bool wide = p.w.wide && p.a.wide;
+  // the block's scales from step `first_step` on; INT: into registers, for put_scales()
+  auto fetch_scales = [&](int first_step, uint32_t* to) {
+    if constexpr (SCALES && kWhole<K>) {
+      const int at = first_step + scale_step, step = at < 0 ? 0 : (at < steps ? at : steps - 1);
+#pragma unroll
+      for (int i = 0; i < SCALE_LOADS; ++i) {
+        const int r = threadIdx.x / BS + i * SCALE_ROWS;
+        if (r < TR) load_scales<K, SUB>(p.w, expert_row + row0 + scale_row[i], step, held[i]);
+        else if (SCALED % SCALE_ROWS == 0 || r < SCALED) load_scales<K, SUB>(p.a, scale_row[i], step, held[i]);
+      }
+    } else if constexpr (!kWhole<K>) {
+      // behind the row's end its last dword
+      int at = WORDS * first_step + scale_step;
+      at = at < 0 ? 0 : (at < WORDS * steps ? at : WORDS * steps - 1);
+#pragma unroll
+      for (int i = 0; i < SCALE_PIECES; ++i) {
+        if (CHUNKS % WAVES != 0 && i * WAVES + wave >= CHUNKS) break;
+        uint32_t* place = to + 64 * (i * WAVES + wave);
+        if (wide) {
+          __builtin_amdgcn_global_load_lds((GlobalWord) reinterpret_cast<uintptr_t>(scale_from[i] + 4 * at), (LocalWord) reinterpret_cast<uintptr_t>(place),
+                                           4, 0, 0);
+        } else {
+          uint32_t v = 0;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) v |= (uint32_t)scale_from[i][4 * at + b < p.a.groups ? 4 * at + b : p.a.groups - 1] << (8 * b);
+          place[lane] = v;
         }
       }
+    }
   };
-  // E8M0 byte, or two E4M3 ones, of row r (of TR + TT) and this lane's 32 values
-  auto block_scale = [&](int b, int r) -> uint32_t {
-    if constexpr (K == KNV) return reinterpret_cast<const uint16_t*>(scales[b])[4 * r + q];
-    else if constexpr (!kWhole<K>) return reinterpret_cast<const uint8_t*>(scales[b])[4 * r + q];
-    else return 0;
+  // INT: [step][part][row]
+  auto put_scales = [&](uint32_t* to) {
+    if constexpr (SCALES && kWhole<K>)
+#pragma unroll
+      for (int i = 0; i < SCALE_LOADS; ++i) {
+        const int r = threadIdx.x / BS + i * SCALE_ROWS;
+        if (SCALED % SCALE_ROWS != 0 && r >= SCALED) continue;
+#pragma unroll
+        for (int j = 0; j < WORDS; ++j) to[scale_step * STRIDE + j * SCALED + r] = scale_value<K>(r < TR ? p.w : p.a, held[i][j]);
+      }
+  };
+  // the scales of row r (of ROWS) and this lane's 32 values of a step of the block: E8M0 byte, or two E4M3 ones
+  auto block_scale = [&](const uint32_t* of, int step, int r) -> uint32_t {
+    if constexpr (kWhole<K>) return 0;
+    else if constexpr (K == KNV) return reinterpret_cast<const uint16_t*>(of + r * PER_ROW + 2 * step)[q];
+    else return reinterpret_cast<const uint8_t*>(of + r * PER_ROW + step)[q];
   };
 
   constexpr bool ENDS = kWhole<K> && SUB == 0;                     // scales at the end
   f32x4 acc[FR][FT] = {};
   i32x4 whole[ENDS ? FR : 1][ENDS ? FT : 1] = {};
-  fetch(s0, 0);
-  fetch_scales(s0);
-  put_scales(0);
-  for (int s = s0; s < s1; ++s) {
-    const int b = (s - s0) & 1;
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");               // this wave's pieces are in LDS; then everybody's
-    __syncthreads();
-    // everything that this step reads of LDS, before the next one's pieces are on their way
-    u32x4 raw_w[FR], raw_a[FT][AB / 64];
-    uint32_t sw[FR], sa[FT];
+  // this lane's row of its wave's first tiles, and where its codes of each step stand there; 16 rows further the order is the same
+  const int w_row0 = 16 * FR * wr + m, a_row0 = 16 * FT * wt + m;
+  int w_at[KS], a_at[WIDE_A ? 2 * KS : KS];
 #pragma unroll
-    for (int i = 0; i < FR; ++i) {
-      const int r = 16 * (FR * wr + i) + m;
-      raw_w[i] = *reinterpret_cast<const u32x4*>(&codes[b][r * kStepBytes + 16 * placed<64>(r, q)]);
-      sw[i] = block_scale(b, r);
+  for (int k = 0; k < KS; ++k) {
+    w_at[k] = w_row0 * WB + 16 * placed<WB>(m, 4 * k + q);
+    if constexpr (!WIDE_A) {
+      a_at[k] = a_row0 * AB + 16 * placed<AB>(m, 4 * k + q);
+    } else {
+      a_at[k] = a_row0 * AB + 16 * placed<AB>(m, 8 * k + (K == KM8 ? q : 2 * q));
+      a_at[KS + k] = a_row0 * AB + 16 * placed<AB>(m, 8 * k + (K == KM8 ? 4 + q : 2 * q + 1));
     }
+  }
+  // The loop has no way out between its BUFS stages: those that do not make up a round are worked on first, as the last of a round and of a block
+  // of scales whose beginning nobody needs.
+  static_assert(BUFS % BLOCK == 0, "");
+  const int rest = (s1 - s0) % BUFS, first = rest ? BUFS - rest : 0, lead = first % BLOCK;
+  // One stage; the pieces of the one BUFS - 1 further are asked for between the first products, into the place of the one before; the next
+  // block's scales at the beginning of this one, and put in their place at its end.  IN: the stage's place in its block of scales.
+  auto work = [&](auto in_block, int s, uint8_t* codes, uint8_t* next_codes) {
+    constexpr int IN = decltype(in_block)::value;
+    const int block = (s - s0 + lead) / BLOCK;
+    const uint32_t* sc = scales[block & 1];
+    // Where the stage to fetch is none or a cut one, the last one's pieces are fetched again: no branch between the products.
+    const int on = s + BUFS - 1 < (has_cut ? s1 - 1 : s1) ? 1 : 0;
+    // this wave's pieces are in LDS (those of the BUFS - 2 stages after it may be on their way); then everybody's
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((BUFS - 2) * MINE + (IN == 1 && BLOCK > 1 && !(CHUNKS % WAVES) ? SCALE_PIECES : 0)) : "memory");
+    if (has_cut && s == s1 - 1) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");             // its pieces were asked for last
+      clear_cut(codes);
+    }
+    // not __syncthreads(), which would also wait for the pieces on their way
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if constexpr (IN == 0 && kWhole<K>) fetch_scales((s + BLOCK) * KS, nullptr);
+    constexpr int UNITS = KS * FR;                                 // row tiles of all steps
+    u32x4 raw_a[KS][FT][WIDE_A ? 2 : 1], raw_w[UNITS];
+    uint32_t scale_a[KS][FT], scale_w[UNITS];
+    auto read_a = [&](int k) {
 #pragma unroll
-    for (int i = 0; i < FT; ++i) {
-      const int r = 16 * (FT * wt + i) + m;
-      const uint8_t* at = &codes[b][TR * kStepBytes + r * AB];
-      if constexpr (AB == 64) {
-        raw_a[i][0] = *reinterpret_cast<const u32x4*>(at + 16 * placed<64>(r, q));
-      } else {
-        raw_a[i][0] = *reinterpret_cast<const u32x4*>(at + 16 * placed<128>(r, K == KM8 ? q : 2 * q));
-        raw_a[i][1] = *reinterpret_cast<const u32x4*>(at + 16 * placed<128>(r, K == KM8 ? 4 + q : 2 * q + 1));
+      for (int j = 0; j < FT; ++j) {
+        raw_a[k][j][0] = *reinterpret_cast<const u32x4*>(codes + TR * WB + 16 * j * AB + a_at[k]);
+        if constexpr (WIDE_A) raw_a[k][j][1] = *reinterpret_cast<const u32x4*>(codes + TR * WB + 16 * j * AB + a_at[KS + k]);
+        scale_a[k][j] = block_scale(sc, IN * KS + k, TR + 16 * j + a_row0);
       }
-      sa[i] = block_scale(b, TR + r);
-    }
-    if (s + 1 < s1) {
-      fetch_scales(s + 1);
-      fetch(s + 1, b ^ 1);
-    }
-    if (s == steps - 1 && left < kStep)
+    };
+    auto read_w = [&](int u) {
+      raw_w[u] = *reinterpret_cast<const u32x4*>(codes + 16 * (u % FR) * WB + w_at[u / FR]);
+      scale_w[u] = block_scale(sc, IN * KS + u / FR, 16 * (u % FR) + w_row0);
+    };
+    read_a(0);
 #pragma unroll
-      for (int i = 0; i < FT; ++i) cut_tail<K, true>(raw_a[i], left);
+    for (int u = 0; u < WA && u < UNITS; ++u) read_w(u);
+    if constexpr (WA >= UNITS) {
+#pragma unroll
+      for (int k = 1; k < KS; ++k) read_a(k);
+    }
     Operand<K, true> a[FT];
+    // whole sums of a row tile, which are scaled and added while the next one's products are made
+    i32x4 sums[2][kWhole<K> && SUB == 1 ? FT : 1];
+    f32x4 row_scales[2];
+    auto add_sums = [&](int u) {
+      if constexpr (kWhole<K> && SUB == 1) {
+        const int i = u % FR;
 #pragma unroll
-    for (int i = 0; i < FT; ++i) make_operand<K, true>(raw_a[i], sa[i], a[i]);
+        for (int j = 0; j < FT; ++j) {
+          float as = 1.0f;
+          if constexpr (!ONE) as = __uint_as_float(sc[(IN * KS + u / FR) * STRIDE + TR + 16 * j + a_row0]);
 #pragma unroll
-    for (int i = 0; i < FR; ++i) {
+          for (int c = 0; c < 4; ++c)
+            acc[i][j][c] = __builtin_fmaf((float)sums[u & 1][j][c], ONE ? row_scales[u & 1][c] : row_scales[u & 1][c] * as, acc[i][j][c]);
+          asm volatile("" : "+v"(acc[i][j]));                          // here and no later, as everything between two barriers
+        }
+      }
+    };
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) {
+      const int k = u / FR, i = u % FR;
+      if (u + WA < UNITS) read_w(u + WA);
+      if (WA < UNITS && i == (FR > 2 ? FR - 3 : 0) && k + 1 < KS) read_a(k + 1);
+      if (i == 0)
+#pragma unroll
+        for (int j = 0; j < FT; ++j) make_operand<K, true>(raw_a[k][j], scale_a[k][j], a[j]);
       Operand<K, false> w;
-      make_operand<K, false>(&raw_w[i], sw[i], w);
+      make_operand<K, false>(&raw_w[u], scale_w[u], w);
       if constexpr (ENDS) {
 #pragma unroll
-        for (int j = 0; j < FT; ++j) whole[i][j] = whole_sum<1>(w, a[j], whole[i][j]);
+        for (int j = 0; j < FT; ++j) {
+          whole[i][j] = whole_sum<1>(w, a[j], whole[i][j]);
+          asm volatile("" : "+v"(whole[i][j]));
+        }
+      } else if constexpr (kWhole<K> && SUB == 1) {
+        row_scales[u & 1] = *reinterpret_cast<const f32x4*>(sc + (IN * KS + k) * STRIDE + 16 * (FR * wr + i) + 4 * q);
+#pragma unroll
+        for (int j = 0; j < FT; ++j) sums[u & 1][j] = whole_sum<1>(w, a[j], i32x4{0, 0, 0, 0});
+        if (u > 0) add_sums(u - 1);
       } else if constexpr (kWhole<K>) {
 #pragma unroll 1
         for (int part = 0; part < SUB; ++part) {
-          const uint32_t* sc = &scales[b][part * (TR + TT)];
-          const f32x4 ws = *reinterpret_cast<const f32x4*>(sc + 16 * (FR * wr + i) + 4 * q);
+          const uint32_t* of = sc + (IN * KS + k) * STRIDE + part * SCALED;
+          const f32x4 ws = *reinterpret_cast<const f32x4*>(of + 16 * (FR * wr + i) + 4 * q);
 #pragma unroll
           for (int j = 0; j < FT; ++j) {
             const i32x4 d = whole_sum<SUB>(w, a[j], i32x4{0, 0, 0, 0}, part);
-            const float as = __uint_as_float(sc[TR + 16 * (FT * wt + j) + m]);
+            const float as = __uint_as_float(of[TR + 16 * j + a_row0]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) acc[i][j][k] = __builtin_fmaf((float)d[k], ws[k] * as, acc[i][j][k]);
+            for (int c = 0; c < 4; ++c) acc[i][j][c] = __builtin_fmaf((float)d[c], ws[c] * as, acc[i][j][c]);
+            asm volatile("" : "+v"(acc[i][j]));
           }
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < FT; ++j) acc[i][j] = step_sum<K, false, true>(w, a[j], acc[i][j]);
+        for (int j = 0; j < FT; ++j) {
+          acc[i][j] = step_sum<K, false, true>(w, a[j], acc[i][j]);
+          asm volatile("" : "+v"(acc[i][j]));
+        }
       }
+#pragma unroll
+      for (int f = EACH * u; f < EACH * (u + 1) && f < MINE; ++f) fetch(f, on, next_codes);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    if (s + 1 < s1) put_scales(b ^ 1);
+    add_sums(UNITS - 1);
+    if constexpr (IN == 0 && !kWhole<K>) fetch_scales((s + BLOCK) * KS, scales[(block + 1) & 1]);
+    if constexpr (IN == BLOCK - 1) put_scales(scales[(block + 1) & 1]);
+    if (has_cut && s + BUFS - 1 == s1 - 1) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      fetch_cut(next_codes);
+    }
+  };
+  auto buffer = [&](int i) -> uint8_t* { return i == 0 ? codes0 : (i == 1 ? codes1 : (i == 2 ? codes2 : codes3)); };
+  fetch_scales((s0 - lead) * KS, scales[0]);
+  if (has_cut && s0 == s1 - 1)
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) from[i] -= behind(i);
+#pragma unroll
+  for (int j = 0; j < BUFS - 1; ++j) {
+    uint8_t* const to = buffer((first + j) % BUFS);
+    if (j > 0 && has_cut && s0 + j == s1 - 1) {
+      fetch_cut(to);
+    } else {
+      const int on = j > 0 && s0 + j < (has_cut ? s1 - 1 : s1) ? 1 : 0;
+#pragma unroll
+      for (int i = 0; i < MINE; ++i) fetch(i, on, to);
+    }
   }
+  put_scales(scales[0]);
+  if (lead) fetch_scales((s0 - lead + BLOCK) * KS, scales[1]);      // what the block's first stage would ask for
+  int s = s0;
+  using std::integral_constant;
+  if constexpr (BUFS == 2) {
+    if (rest) work(integral_constant<int, 1 % BLOCK>{}, s++, codes1, codes0);
+    for (; s < s1; s += 2) {
+      work(integral_constant<int, 0>{}, s, codes0, codes1);
+      work(integral_constant<int, 1 % BLOCK>{}, s + 1, codes1, codes0);
+    }
+  } else {
+    if (rest == 3) work(integral_constant<int, 1 % BLOCK>{}, s++, codes1, codes0);
+    if (rest >= 2) work(integral_constant<int, 2 % BLOCK>{}, s++, codes2, codes1);
+    if (rest >= 1) work(integral_constant<int, 3 % BLOCK>{}, s++, codes3, codes2);
+    for (; s < s1; s += 4) {
+      work(integral_constant<int, 0>{}, s, codes0, codes3);
+      work(integral_constant<int, 1 % BLOCK>{}, s + 1, codes1, codes0);
+      work(integral_constant<int, 2 % BLOCK>{}, s + 2, codes2, codes1);
+      work(integral_constant<int, 3 % BLOCK>{}, s + 3, codes3, codes2);
+    }
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");                 // nothing is on its way to this workgroup's LDS when it ends
 
   float unit = 1.0f;
   if constexpr (kWhole<K>) unit = kWholeUnit<K>;
   if constexpr (K == KNV) unit = p.a.tensor[0] * p.w.tensor[span.expert];
+  f32x4 w_scale[ENDS ? FR : 1];
+  if constexpr (ENDS)
 #pragma unroll
-  for (int j = 0; j < FT; ++j) {
-    const int64_t t = tok0 + 16 * (FT * wt + j) + m;
-    if (t >= span.end) continue;
-    const int64_t a_row = row_of(p, t);
-    float as = unit;
-    if constexpr (ENDS) as *= row_scale(p.a, a_row < 0 ? 0 : a_row);
-#pragma unroll
-    for (int i = 0; i < FR; ++i) {
-      const int64_t r = row0 + 16 * (FR * wr + i) + 4 * q;
-      if (r >= p.rows) continue;
-      f32x4 v;
+    for (int i = 0; i < FR; ++i)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        if constexpr (ENDS) v[k] = (float)whole[i][j][k] * as * row_scale(p.w, expert_row + (r + k < p.rows ? r + k : p.rows - 1));
-        else v[k] = acc[i][j][k] * as;
-        if (a_row < 0) v[k] = 0.0f;
+        const int r = 16 * (FR * wr + i) + 4 * q + k;
+        w_scale[i][k] = row_scale(p.w, expert_row + row0 + (r < rows_here ? r : rows_here - 1));
       }
-      if (p.k_splits == 1) {
-        store_four(p, t, r, v);
-      } else {
+  // results: four neighbours a lane; `store` takes them for a token and a row
+  auto results = [&](auto store) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (r + k < p.rows) p.partial[((int64_t)blockIdx.y * p.tokens + t) * p.rows + r + k] = v[k];
+    for (int j = 0; j < FT; ++j) {
+      const int in = 16 * (FT * wt + j) + m;
+      if (in >= tokens_here) continue;
+      const int64_t t = tok0 + in;
+      float as = unit;
+      const int32_t a_row = row_of(p, t);
+      if constexpr (ENDS || ONE) as *= row_scale(p.a, a_row < 0 ? 0 : a_row);
+#pragma unroll
+      for (int i = 0; i < FR; ++i) {
+        const int r = 16 * (FR * wr + i) + 4 * q;
+        f32x4 v;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if constexpr (ENDS) v[k] = (float)whole[i][j][k] * (as * w_scale[i][k]);
+          else v[k] = acc[i][j][k] * as;
+          v[k] = a_row < 0 ? 0.0f : v[k];
+        }
+        if (r < rows_here) store(t, row0 + r, v);
       }
     }
+  };
+  if (p.k_splits > 1) {
+    float* to = p.partial + blockIdx.y * p.tokens * p.rows;
+    results([&](int64_t t, int64_t r, f32x4 v) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (r + k < p.rows) to[t * p.rows + r + k] = v[k];
+    });
+  } else if (p.out_dtype == RHTQ_IN_F32) {
+    results([&](int64_t t, int64_t r, f32x4 v) { store_four<RHTQ_IN_F32>(p, t, r, v); });
+  } else if (p.out_dtype == RHTQ_IN_BF16) {
+    results([&](int64_t t, int64_t r, f32x4 v) { store_four<RHTQ_IN_BF16>(p, t, r, v); });
+  } else {
+    results([&](int64_t t, int64_t r, f32x4 v) { store_four<RHTQ_IN_F16>(p, t, r, v); });
   }
 }
 
@@ -545,47 +720,43 @@ __global__ __launch_bounds__(64 * WR * WT) void tile_kernel(ProductArgs p, int r
 
 constexpr int kWaves = 8;
 
-// 16 weight rows and up to 16 MT tokens a workgroup.
-template <int K, int SUB, int MT>
+// 16 RW weight rows and up to 16 MT tokens a workgroup; 8 / RW waves share k, each with a range of steps of its own, AHEAD of which are in flight.
+template <int K, int SUB, bool ONE, int MT, int RW>
 __global__ __launch_bounds__(64 * kWaves) void stream_kernel(ProductArgs p) {
-  constexpr int AB = kActBytes<K>, WORDS = kScaleWords<K, SUB>, AHEAD = 2;
+  constexpr int AB = kActBytes<K>, WORDS = kScaleWords<K, SUB>, AHEAD = MT == 1 ? 4 : 2, KW = kWaves / RW;
   constexpr bool ENDS = kWhole<K> && SUB == 0;
+  constexpr bool SUMS = kWhole<K> && !ENDS && !ONE;               // the scales of a lane's four sums are needed on the way
   __shared__ f32x4 part[kWaves][MT][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, q = lane >> 4;
   Span span;
   if (!find_span(p, blockIdx.y, 16 * MT, span)) return;
-  const int64_t row0 = (int64_t)blockIdx.x * 16, expert_row = span.expert * p.rows;
-  const int64_t row = expert_row + (row0 + m < p.rows ? row0 + m : p.rows - 1);
+  const int64_t row0 = (int64_t)blockIdx.x * (16 * RW), expert_row = span.expert * p.rows;
+  const int64_t own_row0 = row0 + 16 * (wave / KW);
+  const int64_t row = expert_row + (own_row0 + m < p.rows ? own_row0 + m : p.rows - 1);
   const int steps = (p.n + kStep - 1) / kStep;
   const int left = p.n - (steps - 1) * kStep;
-  const uint8_t* w_from = p.w.codes + row * (p.n / 2);
-  const uint8_t* a_from[MT];
-  int64_t a_row[MT];                     // of this lane's operand row
-  int64_t sum_row[ENDS || !kWhole<K> ? 1 : MT][4];   // of its four sums
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int64_t t = span.first + 16 * i + m, r = row_of(p, t < span.end ? t : span.end - 1);
-    a_row[i] = r < 0 ? 0 : r;
-    a_from[i] = p.a.codes + a_row[i] * (AB == kStep ? p.n : p.n / 2);
-    if constexpr (kWhole<K> && !ENDS)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) sum_row[i][k] = __shfl(a_row[i], 4 * q + k);
-  }
+  const int s0 = steps * (wave % KW) / KW, s1 = steps * (wave % KW + 1) / KW;
+  const uint8_t* const w_from = p.w.codes + row * (p.n / 2);
   struct Step {
     u32x4 w, a[MT][AB / 64];
-    uint32_t ws[WORDS], as[MT][kWhole<K> ? 4 : WORDS];   // INT groups of at least 128: of the lane's row, of its four sums
+    uint32_t ws[WORDS], as[SUMS || !kWhole<K> ? MT : 1][kWhole<K> ? 4 : WORDS];   // INT groups of at least 128: of the lane's row, of its four sums
   };
-  auto load = [&](int s, Step& c) {
-    const bool end = s == steps - 1;
-    const int at = end && 16 * q >= left / 2 ? left / 2 - 16 : 16 * q;
-    c.w = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w_from + (int64_t)s * kStepBytes + at));
+  const uint8_t* a_from[MT];
+  uint32_t a_row[MT];                                             // of this lane's operand row
+  uint32_t sum_row[SUMS ? MT : 1][4];                             // of its four sums
+  auto load_w = [&](int s, Step& c) {
+    const int at = s == steps - 1 && 16 * q >= left / 2 ? left / 2 - 16 : 16 * q;
+    c.w = *reinterpret_cast<const u32x4*>(w_from + (int64_t)s * kStepBytes + at);
     if constexpr (!kWhole<K> || SUB == 1) load_scales<K, SUB>(p.w, row, s, c.ws);
+  };
+  auto load_a = [&](int s, Step& c) {
+    const bool end = s == steps - 1;
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       const uint8_t* from = a_from[i] + (int64_t)s * AB;
       if constexpr (AB == 64) {
-        c.a[i][0] = *reinterpret_cast<const u32x4*>(from + at);
+        c.a[i][0] = *reinterpret_cast<const u32x4*>(from + (end && 16 * q >= left / 2 ? left / 2 - 16 : 16 * q));
       } else {
         const int x = K == KM8 ? 16 * q : 32 * q, y = K == KM8 ? 64 + 16 * q : 32 * q + 16;
         c.a[i][0] = *reinterpret_cast<const u32x4*>(from + (end && x >= left ? left - 16 : x));
@@ -593,7 +764,7 @@ __global__ __launch_bounds__(64 * kWaves) void stream_kernel(ProductArgs p) {
       }
       if constexpr (!kWhole<K>) {
         load_scales<K, SUB>(p.a, a_row[i], s, c.as[i]);
-      } else if constexpr (SUB == 1) {
+      } else if constexpr (SUMS && SUB == 1) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) c.as[i][k] = part_scale<1>(p.a, sum_row[i][k], s, 0);
       }
@@ -612,7 +783,7 @@ __global__ __launch_bounds__(64 * kWaves) void stream_kernel(ProductArgs p) {
     make_operand<K, false>(&c.w, own_scale, w);
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      if (s == steps - 1 && left < kStep) cut_tail<K, true>(c.a[i], left);
+      cut_tail<K, true>(c.a[i], s == steps - 1 ? left : kStep);
       Operand<K, true> a;
       if constexpr (!kWhole<K>) own_scale = own(c.as[i]);
       make_operand<K, true>(c.a[i], own_scale, a);
@@ -622,11 +793,12 @@ __global__ __launch_bounds__(64 * kWaves) void stream_kernel(ProductArgs p) {
 #pragma unroll 1
         for (int part = 0; part < SUB; ++part) {
           const i32x4 d = whole_sum<SUB>(a, w, i32x4{0, 0, 0, 0}, part);
-          const uint32_t ws = SUB == 1 ? c.ws[0] : part_scale<SUB>(p.w, row, s, part);
+          const float ws = __uint_as_float(scale_value<K>(p.w, SUB == 1 ? c.ws[0] : part_scale<SUB>(p.w, row, s, part)));
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint32_t as = SUB == 1 ? c.as[i][k] : part_scale<SUB>(p.a, sum_row[i][k], s, part);
-            acc[i][k] = __builtin_fmaf((float)d[k], __uint_as_float(scale_value<K>(p.w, ws)) * __uint_as_float(scale_value<K>(p.a, as)), acc[i][k]);
+            float as = ws;
+            if constexpr (SUMS) as *= __uint_as_float(scale_value<K>(p.a, SUB == 1 ? c.as[i][k] : part_scale<SUB>(p.a, sum_row[i][k], s, part)));
+            acc[i][k] = __builtin_fmaf((float)d[k], as, acc[i][k]);
           }
         }
       } else {
@@ -634,20 +806,35 @@ __global__ __launch_bounds__(64 * kWaves) void stream_kernel(ProductArgs p) {
       }
     }
   };
-  // waves take steps in turn
-  Step c[AHEAD];
+  auto at = [&](int s) { return s < s1 ? s : s1 - 1; };
+  if (s0 < s1) {
+    Step c[AHEAD];
 #pragma unroll
-  for (int k = 0; k < AHEAD; ++k) {
-    const int s = wave + k * kWaves;
-    load(s < steps ? s : steps - 1, c[k]);
-  }
-  for (int s = wave; s < steps; s += AHEAD * kWaves) {
+    for (int k = 0; k < AHEAD; ++k) load_w(at(s0 + k), c[k]);     // these do not wait for the index
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) {
-      const int at = s + k * kWaves, next = at + AHEAD * kWaves;
-      if (at < steps) take(at, c[k]);
-      load(next < steps ? next : steps - 1, c[k]);
+    for (int i = 0; i < MT; ++i) {
+      const int64_t t = span.first + 16 * i + m;
+      const int32_t r = row_of(p, t < span.end ? t : span.end - 1);
+      a_row[i] = r < 0 ? 0 : r;
+      a_from[i] = p.a.codes + (uint64_t)a_row[i] * (uint32_t)(AB == kStep ? p.n : p.n / 2);
+      if constexpr (SUMS)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum_row[i][k] = __shfl(a_row[i], 4 * q + k);
     }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) load_a(at(s0 + k), c[k]);
+    // whole batches without a branch between their steps: a load behind a branch that may skip its use is moved there
+    int s = s0;
+    for (; s + AHEAD < s1; s += AHEAD)
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        take(s + k, c[k]);
+        load_w(at(s + k + AHEAD), c[k]);
+        load_a(at(s + k + AHEAD), c[k]);
+      }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (s + k < s1) take(s + k, c[k]);
   }
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
@@ -655,26 +842,27 @@ __global__ __launch_bounds__(64 * kWaves) void stream_kernel(ProductArgs p) {
     else part[wave][i][lane] = acc[i];
   }
   __syncthreads();
-  // result u: token 4 q + k of tile i, row m
+  // result u: token 4 q + k of tile i, row m of row tile g
   const float* sums = reinterpret_cast<const float*>(part);
-  for (int u = threadIdx.x; u < MT * 256; u += 64 * kWaves) {
-    const int i = u >> 8, k = (u >> 6) & 3;
-    const int64_t t = span.first + 16 * i + 4 * q + k;
-    if (t >= span.end || row0 + m >= p.rows) continue;
-    const int64_t r = row_of(p, t);
+  for (int u = threadIdx.x; u < RW * MT * 256; u += 64 * kWaves) {
+    const int g = u / (MT * 256), i = (u >> 8) % MT, k = (u >> 6) & 3;
+    const int64_t t = span.first + 16 * i + 4 * q + k, r = row0 + 16 * g + m;
+    if (t >= span.end || r >= p.rows) continue;
+    const int32_t from_row = row_of(p, t);
     float v = 0.0f;
     if constexpr (ENDS) {
       int total = 0;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) total += __float_as_int(sums[((w * MT + i) * 64 + lane) * 4 + k]);
-      v = (float)total * kWholeUnit<K> * row_scale(p.a, r < 0 ? 0 : r) * row_scale(p.w, row);
+      for (int w = 0; w < KW; ++w) total += __float_as_int(sums[(((g * KW + w) * MT + i) * 64 + lane) * 4 + k]);
+      v = (float)total * kWholeUnit<K> * row_scale(p.w, expert_row + r);
     } else {
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) v += sums[((w * MT + i) * 64 + lane) * 4 + k];
+      for (int w = 0; w < KW; ++w) v += sums[(((g * KW + w) * MT + i) * 64 + lane) * 4 + k];
       if constexpr (kWhole<K>) v *= kWholeUnit<K>;
       if constexpr (K == KNV) v *= p.a.tensor[0] * p.w.tensor[span.expert];
     }
-    store_one(p, t, row0 + m, r < 0 ? 0.0f : v);
+    if constexpr (ENDS || ONE) v *= row_scale(p.a, from_row < 0 ? 0 : from_row);
+    store_one(p, t, r, from_row < 0 ? 0.0f : v);
   }
 }
 
@@ -688,15 +876,34 @@ __global__ __launch_bounds__(256) void join_kernel(ProductArgs p) {
 
 // ---- which kernel -------------------------------------------------------------------------------------------------------------
 
-enum Form { STREAM16, STREAM32, STREAM64, TILE128, TILE256 };
+enum Form { STREAM16, STREAM32, STREAM64, TILE64, TILE128, TILE256 };
 
-Form form_of(int64_t tokens, int64_t rows, int32_t experts) {
-  const int64_t each = (tokens + experts - 1) / experts;           // of an expert, on average
-  if (each <= 16) return STREAM16;
-  if (each <= 32) return STREAM32;
-  if (each <= 64) return STREAM64;
-  const int64_t large = ((rows + 255) / 256) * ((tokens + 255) / 256);
-  return each >= 256 && large >= 256 ? TILE256 : TILE128;
+struct Plan {
+  Form form;
+  int32_t splits;             // parts of k
+};
+
+// From sizes alone.  Up to 64 rows of y an expert (on average) the weights' bytes count: each is read once.  Beyond, the tile whose rounds over the chip
+// cost least: a round of 256 tiles of 256 x 256 counts 1, one of 512 tiles of 128 x 128 (two a CU) 0.65, one of 1024 tiles of 64 x 64 0.42.
+// 8192 x 12288 x 4096 MXFP4 took 255, 307 and 424 us in these forms (6, 7.8 and 10.1 by the rule), 2048 x 12288 x 4096 INT4 111, 91 and 121 (2, 1.95
+// and 2.5), 512 x 4096 x 4096 MXFP4 33, 17 and 13.5 (1, 0.65 and 0.42).  NVFP4's operands take too many registers for the largest.
+// Small tiles that leave half the chip's room empty share k among several workgroups, with 16 stages each at least and up to 32 MB of
+// partial sums: 333 x 4001 x 11008 MXFP8 48 instead of 56 us; 512 x 4096 x 4096 INT4, eight stages each, would take 31 instead of 20.
+Plan plan_of(int64_t tokens, int32_t n, int64_t rows, int32_t experts, bool grouped, int a_fmt) {
+  const int64_t each = (tokens + experts - 1) / experts;
+  if (each <= 16) return {STREAM16, 1};
+  if (each <= 32) return {STREAM32, 1};
+  if (each <= 64) return {STREAM64, 1};
+  auto tiles = [&](int64_t size) { return ((rows + size - 1) / size) * ((tokens + size - 1) / size + (grouped ? experts / 2 : 0)); };
+  auto rounds = [&](int64_t size, int64_t at_once) { return (double)((tiles(size) + at_once - 1) / at_once); };
+  const double large = a_fmt == RHTQ_FMT_NVFP4 ? 1e30 : rounds(256, 256), middle = 0.65 * rounds(128, 512), small = 0.42 * rounds(64, 1024);
+  if (large <= middle && large <= small) return {TILE256, 1};
+  if (middle <= small) return {TILE128, 1};
+  int64_t splits = 1024 / tiles(64);
+  const int64_t stages = n / 256 / 16, room = ((int64_t)32 << 20) / (4 * tokens * rows);
+  if (splits > stages) splits = stages;
+  if (splits > room) splits = room;
+  return {TILE64, grouped || splits < 2 ? 1 : (int32_t)splits};
 }
 
 // Tiles of `size` rows of y: whole ones, and the rest of every expert that has any.
@@ -705,58 +912,72 @@ int64_t slots_of(const ProductArgs& p, int size) {
   return p.tokens / size + (p.experts < p.tokens ? p.experts : p.tokens);
 }
 
-template <int K, int SUB, int MT>
-void go_stream(const ProductArgs& p, hipStream_t s) {
-  hipLaunchKernelGGL((stream_kernel<K, SUB, MT>), dim3((unsigned)((p.rows + 15) / 16), (unsigned)slots_of(p, 16 * MT)), dim3(64 * kWaves), 0, s, p);
+template <int K, int SUB, bool ONE, int MT, int RW>
+void go_stream_rows(const ProductArgs& p, hipStream_t s) {
+  hipLaunchKernelGGL((stream_kernel<K, SUB, ONE, MT, RW>), dim3((unsigned)((p.rows + 16 * RW - 1) / (16 * RW)), (unsigned)slots_of(p, 16 * MT)),
+                     dim3(64 * kWaves), 0, s, p);
 }
 
-template <int K, int SUB, int FR, int FT, int WR, int WT>
+template <int K, int SUB, bool ONE, int MT>
+void go_stream(const ProductArgs& p, hipStream_t s) {
+  // Waves that share k have eight steps each if there are as many and row tiles for four workgroups a CU: 8 tokens x 4 of 64 experts, 4096 x 2048,
+  // took 69, 38 and 35 us with 1, 2 and 4 row tiles a workgroup; 16 tokens, 12288 x 4096 NVFP4, 16.2, 18.5 and 18.1; one token, 4096 x 4096 INT4,
+  // 4.3, 6.6 and 10.7.
+  const int64_t lists = p.starts ? (p.experts < p.tokens ? p.experts : p.tokens) : 1, tiles = (p.rows + 15) / 16 * lists;
+  const int steps = (p.n + kStep - 1) / kStep;
+  const int rw = steps < 24 && tiles >= 4 * 1024 ? 4 : (steps < 24 && tiles >= 2 * 1024 ? 2 : 1);
+  if (rw == 4) go_stream_rows<K, SUB, ONE, MT, 4>(p, s);
+  else if (rw == 2) go_stream_rows<K, SUB, ONE, MT, 2>(p, s);
+  else go_stream_rows<K, SUB, ONE, MT, 1>(p, s);
+}
+
+template <int K, int SUB, bool ONE, int KS, int BUFS, int BS, int FR, int FT, int WR, int WT, int WA>
 void go_tiles(const ProductArgs& p, hipStream_t s) {
   const int row_tiles = (int)((p.rows + 16 * FR * WR - 1) / (16 * FR * WR)), token_tiles = (int)slots_of(p, 16 * FT * WT);
-  hipLaunchKernelGGL((tile_kernel<K, SUB, FR, FT, WR, WT>), dim3((unsigned)((int64_t)row_tiles * token_tiles), (unsigned)p.k_splits),
+  hipLaunchKernelGGL((tile_kernel<K, SUB, ONE, KS, BUFS, BS, FR, FT, WR, WT, WA>), dim3((unsigned)((int64_t)row_tiles * token_tiles), (unsigned)p.k_splits),
                      dim3(64 * WR * WT), 0, s, p, row_tiles, token_tiles);
   if (p.k_splits > 1)
     hipLaunchKernelGGL(join_kernel, dim3((unsigned)((p.tokens * p.rows + 255) / 256)), dim3(256), 0, s, p);
 }
 
-template <int K, int SUB>
-hipError_t go(const ProductArgs& p, hipStream_t s) {
-  switch (form_of(p.tokens, p.rows, p.experts)) {
-    case STREAM16: go_stream<K, SUB, 1>(p, s); break;
-    case STREAM32: go_stream<K, SUB, 2>(p, s); break;
-    case STREAM64: go_stream<K, SUB, 4>(p, s); break;
-    case TILE128: go_tiles<K, SUB, 4, 4, 2, 2>(p, s); break;
+template <int K, int SUB, bool ONE = false>
+hipError_t go(const ProductArgs& p, const Plan& plan, hipStream_t s) {
+  constexpr int KS = SUB > 1 ? 1 : 2, KS256 = SUB > 1 || kActBytes<K> == kStep ? 1 : 2;
+  switch (SUB > 1 && plan.form == TILE256 ? TILE128 : plan.form) {
+    case STREAM16: go_stream<K, SUB, ONE, 1>(p, s); break;
+    case STREAM32: go_stream<K, SUB, ONE, 2>(p, s); break;
+    case STREAM64: go_stream<K, SUB, ONE, 4>(p, s); break;
+    case TILE64: go_tiles<K, SUB, ONE, KS, 2, 2 * KS, 2, 2, 2, 2, SUB < 2 ? 4 : 1>(p, s); break;
+    case TILE128: go_tiles<K, SUB, ONE, KS256, 2, 2 * KS256, 4, 4, 2, 2, SUB < 2 ? 3 : 1>(p, s); break;
     case TILE256:
-      if constexpr (SUB < 2) go_tiles<K, SUB, 8, 4, 2, 4>(p, s);
-      else go_tiles<K, SUB, 4, 4, 2, 2>(p, s);
+      if constexpr (SUB < 2 && K != KNV) go_tiles<K, SUB, ONE, KS256, 2, 2 * KS256, 8, 4, 2, 4, 2>(p, s);
       break;
   }
   return hipGetLastError();
 }
 
 template <int K>
-hipError_t go_whole(const ProductArgs& p, hipStream_t s) {
+hipError_t go_whole(const ProductArgs& p, const Plan& plan, hipStream_t s) {
   const int a = p.a.group_log, w = p.w.group_log;
-  if (a < 0 && w < 0 && p.n <= kMostWholeSum) return go<K, 0>(p, s);
+  if (a < 0 && w < 0 && p.n <= kMostWholeSum) return go<K, 0>(p, plan, s);
   const int least = a < 0 ? w : (w < 0 || a < w ? a : w);
-  if (least < 0 || least >= 7) return go<K, 1>(p, s);
-  if (least == 6) return go<K, 2>(p, s);
-  return least == 5 ? go<K, 4>(p, s) : go<K, 8>(p, s);
+  if (least < 0 || least >= 7) return a < 0 ? go<K, 1, true>(p, plan, s) : go<K, 1>(p, plan, s);
+  if (least == 6) return go<K, 2>(p, plan, s);
+  return least == 5 ? go<K, 4>(p, plan, s) : go<K, 8>(p, plan, s);
 }
 
 }  // namespace
 
-int32_t product_splits(int64_t tokens, int32_t n, int64_t rows, int32_t experts, int a_fmt) {
-  return 1;
-}
+int32_t product_splits(int64_t tokens, int32_t n, int64_t rows, int a_fmt) { return plan_of(tokens, n, rows, 1, false, a_fmt).splits; }
 
 hipError_t launch_product(int a_fmt, const ProductArgs& p, hipStream_t s) {
+  const Plan plan = plan_of(p.tokens, p.n, p.rows, p.experts, p.starts != nullptr, a_fmt);
   switch (a_fmt) {
-    case RHTQ_FMT_INT4: return go_whole<KI4>(p, s);
-    case RHTQ_FMT_INT8: return go_whole<KI8>(p, s);
-    case RHTQ_FMT_NVFP4: return go<KNV, 1>(p, s);
-    case RHTQ_FMT_MXFP4: return go<KM4, 1>(p, s);
-    default: return go<KM8, 1>(p, s);
+    case RHTQ_FMT_INT4: return go_whole<KI4>(p, plan, s);
+    case RHTQ_FMT_INT8: return go_whole<KI8>(p, plan, s);
+    case RHTQ_FMT_NVFP4: return go<KNV, 1>(p, plan, s);
+    case RHTQ_FMT_MXFP4: return go<KM4, 1>(p, plan, s);
+    default: return go<KM8, 1>(p, plan, s);
   }
 }
 

@@ -37,7 +37,7 @@ struct ProductArgs {
 };
 
 // Parts of k that a call's sums are split into (1: no workspace).
-int32_t product_splits(int64_t tokens, int32_t n, int64_t rows, int32_t experts, int a_fmt);
+int32_t product_splits(int64_t tokens, int32_t n, int64_t rows, int a_fmt);
 hipError_t launch_product(int a_fmt, const ProductArgs& p, hipStream_t s);
 
 struct NormArgs {
