@@ -676,6 +676,54 @@ __global__ __launch_bounds__(64 * WR * WT, 2) void tile_kernel(ProductArgs p, in
         const int r = 16 * (FR * wr + i) + 4 * q + k;
         w_scale[i][k] = row_scale(p.w, expert_row + row0 + (r < rows_here ? r : rows_here - 1));
       }
+  // result (i, j) of this lane: token 16 (FT wt + j) + m, four rows from 16 (FR wr + i) + 4 q on; `none`: no row of a
+  auto result = [&](int i, int j, float as, bool none) -> f32x4 {
+    f32x4 v;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (ENDS) v[k] = (float)whole[i][j][k] * (as * w_scale[i][k]);
+      else v[k] = acc[i][j][k] * as;
+      v[k] = none ? 0.0f : v[k];
+    }
+    return v;
+  };
+  auto token_scale = [&](int32_t a_row) -> float {
+    float as = unit;
+    if constexpr (ENDS || ONE) as *= row_scale(p.a, a_row < 0 ? 0 : a_row);
+    return as;
+  };
+  if (p.k_splits == 1 && p.out_dtype != RHTQ_IN_F32 && (p.rows & 7) == 0) {
+    // 16-bit results: a wave's 16 tokens at a time through its own part of LDS, so that a store's lanes write whole rows of the wave's tile
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // everybody's last reads and pieces are done
+    constexpr int LINE = 32 * FR + 16, CHUNKS_T = 2 * FR;            // bytes of a token's row there; of 16 bytes
+    static_assert(16 * LINE * WAVES <= CODES, "");
+    uint8_t* const own = codes0 + 16 * LINE * wave;
+    auto write = [&](auto type) {
+      constexpr int T = decltype(type)::value;
+#pragma unroll
+      for (int j = 0; j < FT; ++j) {
+        const int in = 16 * (FT * wt + j) + m;
+        const int32_t a_row = row_of(p, tok0 + (in < tokens_here ? in : tokens_here - 1));
+        const float as = token_scale(a_row);
+#pragma unroll
+        for (int i = 0; i < FR; ++i) {
+          const f32x4 v = result(i, j, as, a_row < 0);
+          *reinterpret_cast<u32x2*>(own + m * LINE + 32 * i + 8 * q) = u32x2{to16<T>(v[0]) | to16<T>(v[1]) << 16, to16<T>(v[2]) | to16<T>(v[3]) << 16};
+        }
+#pragma unroll
+        for (int c = 0; c < 16 * CHUNKS_T; c += 64) {
+          const int t = (c + lane) / CHUNKS_T, r = (c + lane) % CHUNKS_T;
+          const u32x4 line = *reinterpret_cast<const u32x4*>(own + t * LINE + 16 * r);
+          const int token = 16 * (FT * wt + j) + t, row = 16 * FR * wr + 8 * r;
+          if (token < tokens_here && row < rows_here)
+            *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.y) + (tok0 + token) * p.rows + row0 + row) = line;
+        }
+      }
+    };
+    if (p.out_dtype == RHTQ_IN_BF16) write(std::integral_constant<int, RHTQ_IN_BF16>{});
+    else write(std::integral_constant<int, RHTQ_IN_F16>{});
+    return;
+  }
   // results: four neighbours a lane; `store` takes them for a token and a row
   auto results = [&](auto store) {
 #pragma unroll
@@ -683,20 +731,12 @@ __global__ __launch_bounds__(64 * WR * WT, 2) void tile_kernel(ProductArgs p, in
       const int in = 16 * (FT * wt + j) + m;
       if (in >= tokens_here) continue;
       const int64_t t = tok0 + in;
-      float as = unit;
       const int32_t a_row = row_of(p, t);
-      if constexpr (ENDS || ONE) as *= row_scale(p.a, a_row < 0 ? 0 : a_row);
+      const float as = token_scale(a_row);
 #pragma unroll
       for (int i = 0; i < FR; ++i) {
         const int r = 16 * (FR * wr + i) + 4 * q;
-        f32x4 v;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if constexpr (ENDS) v[k] = (float)whole[i][j][k] * (as * w_scale[i][k]);
-          else v[k] = acc[i][j][k] * as;
-          v[k] = a_row < 0 ? 0.0f : v[k];
-        }
-        if (r < rows_here) store(t, row0 + r, v);
+        if (r < rows_here) store(t, row0 + r, result(i, j, as, a_row < 0));
       }
     }
   };
@@ -718,12 +758,15 @@ __global__ __launch_bounds__(64 * WR * WT, 2) void tile_kernel(ProductArgs p, in
 
 // ---- few tokens: codes straight to registers, k split over a workgroup's waves ---------------------------------------------------
 
+// One token, 4096 x 4096 INT4, 4.1 us; 16 tokens, 12288 x 4096 NVFP4, 13.8 us (28 MB at 2.0 TB/s): the life of a workgroup is two round trips to memory,
+// of AHEAD steps each.  Four steps ahead took 4.3 and 16.2 us: half as many workgroups fit a CU.
+
 constexpr int kWaves = 8;
 
 // 16 RW weight rows and up to 16 MT tokens a workgroup; 8 / RW waves share k, each with a range of steps of its own, AHEAD of which are in flight.
 template <int K, int SUB, bool ONE, int MT, int RW>
 __global__ __launch_bounds__(64 * kWaves) void stream_kernel(ProductArgs p) {
-  constexpr int AB = kActBytes<K>, WORDS = kScaleWords<K, SUB>, AHEAD = MT == 1 ? 4 : 2, KW = kWaves / RW;
+  constexpr int AB = kActBytes<K>, WORDS = kScaleWords<K, SUB>, AHEAD = 2, KW = kWaves / RW;
   constexpr bool ENDS = kWhole<K> && SUB == 0;
   constexpr bool SUMS = kWhole<K> && !ENDS && !ONE;               // the scales of a lane's four sums are needed on the way
   __shared__ f32x4 part[kWaves][MT][64];
@@ -920,14 +963,12 @@ void go_stream_rows(const ProductArgs& p, hipStream_t s) {
 
 template <int K, int SUB, bool ONE, int MT>
 void go_stream(const ProductArgs& p, hipStream_t s) {
-  // Waves that share k have eight steps each if there are as many and row tiles for four workgroups a CU: 8 tokens x 4 of 64 experts, 4096 x 2048,
-  // took 69, 38 and 35 us with 1, 2 and 4 row tiles a workgroup; 16 tokens, 12288 x 4096 NVFP4, 16.2, 18.5 and 18.1; one token, 4096 x 4096 INT4,
-  // 4.3, 6.6 and 10.7.
+  // Waves that share k have four steps each at least if there are row tiles for eight workgroups a CU: 8 tokens x 4 of 64 experts, 4096 x 2048, took
+  // 39.6, 32.7 and 33.7 us with 1, 2 and 4 row tiles a workgroup; 16 tokens, 12288 x 4096 NVFP4, 13.8, 17.8 and 17.3; one token, 4096 x 4096
+  // INT4, 4.1, 6.5 and 10.8.
   const int64_t lists = p.starts ? (p.experts < p.tokens ? p.experts : p.tokens) : 1, tiles = (p.rows + 15) / 16 * lists;
-  const int steps = (p.n + kStep - 1) / kStep;
-  const int rw = steps < 24 && tiles >= 4 * 1024 ? 4 : (steps < 24 && tiles >= 2 * 1024 ? 2 : 1);
-  if (rw == 4) go_stream_rows<K, SUB, ONE, MT, 4>(p, s);
-  else if (rw == 2) go_stream_rows<K, SUB, ONE, MT, 2>(p, s);
+  const int rw = p.n < 24 * kStep && tiles >= 2 * 2048 ? 2 : 1;
+  if (rw == 2) go_stream_rows<K, SUB, ONE, MT, 2>(p, s);
   else go_stream_rows<K, SUB, ONE, MT, 1>(p, s);
 }
 
