@@ -12,19 +12,15 @@ from typing import NamedTuple
 
 import torch
 
-from . import _FMT, _SCALE, _check, _expect, lib
+from . import _SCALE, _check, _expect, lib
 from .serving import _I32, _IN, _U8, _On, _int32, _one_device, _p, _rows16, _signs
 
 EXPORTED_PRODUCTS = ["rhtq_products_version", "rhtq_matmul_workspace", "rhtq_matmul", "rhtq_grouped_matmul", "rhtq_norm_forward"]
 
 RHTQ_FMT_INT8, RHTQ_FMT_MXFP8 = 3, 4
-_FMT8 = {**_FMT, "int8": RHTQ_FMT_INT8, "mxfp8": RHTQ_FMT_MXFP8}
-_GROUP = {"nvfp4": 16, "mxfp4": 32, "mxfp8": 32}
 _SCALE_NAME = {"nvfp4": "e4m3", "mxfp4": "e8m0", "mxfp8": "e8m0"}
 _SCALE_DTYPE = {"f32": torch.float32, "f16": torch.float16, "e4m3": torch.uint8, "e8m0": torch.uint8}
 _SCALE_CODE = {torch.float32: _SCALE["f32"], torch.float16: _SCALE["f16"]}
-_WHOLE = ("int4", "int8")
-_PAIR = {"int4": "int4", "int8": "int4", "nvfp4": "nvfp4", "mxfp4": "mxfp4", "mxfp8": "mxfp4"}
 
 # rhtq_rows_t as bytes, which a pointer argument takes as they are
 _pack_rows = struct.Struct("@3P3i").pack
@@ -63,83 +59,81 @@ class RhtqRows(NamedTuple):
     group: int = 0
 
 
-class _Side:
-    """Rows after their checks: sizes and what keeps the memory alive."""
-    __slots__ = ("rows", "lead", "n", "group", "scale", "codes", "scales", "tensor", "fmt")
-
-    def __init__(self, r, name, dims):
-        codes, scales, tensor, fmt, group = r
-        code = _FMT8.get(fmt)
-        if code is None:
-            raise ValueError(f"{name}: unknown fmt {fmt!r}")
-        shape = codes.shape
-        if len(shape) != dims:
-            raise ValueError(f"{name}.codes must be {dims}-D")
-        if codes.dtype is not (torch.int8 if fmt == "int8" else _U8):
-            raise ValueError(f"{name}.codes: {codes.dtype}, expected {'int8' if fmt == 'int8' else 'uint8'}")
-        n = shape[-1] if code >= RHTQ_FMT_INT8 else 2 * shape[-1]
-        group = group or _GROUP.get(fmt, 0)
-        each = group or n
-        if group < 0 or each == 0 or n % each:
-            raise ValueError(f"{name}: group {group} does not divide n = {n}")
-        want = (*shape[:-1], n // each)
-        if fmt in _WHOLE:
-            self.scale = _SCALE_CODE.get(scales.dtype)
-            if self.scale is None:
-                raise ValueError(f"{name}.scales: {scales.dtype}, expected float16 or float32")
-        else:
-            self.scale = _SCALE[_SCALE_NAME[fmt]]
-            if scales.dtype is not _U8:
-                raise ValueError(f"{name}.scales: {scales.dtype}, expected uint8")
-        if scales.shape != want:
-            raise ValueError(f"{name}.scales: {tuple(scales.shape)}, expected {want}")
-        self.lead = shape[0] if dims == 3 else 1
-        if fmt == "nvfp4":
-            if tensor is None:
-                raise ValueError(f"{name}: NVFP4 needs its tensor_scale")
-            if tensor.dtype != torch.float32 or tensor.numel() != self.lead:
-                raise ValueError(f"{name}.tensor_scale must be float32 with {self.lead} entries")
-        else:
-            tensor = None
-        self.rows, self.n, self.group, self.fmt = shape[-2], n, group, fmt
-        self.codes, self.scales, self.tensor = codes, scales, tensor
-
-    def packed(self):
-        """rhtq_rows_t as bytes; codes from 16 bytes on, scales and the tensor scale contiguous (copies where they are not)."""
-        if not self.codes.is_contiguous() or self.codes.data_ptr() & 15:
-            self.codes = _rows16(self.codes)
-        if not self.scales.is_contiguous():
-            self.scales = self.scales.contiguous()
-        if self.tensor is not None and not self.tensor.is_contiguous():
-            self.tensor = self.tensor.contiguous()
-        return _pack_rows(self.codes.data_ptr(), self.scales.data_ptr(), _p(self.tensor) or 0, _FMT8[self.fmt], self.group, self.scale)
-
-    def held(self, r):
-        """What packed() copied."""
-        return [t for t, u in ((self.codes, r.codes), (self.scales, r.scales), (self.tensor, r.tensor_scale)) if t is not None and t is not u]
+# fmt: C code, group, whether a code is a byte, dtype of the codes, scale type (None: from the scales), weights it is multiplied with
+_INFO = {"int4": (0, 0, False, _U8, None, "int4"), "int8": (RHTQ_FMT_INT8, 0, True, torch.int8, None, "int4"),
+         "nvfp4": (1, 16, False, _U8, _SCALE["e4m3"], "nvfp4"), "mxfp4": (2, 32, False, _U8, _SCALE["e8m0"], "mxfp4"),
+         "mxfp8": (RHTQ_FMT_MXFP8, 32, True, _U8, _SCALE["e8m0"], "mxfp4")}
 
 
-def _product(a, w, out, out_dtype, tokens, dims):
-    sa, sw = _Side(a, "a", 2), _Side(w, "w", dims)
-    if sa.n != sw.n:
-        raise ValueError(f"a has rows of {sa.n} values, w of {sw.n}")
-    if _PAIR[sa.fmt] != sw.fmt:
-        raise ValueError(f"{sa.fmt} rows are multiplied with {_PAIR[sa.fmt]} weights: got {sw.fmt}")
-    if tokens is None:
-        tokens = sa.rows
+def _rows(r, name, dims):
+    """(rows, experts, n, rhtq_rows_t as bytes, what the bytes point to) of RhtqRows after their checks: codes from 16 bytes on, scales and the
+    tensor scale contiguous (copies where they are not)."""
+    codes, scales, tensor, fmt, group = r
+    info = _INFO.get(fmt)
+    if info is None:
+        raise ValueError(f"{name}: unknown fmt {fmt!r}")
+    code, own_group, wide, codes_type, scale, _ = info
+    shape = codes.shape
+    if len(shape) != dims:
+        raise ValueError(f"{name}.codes must be {dims}-D")
+    if codes.dtype is not codes_type:
+        raise ValueError(f"{name}.codes: {codes.dtype}, expected {str(codes_type)[6:]}")
+    n = shape[-1] if wide else 2 * shape[-1]
+    group = group or own_group
+    each = group or n
+    if group < 0 or each == 0 or n % each:
+        raise ValueError(f"{name}: group {group} does not divide n = {n}")
+    if scale is None:
+        scale = _SCALE_CODE.get(scales.dtype)
+        if scale is None:
+            raise ValueError(f"{name}.scales: {scales.dtype}, expected float16 or float32")
+    elif scales.dtype is not _U8:
+        raise ValueError(f"{name}.scales: {scales.dtype}, expected uint8")
+    want = shape[:-1] + (n // each,)
+    if scales.shape != want:
+        raise ValueError(f"{name}.scales: {tuple(scales.shape)}, expected {tuple(want)}")
+    lead = shape[0] if dims == 3 else 1
+    at = 0
+    if fmt == "nvfp4":
+        if tensor is None:
+            raise ValueError(f"{name}: NVFP4 needs its tensor_scale")
+        if tensor.dtype != torch.float32 or tensor.numel() != lead:
+            raise ValueError(f"{name}.tensor_scale must be float32 with {lead} entries")
+        tensor = tensor if tensor.is_contiguous() else tensor.contiguous()
+        at = tensor.data_ptr()
+    else:
+        tensor = None
+    where = codes.data_ptr()
+    if where & 15 or not codes.is_contiguous():
+        codes = _rows16(codes)
+        where = codes.data_ptr()
+    if not scales.is_contiguous():
+        scales = scales.contiguous()
+    return shape[-2], lead, n, _pack_rows(where, scales.data_ptr(), at, code, group, scale), (codes, scales, tensor)
+
+
+def _kind(a, w, out, out_dtype):
+    """Output type and its C code, after the checks that concern both sides."""
+    if _INFO[a.fmt][5] != w.fmt:
+        raise ValueError(f"{a.fmt} rows are multiplied with {_INFO[a.fmt][5]} weights: got {w.fmt}")
     if out is not None:
         out_dtype = out.dtype
     kind = _IN.get(out_dtype)
     if kind is None:
         raise ValueError("out_dtype must be bfloat16, float16 or float32")
-    if out is not None:
-        _expect(out, "out", out_dtype, (tokens, sw.rows))
-    return sa, sw, kind, out_dtype
+    return out_dtype, kind
 
 
-def _tensors(a, w):
-    return {"a.codes": a.codes, "a.scales": a.scales, "a.tensor_scale": a.tensor_scale if a.fmt == "nvfp4" else None, "w.codes": w.codes,
-            "w.scales": w.scales, "w.tensor_scale": w.tensor_scale if w.fmt == "nvfp4" else None}
+def _same(index, named):
+    """Every tensor on device `index`; raises as the other calls do."""
+    for t in named.values():
+        if t is not None and t.get_device() != index or index < 0:
+            return _one_device(index, named)
+
+
+def _copied(r, held):
+    """What _rows() copied."""
+    return [t for t, u in zip(held, r) if t is not None and t is not u]
 
 
 def rhtq_products_version() -> int:
@@ -149,23 +143,29 @@ def rhtq_products_version() -> int:
 def rhtq_matmul(a: RhtqRows, w: RhtqRows, out=None, out_dtype=torch.bfloat16, stream=None):
     """y [tokens][rows] = a [tokens] rows times the transpose of w [rows] rows, both quantised and rotated alike (or not): INT4 or INT8 with
     INT4 weights, NVFP4 with NVFP4, MXFP4 or MXFP8 with MXFP4.  Groups of a and w may differ.  y has out's type, or out_dtype."""
-    sa, sw, kind, out_dtype = _product(a, w, out, out_dtype, None, 2)
-    tokens, rows, n = sa.rows, sw.rows, sa.n
-    index = a.codes.get_device()
-    _one_device(index, {**_tensors(a, w), "out": out})
+    tokens, _, n, pa, held_a = _rows(a, "a", 2)
+    rows, _, n_w, pw, held_w = _rows(w, "w", 2)
+    if n != n_w:
+        raise ValueError(f"a has rows of {n} values, w of {n_w}")
+    out_dtype, kind = _kind(a, w, out, out_dtype)
+    if out is not None:
+        _expect(out, "out", out_dtype, (tokens, rows))
+    first = a[0]
+    index = first.get_device()
+    _same(index, {"a.codes": first, "a.scales": a[1], "a.tensor_scale": held_a[2], "w.codes": w[0], "w.scales": w[1], "w.tensor_scale": held_w[2],
+                  "out": out})
     on = _On(index)
     try:
-        pa, pw = sa.packed(), sw.packed()
         own = out is None
         if own:
-            out = a.codes.new_empty((tokens, rows), dtype=out_dtype)
-        need = lib.rhtq_matmul_workspace(tokens, n, rows, _FMT8[sa.fmt])
-        work = a.codes.new_empty(need, dtype=_U8) if need else None
+            out = first.new_empty((tokens, rows), dtype=out_dtype)
+        need = lib.rhtq_matmul_workspace(tokens, n, rows, _INFO[a[3]][0])
+        work = first.new_empty(need, dtype=_U8) if need else None
         if stream is not None:
             on.follow(stream)
         _check(lib.rhtq_matmul(pa, tokens, n, pw, rows, out.data_ptr(), kind, _p(work), need, on.raw), "rhtq_matmul")
         if on.stream is not None:
-            on.keep(*sa.held(a), *sw.held(w), work, out if own else None)
+            on.keep(*_copied(a, held_a), *_copied(w, held_w), work, out if own else None)
     finally:
         on.leave()
     return out
@@ -177,26 +177,32 @@ def rhtq_grouped_matmul(a: RhtqRows, w: RhtqRows, starts, index=None, out=None, 
     starts[0] or from starts[experts] on are left as they were (without `out`: unspecified).  Formats as in rhtq_matmul."""
     if starts.dim() != 1 or (index is not None and index.dim() != 1):
         raise ValueError("starts and index must be 1-D")
-    tokens = a.codes.shape[0] if index is None else index.shape[0]
-    sa, sw, kind, out_dtype = _product(a, w, out, out_dtype, tokens, 3)
-    rows, experts = sw.rows, sw.lead
+    a_rows, _, n, pa, held_a = _rows(a, "a", 2)
+    rows, experts, n_w, pw, held_w = _rows(w, "w", 3)
+    if n != n_w:
+        raise ValueError(f"a has rows of {n} values, w of {n_w}")
+    tokens = a_rows if index is None else index.shape[0]
+    out_dtype, kind = _kind(a, w, out, out_dtype)
+    if out is not None:
+        _expect(out, "out", out_dtype, (tokens, rows))
     _int32(starts, "starts", (experts + 1,))
     if index is not None:
         _int32(index, "index", (tokens,))
-    where = a.codes.get_device()
-    _one_device(where, {**_tensors(a, w), "starts": starts, "index": index, "out": out})
+    first = a[0]
+    where = first.get_device()
+    _same(where, {"a.codes": first, "a.scales": a[1], "a.tensor_scale": held_a[2], "w.codes": w[0], "w.scales": w[1], "w.tensor_scale": held_w[2],
+                  "starts": starts, "index": index, "out": out})
     on = _On(where)
     try:
-        pa, pw = sa.packed(), sw.packed()
         own = out is None
         if own:
-            out = a.codes.new_empty((tokens, rows), dtype=out_dtype)
+            out = first.new_empty((tokens, rows), dtype=out_dtype)
         if stream is not None:
             on.follow(stream)
-        _check(lib.rhtq_grouped_matmul(pa, sa.rows, tokens, sa.n, pw, experts, rows, starts.data_ptr(), _p(index), out.data_ptr(), kind,
-                                       on.raw), "rhtq_grouped_matmul")
+        _check(lib.rhtq_grouped_matmul(pa, a_rows, tokens, n, pw, experts, rows, starts.data_ptr(), _p(index), out.data_ptr(), kind, on.raw),
+               "rhtq_grouped_matmul")
         if on.stream is not None:
-            on.keep(*sa.held(a), *sw.held(w), out if own else None)
+            on.keep(*_copied(a, held_a), *_copied(w, held_w), out if own else None)
     finally:
         on.leave()
     return out
@@ -208,16 +214,17 @@ def rhtq_norm_forward(x, weight=None, residual=None, eps: float = 1e-5, signs=No
     block by block if block > 0 ((I (x) H_block) diag(signs) / sqrt(block); block = n: the whole row, a power of two).  x, residual [tokens][n]
     and weight [n] (None: ones) are all bfloat16, float16 or float32.  fmt 'int4', 'int8' (group 0: one scale a row; scale_dtype 'f32' or
     'f16'), 'nvfp4' (tensor_scale is given, float32 [1]), 'mxfp4' or 'mxfp8'.  residual_out may be residual or x."""
-    code = _FMT8.get(fmt)
-    if code is None:
+    info = _INFO.get(fmt)
+    if info is None:
         raise ValueError(f"unknown fmt {fmt!r}")
+    code, own_group, wide, codes_type, _, _ = info
     if x.dim() != 2:
         raise ValueError("x must be 2-D [tokens][n]")
     kind = _IN.get(x.dtype)
     if kind is None:
         raise ValueError("x must be bfloat16, float16 or float32")
     tokens, n = shape = x.shape
-    group = group or _GROUP.get(fmt, 0)
+    group = group or own_group
     if scale_dtype is None:
         scale_dtype = _SCALE_NAME.get(fmt, "f32")
     scale_type = _SCALE_DTYPE.get(scale_dtype)
@@ -245,7 +252,7 @@ def rhtq_norm_forward(x, weight=None, residual=None, eps: float = 1e-5, signs=No
     if weight is not None and (weight.dtype is not x.dtype or weight.shape != shape[1:]):
         raise ValueError(f"weight: {weight.dtype} {tuple(weight.shape)}, expected {x.dtype} {(n,)}")
     index = x.get_device()
-    _one_device(index, {"x": x, "weight": weight, "residual": residual, "tensor_scale": tensor_scale, "residual_out": residual_out})
+    _same(index, {"x": x, "weight": weight, "residual": residual, "tensor_scale": tensor_scale, "residual_out": residual_out})
     on = _On(index)
     try:
         xc, rc = _rows16(x), residual if residual is None else _rows16(residual)
@@ -254,8 +261,7 @@ def rhtq_norm_forward(x, weight=None, residual=None, eps: float = 1e-5, signs=No
         h = residual_out
         if residual is not None and h is None:
             h = x.new_empty(shape)
-        wide = code >= RHTQ_FMT_INT8
-        codes = x.new_empty((tokens, n if wide else n // 2), dtype=torch.int8 if fmt == "int8" else _U8)
+        codes = x.new_empty((tokens, n if wide else n // 2), dtype=codes_type)
         scales = x.new_empty((tokens, n // each), dtype=scale_type)
         if stream is not None:
             on.follow(stream)
