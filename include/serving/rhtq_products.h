@@ -51,9 +51,9 @@ typedef struct {
  *   w          [rows] rows
  *   y_out      [tokens][rows] in out_dtype (RHTQ_IN_BF16, RHTQ_IN_F16 or RHTQ_IN_F32), 16-byte aligned
  *   workspace  rhtq_matmul_workspace(...) bytes, 16-byte aligned
- * n: a multiple of 32 up to 2^20; tokens up to 2^20, rows up to 2^24, tokens * rows up to 2^36 (0: nothing to do).  Products of codes are exact, sums are in fp32 (of
- * INT4 and INT8 within a group: in 32-bit integers); a tensor scale is applied to the sum.  A scale that is not finite shows in the
- * results that it takes part in.
+ * n: a multiple of 32 up to 2^20; tokens up to 2^20, rows up to 2^24, tokens * rows up to 2^36 (0: nothing to do).  Products of codes are
+ * exact, sums are in fp32 (of INT4 and INT8 within a group: in 32-bit integers); a tensor scale is applied to the sum.  A scale that is not
+ * finite shows in the results that it takes part in.
  */
 int64_t rhtq_matmul_workspace(int64_t tokens, int32_t n, int64_t rows, int a_fmt);
 int rhtq_matmul(const rhtq_rows_t* a, int64_t tokens, int32_t n, const rhtq_rows_t* w, int64_t rows, void* y_out, int out_dtype,
@@ -66,7 +66,7 @@ int rhtq_matmul(const rhtq_rows_t* a, int64_t tokens, int32_t n, const rhtq_rows
  *   w          [experts][rows] rows, an expert's after the other's
  *   starts     int32 [experts + 1], ascending; what lies outside [0, tokens] counts as its nearer end.  Read on the device only
  *   y_out      [tokens][rows]; rows before starts[0] and from starts[experts] on are left as they were
- * experts 1 to 32767, the rest as in rhtq_matmul.  No workspace.
+ * experts 1 to 32767, (tokens + 64 * experts) * rows up to 2^35, the rest as in rhtq_matmul.  An index may repeat.  No workspace.
  */
 int rhtq_grouped_matmul(const rhtq_rows_t* a, int64_t a_rows, int64_t tokens, int32_t n, const rhtq_rows_t* w, int32_t experts, int64_t rows,
                         const int32_t* starts, const int32_t* index, void* y_out, int out_dtype, rhtq_stream_t stream);
@@ -81,7 +81,9 @@ int rhtq_grouped_matmul(const rhtq_rows_t* a, int64_t a_rows, int64_t tokens, in
  *   x, residual, residual_out  [tokens][n] bf16, fp16 or fp32, rows contiguous, 16-byte aligned; residual_out may be residual or x
  * n: a multiple of 32 up to 32768; block a power of two, 16 to n, dividing n; groups lie inside a block (INT4 and INT8 group 0, one a
  * row: any block) and, where they are not one a row, hold up to 32768 values.  eps is finite and not negative.  The mean, the norm and
- * the rotation are in fp32.  A row of zeros with eps 0, or with a value that is not finite, has unspecified codes.
+ * the rotation are in fp32.  A row of h with a value that is not finite, or whose sum of squares is not in fp32, has NaN scales (INT4 and INT8
+ * NaN, E8M0 0xFF, E4M3 0x7F), and so has a group of y with such a value; their codes are unspecified.  Where the mean in fp32 and eps are both
+ * zero, y is zero.
  */
 int rhtq_norm_forward(const void* x, const void* residual, void* residual_out, int in_dtype, int64_t tokens, int32_t n, const void* weight,
                       float eps, const int8_t* signs, int32_t block, int fmt, int32_t group, int scale_dtype, void* codes_out,

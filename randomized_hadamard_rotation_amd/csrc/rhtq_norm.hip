@@ -31,10 +31,16 @@ __device__ __forceinline__ void lane_stage5(float& a, float& b) {
   b = __uint_as_float(p[1]);
 }
 
+// The larger of two magnitudes; NaN is larger than any, so that it is not lost.
+__device__ __forceinline__ float larger(float a, float b) {
+  const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+  return __uint_as_float(x > y ? x : y);
+}
+
 // Largest (or sum) of a wave's values in every lane, in one order.
 template <bool SUM>
 __device__ __forceinline__ float wave_all(float v) {
-  auto put = [](float a, float b) { return SUM ? a + b : fmaxf(a, b); };
+  auto put = [](float a, float b) { return SUM ? a + b : larger(a, b); };
   v = put(v, lane_xor16<0>(v));
   v = put(v, lane_xor16<1>(v));
   v = put(v, lane_xor16<2>(v));
@@ -134,8 +140,9 @@ __global__ __launch_bounds__(64 * kMostWaves) void norm_kernel(NormArgs a) {
     __syncthreads();
     sum = wave_all<true>(lane < waves ? wave_sum[lane] : 0.0f);
   }
-  const bool lost = !(sum < __builtin_inff());                         // an infinity or NaN in the row: its scales are NaN
-  float r = 1.0f / __builtin_sqrtf(sum / (float)a.n + a.eps);
+  const bool row_lost = !(sum < __builtin_inff());                     // an infinity or NaN in the row: its scales are NaN
+  const float mean = sum / (float)a.n + a.eps;
+  float r = mean == 0.0f ? 0.0f : 1.0f / __builtin_sqrtf(mean);        // a row of zeros stays one
   if (a.block_log >= 0) r *= a.block_log & 1 ? __builtin_ldexpf(0.70710678118654752f, -(a.block_log >> 1)) : __builtin_ldexpf(1.0f, -(a.block_log >> 1));
 #pragma unroll
   for (int i = 0; i < HELD; ++i) {
@@ -219,17 +226,17 @@ __global__ __launch_bounds__(64 * kMostWaves) void norm_kernel(NormArgs a) {
   for (int i = 0; i < HELD; ++i) {
     float m = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = fmaxf(m, __builtin_fabsf(v[i][j]));
+    for (int j = 0; j < 8; ++j) m = larger(m, __builtin_fabsf(v[i][j]));
     if (a.group_log < 0 || a.group_log >= 9) {
       m = wave_all<false>(m);
     } else {
-      m = fmaxf(m, lane_xor16<0>(m));
-      if (a.group_log > 4) m = fmaxf(m, lane_xor16<1>(m));
-      if (a.group_log > 5) m = fmaxf(m, lane_xor16<2>(m));
-      if (a.group_log > 6) m = fmaxf(m, lane_xor16<3>(m));
+      m = larger(m, lane_xor16<0>(m));
+      if (a.group_log > 4) m = larger(m, lane_xor16<1>(m));
+      if (a.group_log > 5) m = larger(m, lane_xor16<2>(m));
+      if (a.group_log > 6) m = larger(m, lane_xor16<3>(m));
       if (a.group_log > 7) {
         auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(m), __float_as_uint(m), false, false);
-        m = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+        m = larger(__uint_as_float(p[0]), __uint_as_float(p[1]));
       }
     }
     top[i] = m;
@@ -249,7 +256,7 @@ __global__ __launch_bounds__(64 * kMostWaves) void norm_kernel(NormArgs a) {
       for (int i = 0; i < HELD; ++i) {
         const int first = (i * waves + wave) & -span;
         float m = 0.0f;
-        for (int g = 0; g < span && first + g < HELD * waves; ++g) m = fmaxf(m, granule[first + g]);
+        for (int g = 0; g < span && first + g < HELD * waves; ++g) m = larger(m, granule[first + g]);
         top[i] = m;
       }
     }
@@ -263,6 +270,16 @@ __global__ __launch_bounds__(64 * kMostWaves) void norm_kernel(NormArgs a) {
     if (e >= a.n) continue;
     const bool first = (e & mask) == 0;                                // this thread stores the group's scale
     const int64_t at = row * groups + (a.group_log < 0 ? 0 : e >> a.group_log);
+    const bool lost = row_lost || !(top[i] < __builtin_inff());        // or in the group, from the weights
+    // 1 / scale as a factor that is finite: values below 2^-100 are moved up with it
+    auto inverse = [&](float kept) {
+      if (kept < 0x1p-100f) {
+        kept *= 0x1p100f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] *= 0x1p100f;
+      }
+      return kept > 0.0f ? 1.0f / kept : 0.0f;
+    };
     if (a.fmt == RHTQ_FMT_INT4 || a.fmt == RHTQ_FMT_INT8) {
       const bool four = a.fmt == RHTQ_FMT_INT4;
       const float s = lost ? __builtin_nanf("") : top[i] / (four ? 7.0f : 127.0f);
@@ -272,7 +289,7 @@ __global__ __launch_bounds__(64 * kMostWaves) void norm_kernel(NormArgs a) {
         if (a.f32) reinterpret_cast<float*>(a.scales)[at] = s;
         else reinterpret_cast<__half*>(a.scales)[at] = h;
       }
-      const float inv = kept > 0.0f ? 1.0f / kept : 0.0f, most = four ? 7.0f : 127.0f;
+      const float inv = inverse(kept), most = four ? 7.0f : 127.0f;
       float c[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) c[j] = __builtin_rintf(__builtin_amdgcn_fmed3f(v[i][j] * inv, -most - 1.0f, most));
@@ -308,7 +325,7 @@ __global__ __launch_bounds__(64 * kMostWaves) void norm_kernel(NormArgs a) {
         const float g = a.tensor[0];
         const uint32_t code = g > 0.0f ? e4m3_code(top[i] / (6.0f * g)) : 0u;
         const float s = e4m3_value(code) * g;
-        inv = s > 0.0f ? 1.0f / s : 0.0f;
+        inv = inverse(s);
         if (first) reinterpret_cast<uint8_t*>(a.scales)[at] = lost ? 0x7F : (uint8_t)code;
       }
       uint32_t w = 0;

@@ -351,3 +351,191 @@ def test_views_and_empty_calls():
     x = torch.randn(3, 128, device="cuda").to(torch.bfloat16)
     rows, _ = R.rhtq_norm_forward(x.t().contiguous().t())
     assert torch.equal(rows.codes, R.rhtq_norm_forward(x)[0].codes)
+
+
+def on_gpu(rows, fmt):
+    return M.values(*rows, fmt).cuda()
+
+
+def expect_on_gpu(y, av, wv, out):
+    """expect() with the 64-bit product on the GPU, in blocks of rows."""
+    step = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11, "f32": 2.0 ** -24}[out]
+    for i in range(0, av.shape[0], 1024):
+        a = av[i:i + 1024]
+        want, mags = a @ wv.t(), a.abs() @ wv.abs().t()
+        bound = step * want.abs() + (1 + step) * mags * (av.shape[-1] + 8) * 2.0 ** -24 + 2.0 ** -25
+        assert ((y[i:i + 1024].double() - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("pair", [PAIRS[0], PAIRS[1], PAIRS[3], PAIRS[7], PAIRS[8], PAIRS[9], PAIRS[13], PAIRS[14], PAIRS[15]], ids=lambda p: "-".join(map(str, p)))
+@pytest.mark.parametrize("n,tokens,rows", [(256, 4090, 4088), (768, 4096, 4096), (1280, 3850, 4001)])
+def test_product_whole_rounds_of_large_tiles(pair, n, tokens, rows):
+    """As many tiles of 256 x 256 as the chip has room for; one stage of k, an odd number of them, rows that no vector store fits."""
+    a, ag, w, wg, scale = pair
+    g = gen(n)
+    ra, rw = M.random_rows((tokens, n), a, ag, scale, g), M.random_rows((rows, n), w, wg, scale, g)
+    out = "bf16" if rows % 8 == 0 else "f32"
+    y = R.rhtq_matmul(to_rows(ra, a, ag), to_rows(rw, w, wg), out_dtype=OUT[out])
+    expect_on_gpu(y, on_gpu(ra, a), on_gpu(rw, w), out)
+
+
+@pytest.mark.parametrize("pair", [PAIRS[0], PAIRS[7], PAIRS[13], PAIRS[14], PAIRS[15]], ids=lambda p: "-".join(map(str, p)))
+@pytest.mark.parametrize("n", [32, 224, 352, 608])
+def test_large_tiles_end_inside_a_stage(pair, n):
+    a, ag, w, wg, scale = pair
+    g = gen(n)
+    ra, rw = M.random_rows((4096, n), a, ag, scale, g), M.random_rows((4096, n), w, wg, scale, g)
+    y = R.rhtq_matmul(to_rows(ra, a, ag), to_rows(rw, w, wg), out_dtype=torch.float16)
+    # sums beyond fp16's largest number are infinite there
+    av, wv = on_gpu(ra, a), on_gpu(rw, w)
+    want = av @ wv.t()
+    mags = av.abs() @ wv.abs().t()
+    inside = want.abs() < 65000
+    bound = 2.0 ** -11 * want.abs() + mags * (n + 8) * 2.0 ** -23 + 2.0 ** -25
+    assert ((y.double() - want).abs() <= bound)[inside].all() and (y[want.abs() > 66000].isinf()).all()
+
+
+@pytest.mark.parametrize("pair", PAIRS, ids=lambda p: "-".join(map(str, p)))
+@pytest.mark.parametrize("n", [8448, 8320, 8224])
+def test_product_in_parts_of_k(pair, n):
+    """Few tiles and a long k: several workgroups share it, and their sums are joined.  33 stages, the last one whole, half full or an eighth."""
+    a, ag, w, wg, scale = pair
+    if not fits(n, ag, wg):
+        pytest.skip("a group does not divide n")
+    tokens, rows = 70, 100
+    g = gen(77)
+    ra, rw = M.random_rows((tokens, n), a, ag, scale, g), M.random_rows((rows, n), w, wg, scale, g)
+    assert R.lib.rhtq_matmul_workspace(tokens, n, rows, 0) == 2 * 4 * tokens * rows       # two parts of at least 16 stages
+    for out in ("f32", "bf16"):
+        y = R.rhtq_matmul(to_rows(ra, a, ag), to_rows(rw, w, wg), out_dtype=OUT[out])
+        expect_on_gpu(y, on_gpu(ra, a), on_gpu(rw, w), out)
+
+
+@pytest.mark.parametrize("pair", [PAIRS[1], PAIRS[3], PAIRS[13], PAIRS[14], PAIRS[15]], ids=lambda p: "-".join(map(str, p)))
+def test_grouped_large_tiles(pair):
+    a, ag, w, wg, scale = pair
+    n, rows, lengths = 256, 4088, [1000, 0, 513, 1, 900, 700]
+    tokens, a_rows = sum(lengths), 300
+    g = gen(78)
+    ra, rw = M.random_rows((a_rows, n), a, ag, scale, g), M.random_rows((6, rows, n), w, wg, scale, g)
+    index = torch.randint(0, a_rows, (tokens + 5,), generator=g, dtype=torch.int32)
+    index[7] = -3
+    starts = starts_of(lengths)
+    out = torch.full((tokens + 5, rows), 7.0, device="cuda", dtype=torch.bfloat16)
+    R.rhtq_grouped_matmul(to_rows(ra, a, ag), to_rows(rw, w, wg), starts.cuda(), index.cuda(), out=out)
+    av, wv = on_gpu(ra, a), on_gpu(rw, w)
+    assert (out[tokens:] == 7.0).all() and (out[7] == 0).all()
+    picked = av[index.clamp(min=0).long().cuda()]
+    picked[7] = 0
+    for e in range(6):
+        i, j = int(starts[e]), int(starts[e + 1])
+        if j > i:
+            expect_on_gpu(out[i:j], picked[i:j], wv[e], "bf16")
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8", "nvfp4"])
+@pytest.mark.parametrize("tokens", [4, 70, 300])
+def test_block_scales_at_odd_addresses(fmt, tokens):
+    g = gen(tokens)
+    w = "nvfp4" if fmt == "nvfp4" else "mxfp4"
+    n, rows = 512, 130
+    ra, rw = M.random_rows((tokens, n), fmt, 0, "", g), M.random_rows((rows, n), w, 0, "", g)
+    a, b = to_rows(ra, fmt), to_rows(rw, w)
+    want = R.rhtq_matmul(a, b, out_dtype=torch.float32)
+    for off in (1, 2, 3):
+        def moved(r):
+            s = torch.zeros(r.scales.numel() + 8, dtype=torch.uint8, device="cuda")[off:off + r.scales.numel()].view(r.scales.shape)
+            s.copy_(r.scales)
+            return r._replace(scales=s)
+        assert torch.equal(R.rhtq_matmul(moved(a), b, out_dtype=torch.float32), want)
+        assert torch.equal(R.rhtq_matmul(a, moved(b), out_dtype=torch.float32), want)
+
+
+def test_calls_on_two_streams_at_once():
+    """Each call has a workspace of its own: twelve pairs of calls at once give what they give one after the other."""
+    g = gen(80)
+    a = to_rows(M.random_rows((70, 8448), "mxfp8", 0, "", g), "mxfp8")
+    w = to_rows(M.random_rows((200, 8448), "mxfp4", 0, "", g), "mxfp4")
+    b = to_rows(M.random_rows((90, 8448), "int4", 0, "f16", g), "int4")
+    v = to_rows(M.random_rows((200, 8448), "int4", 0, "f16", g), "int4")
+    want = R.rhtq_matmul(a, w), R.rhtq_matmul(b, v)
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    got = [(R.rhtq_matmul(a, w, stream=one), R.rhtq_matmul(b, v, stream=two)) for _ in range(12)]
+    torch.cuda.synchronize()
+    for x, y in got:
+        assert torch.equal(x, want[0]) and torch.equal(y, want[1])
+
+
+def test_norm_scales_of_rows_beyond_fp32():
+    """A mean of squares that fp32 does not hold gives NaN scales, as a value that is not finite does; the rows beside it stay."""
+    x = torch.ones(3, 128, device="cuda")
+    x[1] = 1e25
+    for fmt in ("int8", "int4"):
+        rows, _ = R.rhtq_norm_forward(x, fmt=fmt)
+        assert torch.isnan(rows.scales[1]).all() and torch.isfinite(rows.scales[[0, 2]]).all()
+    rows, _ = R.rhtq_norm_forward(x, fmt="mxfp4")
+    assert (rows.scales[1] == 255).all() and (rows.scales[[0, 2]] < 255).all()
+
+
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+@pytest.mark.parametrize("fmt", ["int8", "int4", "mxfp8", "mxfp4", "nvfp4"])
+@pytest.mark.parametrize("block", [0, 32])
+def test_a_weight_that_is_not_finite_shows(bad, fmt, block):
+    """Its groups get NaN scales, the others none."""
+    x = torch.rand(3, 256, device="cuda", generator=torch.Generator("cuda").manual_seed(1)) + 0.5
+    weight = torch.ones(256, device="cuda")
+    weight[100] = bad
+    ts = torch.tensor([0.01], device="cuda") if fmt == "nvfp4" else None
+    rows, _ = R.rhtq_norm_forward(x, weight, fmt=fmt, group=32 if fmt in ("int8", "int4") else 0, block=block, tensor_scale=ts)
+    nan = torch.isnan(rows.scales) if fmt in ("int8", "int4") else rows.scales == (127 if fmt == "nvfp4" else 255)
+    size = 16 if fmt == "nvfp4" else 32
+    want = torch.zeros_like(nan)
+    first, last = (96, 128) if block else (100 // size * size, 100 // size * size + size)     # a rotation spreads it over its block
+    want[:, first // size:last // size] = True
+    assert torch.equal(nan, want)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "int4", "mxfp8", "mxfp4", "nvfp4"])
+@pytest.mark.parametrize("weight", [False, True])
+def test_norm_of_zeros_without_eps(fmt, weight):
+    x = torch.zeros(2, 128, device="cuda")
+    x[1] = 3.0
+    ts = torch.tensor([0.01], device="cuda") if fmt == "nvfp4" else None
+    rows, _ = R.rhtq_norm_forward(x, torch.ones(128, device="cuda") if weight else None, eps=0.0, fmt=fmt, tensor_scale=ts, block=64)
+    assert (rows.codes[0] == 0).all() and (rows.scales[0] == 0).all() and (rows.scales[1] != 0).any()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "int4", "nvfp4"])
+def test_norm_scales_below_the_normal_range(fmt):
+    """Weights of 2^-133: 1 / scale is beyond fp32, the codes are right nevertheless.  Both y and the scale are whole multiples of 2^-149; a code is
+    off by half a step, of NVFP4 by up to one (between 4 and 6), and the scale's rounding times the code, up to 127, adds to that; so does the
+    rounding of weight / root mean square times x."""
+    x = norm_case(5, 256, "f32", gen(11)).cuda()
+    weight = torch.full((256,), 2.0 ** -133, device="cuda")
+    ts = torch.tensor([2.0 ** -138], device="cuda") if fmt == "nvfp4" else None
+    rows, _ = R.rhtq_norm_forward(x, weight, fmt=fmt, group=16 if fmt != "nvfp4" else 0, tensor_scale=ts)
+    xd = x.double()
+    y = (xd * 2.0 ** -133 / (xd.square().mean(1, keepdim=True) + 1e-5).sqrt()).cpu()
+    got = M.values(rows.codes.cpu(), rows.scales.cpu(), None if ts is None else ts.cpu(), fmt)
+    scale = M.scale_values(rows.scales.cpu(), fmt, None if ts is None else ts.cpu()).repeat_interleave(16, -1)
+    most = {"int8": 0.5, "int4": 0.5, "nvfp4": 1.0}[fmt]
+    # NVFP4: a group's scale is rounded to E4M3, 2^-4 of it: the largest code, 6, may fall short by 6 / 16 of a step more
+    more = 6 * 2.0 ** -4 if fmt == "nvfp4" else 0.0
+    assert ((got - y).abs() <= (most + more) * scale * (1 + 2.0 ** -10) + (130 + xd.abs().cpu()) * 2.0 ** -149).all()
+    assert (got.abs().amax(1) > 0).all()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("tokens", [3, 70])
+def test_block_scales_of_the_whole_range(fmt, tokens):
+    """E8M0 scales from 2^-120 to 2^120 that meet their opposites, give or take 2^8."""
+    g = gen(12)
+    n, rows = 256, 20
+    ca, _, _ = M.random_rows((tokens, n), fmt, 0, "", g)
+    cw, _, _ = M.random_rows((rows, n), "mxfp4", 0, "", g)
+    e = torch.randint(-120, 121, (n // 32,), generator=g)
+    sa = (127 + e).to(torch.uint8).expand(tokens, -1).contiguous()
+    sw = (127 - e + torch.randint(-7, 7, (rows, n // 32), generator=g)).clamp(0, 254).to(torch.uint8)
+    ra, rw = (ca, sa, None), (cw, sw, None)
+    y = R.rhtq_matmul(to_rows(ra, fmt), to_rows(rw, "mxfp4"), out_dtype=torch.float32)
+    expect(y, M.values(*ra, fmt), M.values(*rw, "mxfp4"), "f32")
