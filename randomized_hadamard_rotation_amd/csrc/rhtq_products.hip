@@ -338,9 +338,9 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t all, int row_tiles
 }
 
 // FR x FT tiles of 16 weight rows x 16 tokens a wave, WR x WT waves.  A stage is KS steps (two where a row's 128 bytes fit: whole cache lines);
-// BUFS stages' codes lie in LDS, one being worked on, the next ones there or on their way.  Scales come for BS steps at a time, so that a
-// row's are one request, a block ahead.  WA row tiles' codes are read from LDS ahead of their products.
-template <int K, int SUB, bool ONE, int KS, int BUFS, int BS, int FR, int FT, int WR, int WT, int WA>
+// two stages' codes lie in LDS, one being worked on, the next on its way.  Scales come for a block of two stages at a time, so that a row's are
+// one request, a block ahead.  WA row tiles' codes are read from LDS ahead of their products.
+template <int K, int SUB, bool ONE, int KS, int FR, int FT, int WR, int WT, int WA>
 __global__ __launch_bounds__(64 * WR * WT, 2) void tile_kernel(ProductArgs p, int row_tiles, int token_tiles) {
   constexpr int WAVES = WR * WT, THREADS = 64 * WAVES, TR = 16 * FR * WR, TT = 16 * FT * WT, ROWS = TR + TT;
   constexpr int WB = KS * kStepBytes, AB = KS * kActBytes<K>, WORDS = kScaleWords<K, SUB>;
@@ -351,7 +351,7 @@ __global__ __launch_bounds__(64 * WR * WT, 2) void tile_kernel(ProductArgs p, in
   static_assert(PIECES % WAVES == 0, "");
   constexpr int SLOTS = KS * FR / 2, EACH = (MINE + SLOTS - 1) / SLOTS;   // pieces asked for after one row tile's products, in the first half
   constexpr bool SCALES = !(kWhole<K> && SUB == 0);
-  constexpr int BLOCK = BS / KS;                                   // stages of a block of scales
+  constexpr int BLOCK = 2, BS = BLOCK * KS;                        // stages and steps of a block of scales
   constexpr int SCALED = ONE ? TR : ROWS;                          // rows whose scales are needed on the way
   // INT: thread u has step u % BS of rows u / BS + i * SCALE_ROWS, through registers; a step's scales stand STRIDE dwords after the one's before,
   // in other banks.  Blocks: a wave's 64 dwords are those of CHUNK rows, [row][step], fetched as the codes are.
@@ -360,7 +360,7 @@ __global__ __launch_bounds__(64 * WR * WT, 2) void tile_kernel(ProductArgs p, in
   constexpr int SCALE_PIECES = kWhole<K> ? 0 : (CHUNKS + WAVES - 1) / WAVES;
   static_assert(kWhole<K> || (ROWS % CHUNK == 0 && TR % CHUNK == 0), "");
   // objects of their own, so that a read of one does not wait for what is on its way to the other
-  __shared__ __attribute__((aligned(16))) uint8_t codes0[CODES], codes1[CODES], codes2[BUFS > 2 ? CODES : 16], codes3[BUFS > 3 ? CODES : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t codes0[CODES], codes1[CODES];
   __shared__ __attribute__((aligned(16))) uint32_t scales[2][SCALES ? (kWhole<K> ? BS * STRIDE : ROWS * PER_ROW) : 4];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, q = lane >> 4;
@@ -472,6 +472,7 @@ __global__ __launch_bounds__(64 * WR * WT, 2) void tile_kernel(ProductArgs p, in
 #pragma unroll
           for (int b = 0; b < 4; ++b) v |= (uint32_t)scale_from[i][4 * at + b < p.a.groups ? 4 * at + b : p.a.groups - 1] << (8 * b);
           place[lane] = v;
+          asm volatile("s_waitcnt vmcnt(0)" ::: "memory");         // as a stage counts what it waits for, none of its codes are on their way
         }
       }
     }
@@ -510,20 +511,19 @@ __global__ __launch_bounds__(64 * WR * WT, 2) void tile_kernel(ProductArgs p, in
       a_at[KS + k] = a_row0 * AB + 16 * placed<AB>(m, 8 * k + (K == KM8 ? 4 + q : 2 * q + 1));
     }
   }
-  // The loop has no way out between its BUFS stages: those that do not make up a round are worked on first, as the last of a round and of a block
-  // of scales whose beginning nobody needs.
-  static_assert(BUFS % BLOCK == 0, "");
-  const int rest = (s1 - s0) % BUFS, first = rest ? BUFS - rest : 0, lead = first % BLOCK;
-  // One stage; the pieces of the one BUFS - 1 further are asked for between the first products, into the place of the one before; the next
-  // block's scales at the beginning of this one, and put in their place at its end.  IN: the stage's place in its block of scales.
+  // The loop has no way out between its two stages: an odd one is worked on first, as the second of a block of scales whose beginning nobody
+  // needs.
+  const int lead = (s1 - s0) % 2;
+  // One stage; the pieces of the next are asked for between the first products, into the place of the one before; the next block's scales in the
+  // first stage of this one, and put in their place at its end.  IN: the stage's place in its block of scales.
   auto work = [&](auto in_block, int s, uint8_t* codes, uint8_t* next_codes) {
     constexpr int IN = decltype(in_block)::value;
     const int block = (s - s0 + lead) / BLOCK;
     const uint32_t* sc = scales[block & 1];
     // Where the stage to fetch is none or a cut one, the last one's pieces are fetched again: no branch between the products.
-    const int on = s + BUFS - 1 < (has_cut ? s1 - 1 : s1) ? 1 : 0;
-    // this wave's pieces are in LDS (those of the BUFS - 2 stages after it may be on their way); then everybody's
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((BUFS - 2) * MINE + (IN == 1 && BLOCK > 1 && !(CHUNKS % WAVES) ? SCALE_PIECES : 0)) : "memory");
+    const int on = s + 1 < (has_cut ? s1 - 1 : s1) ? 1 : 0;
+    // this wave's pieces are in LDS (those of scales, asked for after them, may be on their way); then everybody's
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(IN == 1 && !(CHUNKS % WAVES) ? SCALE_PIECES : 0) : "memory");
     if (has_cut && s == s1 - 1) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");             // its pieces were asked for last
       clear_cut(codes);
@@ -621,47 +621,25 @@ __global__ __launch_bounds__(64 * WR * WT, 2) void tile_kernel(ProductArgs p, in
     add_sums(UNITS - 1);
     if constexpr (IN == 0 && !kWhole<K>) fetch_scales((s + BLOCK) * KS, scales[(block + 1) & 1]);
     if constexpr (IN == BLOCK - 1) put_scales(scales[(block + 1) & 1]);
-    if (has_cut && s + BUFS - 1 == s1 - 1) {
+    if (has_cut && s + 1 == s1 - 1) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       fetch_cut(next_codes);
     }
   };
-  auto buffer = [&](int i) -> uint8_t* { return i == 0 ? codes0 : (i == 1 ? codes1 : (i == 2 ? codes2 : codes3)); };
   fetch_scales((s0 - lead) * KS, scales[0]);
   if (has_cut && s0 == s1 - 1)
 #pragma unroll
     for (int i = 0; i < MINE; ++i) from[i] -= behind(i);
 #pragma unroll
-  for (int j = 0; j < BUFS - 1; ++j) {
-    uint8_t* const to = buffer((first + j) % BUFS);
-    if (j > 0 && has_cut && s0 + j == s1 - 1) {
-      fetch_cut(to);
-    } else {
-      const int on = j > 0 && s0 + j < (has_cut ? s1 - 1 : s1) ? 1 : 0;
-#pragma unroll
-      for (int i = 0; i < MINE; ++i) fetch(i, on, to);
-    }
-  }
+  for (int i = 0; i < MINE; ++i) fetch(i, 0, lead ? codes1 : codes0);
   put_scales(scales[0]);
   if (lead) fetch_scales((s0 - lead + BLOCK) * KS, scales[1]);      // what the block's first stage would ask for
   int s = s0;
   using std::integral_constant;
-  if constexpr (BUFS == 2) {
-    if (rest) work(integral_constant<int, 1 % BLOCK>{}, s++, codes1, codes0);
-    for (; s < s1; s += 2) {
-      work(integral_constant<int, 0>{}, s, codes0, codes1);
-      work(integral_constant<int, 1 % BLOCK>{}, s + 1, codes1, codes0);
-    }
-  } else {
-    if (rest == 3) work(integral_constant<int, 1 % BLOCK>{}, s++, codes1, codes0);
-    if (rest >= 2) work(integral_constant<int, 2 % BLOCK>{}, s++, codes2, codes1);
-    if (rest >= 1) work(integral_constant<int, 3 % BLOCK>{}, s++, codes3, codes2);
-    for (; s < s1; s += 4) {
-      work(integral_constant<int, 0>{}, s, codes0, codes3);
-      work(integral_constant<int, 1 % BLOCK>{}, s + 1, codes1, codes0);
-      work(integral_constant<int, 2 % BLOCK>{}, s + 2, codes2, codes1);
-      work(integral_constant<int, 3 % BLOCK>{}, s + 3, codes3, codes2);
-    }
+  if (lead) work(integral_constant<int, 1>{}, s++, codes1, codes0);
+  for (; s < s1; s += 2) {
+    work(integral_constant<int, 0>{}, s, codes0, codes1);
+    work(integral_constant<int, 1>{}, s + 1, codes1, codes0);
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");                 // nothing is on its way to this workgroup's LDS when it ends
 
@@ -974,10 +952,10 @@ void go_stream(const ProductArgs& p, hipStream_t s) {
   else go_stream_rows<K, SUB, ONE, MT, 1>(p, s);
 }
 
-template <int K, int SUB, bool ONE, int KS, int BUFS, int BS, int FR, int FT, int WR, int WT, int WA>
+template <int K, int SUB, bool ONE, int KS, int FR, int FT, int WR, int WT, int WA>
 void go_tiles(const ProductArgs& p, hipStream_t s) {
   const int row_tiles = (int)((p.rows + 16 * FR * WR - 1) / (16 * FR * WR)), token_tiles = (int)slots_of(p, 16 * FT * WT);
-  hipLaunchKernelGGL((tile_kernel<K, SUB, ONE, KS, BUFS, BS, FR, FT, WR, WT, WA>), dim3((unsigned)((int64_t)row_tiles * token_tiles), (unsigned)p.k_splits),
+  hipLaunchKernelGGL((tile_kernel<K, SUB, ONE, KS, FR, FT, WR, WT, WA>), dim3((unsigned)((int64_t)row_tiles * token_tiles), (unsigned)p.k_splits),
                      dim3(64 * WR * WT), 0, s, p, row_tiles, token_tiles);
   if (p.k_splits > 1)
     hipLaunchKernelGGL(join_kernel, dim3((unsigned)((p.tokens * p.rows + 255) / 256)), dim3(256), 0, s, p);
@@ -990,10 +968,10 @@ hipError_t go(const ProductArgs& p, const Plan& plan, hipStream_t s) {
     case STREAM16: go_stream<K, SUB, ONE, 1>(p, s); break;
     case STREAM32: go_stream<K, SUB, ONE, 2>(p, s); break;
     case STREAM64: go_stream<K, SUB, ONE, 4>(p, s); break;
-    case TILE64: go_tiles<K, SUB, ONE, KS, 2, 2 * KS, 2, 2, 2, 2, SUB < 2 ? 4 : 1>(p, s); break;
-    case TILE128: go_tiles<K, SUB, ONE, KS256, 2, 2 * KS256, 4, 4, 2, 2, SUB < 2 ? 3 : 1>(p, s); break;
+    case TILE64: go_tiles<K, SUB, ONE, KS, 2, 2, 2, 2, SUB < 2 ? 4 : 1>(p, s); break;
+    case TILE128: go_tiles<K, SUB, ONE, KS256, 4, 4, 2, 2, SUB < 2 ? 3 : 1>(p, s); break;
     case TILE256:
-      if constexpr (SUB < 2 && K != KNV) go_tiles<K, SUB, ONE, KS256, 2, 2 * KS256, 8, 4, 2, 4, 2>(p, s);
+      if constexpr (SUB < 2 && K != KNV) go_tiles<K, SUB, ONE, KS256, 8, 4, 2, 4, 2>(p, s);
       break;
   }
   return hipGetLastError();

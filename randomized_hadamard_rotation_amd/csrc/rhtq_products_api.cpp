@@ -101,7 +101,8 @@ int rhtq_grouped_matmul(const rhtq_rows_t* a, int64_t a_rows, int64_t tokens, in
                         const int32_t* starts, const int32_t* index, void* y_out, int out_dtype, rhtq_stream_t stream) {
   const int st = check_product(a, w, a_rows, tokens, n, rows, out_dtype);
   if (st != RHTQ_OK) return st;
-  if (experts < 1 || experts > kMostExperts || (!index && a_rows < tokens)) return RHTQ_EINVAL;
+  if (experts < 1 || experts > kMostExperts || (!index && a_rows < tokens) || (tokens + 64 * (int64_t)experts) * rows > kMostResults / 2)
+    return RHTQ_EINVAL;
   if (tokens == 0 || rows == 0) return RHTQ_OK;
   if (a_rows == 0) return RHTQ_EINVAL;               // an index has to have a row to name
   if (!rows_pointers(a) || !rows_pointers(w) || !starts || !aligned(starts, 4) || !aligned(index, 4) || !y_out || !aligned(y_out, 16))

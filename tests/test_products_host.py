@@ -184,3 +184,10 @@ def test_python_norm_refusals():
     refused(lambda: R.rhtq_norm_forward(x, residual=x, residual_out=x.half()), "residual_out")
     refused(lambda: R.rhtq_norm_forward(x, weight=torch.zeros(64)), "weight")
     refused(lambda: R.rhtq_norm_forward(x, weight=torch.zeros(128).half()), "weight")
+
+
+def test_grouped_results_beyond_a_grid():
+    """(tokens + 64 experts) rows: up to 2^35."""
+    assert grouped(tokens=1 << 19, a_rows=1 << 19, rows=1 << 16, n=128) == EINVAL
+    assert grouped(tokens=64, a_rows=64, experts=16384, rows=1 << 15, n=128) == EINVAL
+    assert grouped(tokens=0, experts=32767, rows=16384, n=128) == OK
