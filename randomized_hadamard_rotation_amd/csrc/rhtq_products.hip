@@ -39,7 +39,8 @@ template <int K>
 constexpr int kActBytes = K == KI8 || K == KM8 ? kStep : kStepBytes;   // of a row of activations in a step
 
 // How INT scales apply.  SUB: parts of a step with scales of their own; 0: one scale a row on both sides, applied at the end.  ONE: one scale a
-// row of the activations, applied at the end, and groups of at least 128 for the weights (SUB 1).
+// row of the activations, applied at the end, and groups of at least 128 for the weights (SUB 1).  HALF: scales of the activations that are fp16
+// numbers (SUB 1, not ONE).
 template <int K, int SUB>
 constexpr int kScaleWords = kWhole<K> ? (SUB ? SUB : 1) : (K == KNV ? 2 : 1);   // dwords of a row's scales in a step, as LDS holds them
 
@@ -157,9 +158,10 @@ __device__ __forceinline__ void make_operand(const u32x4* raw, uint32_t scale, O
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        // bit 6 set: exponent field of 8 or more, a value of at least 2
-        const uint32_t v = raw[h][j], t = v & 0x40404040u, large = t | (t - (t >> 6));
-        o.part[h][j] = (int)(v & (large | 0x80808080u));
+        // bit 6 set: exponent field of 8 or more, a value of at least 2.  Selector 8 is the sign of byte 1 of the second source, 9 of its byte 3,
+        // 10 and 11 of the first's.
+        const uint32_t v = raw[h][j], large = __builtin_amdgcn_perm(v << 9, v << 1, 0x090B080Au);
+        o.part[h][j] = (int)(v & large);
         o.part[2 + h][j] = (int)(v & ~large);
       }
     o.scale = (int)scale;
@@ -207,6 +209,11 @@ __device__ __forceinline__ i32x4 whole_sum(const X& x, const Y& y, i32x4 c, int 
   }
   return c;
 }
+
+// A whole sum of a step is at most 128 * 128 * 128 = 2^21.  Added to the bits of this number it gives those of (number + sum), so that
+//   (number + sum) s - number s = sum s,
+// one fused instruction that scales a sum and makes it a float at once; number s is exact for scales of fp16.
+constexpr float kSumBase = 12582912.0f;   // 1.5 * 2^23
 
 template <int K>
 constexpr float kWholeUnit = K == KI4 ? 1.0f / 256.0f : 1.0f / 16.0f;
@@ -340,7 +347,7 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t all, int row_tiles
 // FR x FT tiles of 16 weight rows x 16 tokens a wave, WR x WT waves.  A stage is KS steps (two where a row's 128 bytes fit: whole cache lines);
 // two stages' codes lie in LDS, one being worked on, the next on its way.  Scales come for a block of two stages at a time, so that a row's are
 // one request, a block ahead.  WA row tiles' codes are read from LDS ahead of their products.
-template <int K, int SUB, bool ONE, int KS, int FR, int FT, int WR, int WT, int WA>
+template <int K, int SUB, bool ONE, bool HALF, int KS, int FR, int FT, int WR, int WT, int WA>
 __global__ __launch_bounds__(64 * WR * WT, 2) void tile_kernel(ProductArgs p, int row_tiles, int token_tiles) {
   constexpr int WAVES = WR * WT, THREADS = 64 * WAVES, TR = 16 * FR * WR, TT = 16 * FT * WT, ROWS = TR + TT;
   constexpr int WB = KS * kStepBytes, AB = KS * kActBytes<K>, WORDS = kScaleWords<K, SUB>;
@@ -557,16 +564,22 @@ __global__ __launch_bounds__(64 * WR * WT, 2) void tile_kernel(ProductArgs p, in
     // whole sums of a row tile, which are scaled and added while the next one's products are made
     i32x4 sums[2][kWhole<K> && SUB == 1 ? FT : 1];
     f32x4 row_scales[2];
+    float token_scales[KS][FT];
+    constexpr int BASE = __builtin_bit_cast(int, kSumBase);
+    const i32x4 base = {BASE, BASE, BASE, BASE};
     auto add_sums = [&](int u) {
       if constexpr (kWhole<K> && SUB == 1) {
         const int i = u % FR;
 #pragma unroll
         for (int j = 0; j < FT; ++j) {
-          float as = 1.0f;
-          if constexpr (!ONE) as = __uint_as_float(sc[(IN * KS + u / FR) * STRIDE + TR + 16 * j + a_row0]);
+          const float as = ONE ? 1.0f : token_scales[u / FR][j];
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            acc[i][j][c] = __builtin_fmaf((float)sums[u & 1][j][c], ONE ? row_scales[u & 1][c] : row_scales[u & 1][c] * as, acc[i][j][c]);
+          for (int c = 0; c < 4; ++c) {
+            if constexpr (HALF)
+              acc[i][j][c] = __builtin_fmaf(__builtin_fmaf(__int_as_float(sums[u & 1][j][c]), as, -kSumBase * as), row_scales[u & 1][c], acc[i][j][c]);
+            else
+              acc[i][j][c] = __builtin_fmaf((float)sums[u & 1][j][c], ONE ? row_scales[u & 1][c] : row_scales[u & 1][c] * as, acc[i][j][c]);
+          }
           asm volatile("" : "+v"(acc[i][j]));                          // here and no later, as everything between two barriers
         }
       }
@@ -578,7 +591,10 @@ __global__ __launch_bounds__(64 * WR * WT, 2) void tile_kernel(ProductArgs p, in
       if (WA < UNITS && i == (FR > 2 ? FR - 3 : 0) && k + 1 < KS) read_a(k + 1);
       if (i == 0)
 #pragma unroll
-        for (int j = 0; j < FT; ++j) make_operand<K, true>(raw_a[k][j], scale_a[k][j], a[j]);
+        for (int j = 0; j < FT; ++j) {
+          make_operand<K, true>(raw_a[k][j], scale_a[k][j], a[j]);
+          if constexpr (kWhole<K> && SUB == 1 && !ONE) token_scales[k][j] = __uint_as_float(sc[(IN * KS + k) * STRIDE + TR + 16 * j + a_row0]);
+        }
       Operand<K, false> w;
       make_operand<K, false>(&raw_w[u], scale_w[u], w);
       if constexpr (ENDS) {
@@ -590,7 +606,7 @@ __global__ __launch_bounds__(64 * WR * WT, 2) void tile_kernel(ProductArgs p, in
       } else if constexpr (kWhole<K> && SUB == 1) {
         row_scales[u & 1] = *reinterpret_cast<const f32x4*>(sc + (IN * KS + k) * STRIDE + 16 * (FR * wr + i) + 4 * q);
 #pragma unroll
-        for (int j = 0; j < FT; ++j) sums[u & 1][j] = whole_sum<1>(w, a[j], i32x4{0, 0, 0, 0});
+        for (int j = 0; j < FT; ++j) sums[u & 1][j] = whole_sum<1>(w, a[j], HALF ? base : i32x4{0, 0, 0, 0});
         if (u > 0) add_sums(u - 1);
       } else if constexpr (kWhole<K>) {
 #pragma unroll 1
@@ -952,26 +968,28 @@ void go_stream(const ProductArgs& p, hipStream_t s) {
   else go_stream_rows<K, SUB, ONE, MT, 1>(p, s);
 }
 
-template <int K, int SUB, bool ONE, int KS, int FR, int FT, int WR, int WT, int WA>
+template <int K, int SUB, bool ONE, bool HALF, int KS, int FR, int FT, int WR, int WT, int WA>
 void go_tiles(const ProductArgs& p, hipStream_t s) {
   const int row_tiles = (int)((p.rows + 16 * FR * WR - 1) / (16 * FR * WR)), token_tiles = (int)slots_of(p, 16 * FT * WT);
-  hipLaunchKernelGGL((tile_kernel<K, SUB, ONE, KS, FR, FT, WR, WT, WA>), dim3((unsigned)((int64_t)row_tiles * token_tiles), (unsigned)p.k_splits),
+  hipLaunchKernelGGL((tile_kernel<K, SUB, ONE, HALF, KS, FR, FT, WR, WT, WA>), dim3((unsigned)((int64_t)row_tiles * token_tiles), (unsigned)p.k_splits),
                      dim3(64 * WR * WT), 0, s, p, row_tiles, token_tiles);
   if (p.k_splits > 1)
     hipLaunchKernelGGL(join_kernel, dim3((unsigned)((p.tokens * p.rows + 255) / 256)), dim3(256), 0, s, p);
 }
 
-template <int K, int SUB, bool ONE = false>
+template <int K, int SUB, bool ONE = false, bool HALF = false>
 hipError_t go(const ProductArgs& p, const Plan& plan, hipStream_t s) {
+  // E4M3 operands cost most to make: a wave takes all weight rows of its tile, so that it makes each of its tokens' operands only once
+  constexpr int WHOLE_ROWS = K == KM8 ? 2 : 1;
   constexpr int KS = SUB > 1 ? 1 : 2, KS256 = SUB > 1 || kActBytes<K> == kStep ? 1 : 2;
   switch (SUB > 1 && plan.form == TILE256 ? TILE128 : plan.form) {
     case STREAM16: go_stream<K, SUB, ONE, 1>(p, s); break;
     case STREAM32: go_stream<K, SUB, ONE, 2>(p, s); break;
     case STREAM64: go_stream<K, SUB, ONE, 4>(p, s); break;
-    case TILE64: go_tiles<K, SUB, ONE, KS, 2, 2, 2, 2, SUB < 2 ? 4 : 1>(p, s); break;
-    case TILE128: go_tiles<K, SUB, ONE, KS256, 4, 4, 2, 2, SUB < 2 ? 3 : 1>(p, s); break;
+    case TILE64: go_tiles<K, SUB, ONE, HALF, KS, 2 * WHOLE_ROWS, 2 / WHOLE_ROWS, 2 / WHOLE_ROWS, 2 * WHOLE_ROWS, SUB < 2 ? 4 : 1>(p, s); break;
+    case TILE128: go_tiles<K, SUB, ONE, HALF, KS256, 4 * WHOLE_ROWS, 4 / WHOLE_ROWS, 2 / WHOLE_ROWS, 2 * WHOLE_ROWS, SUB < 2 ? 3 : 1>(p, s); break;
     case TILE256:
-      if constexpr (SUB < 2 && K != KNV) go_tiles<K, SUB, ONE, KS256, 8, 4, 2, 4, 2>(p, s);
+      if constexpr (SUB < 2 && K != KNV) go_tiles<K, SUB, ONE, HALF, KS256, 8, 4, 2, 4, 2>(p, s);
       break;
   }
   return hipGetLastError();
@@ -982,7 +1000,10 @@ hipError_t go_whole(const ProductArgs& p, const Plan& plan, hipStream_t s) {
   const int a = p.a.group_log, w = p.w.group_log;
   if (a < 0 && w < 0 && p.n <= kMostWholeSum) return go<K, 0>(p, plan, s);
   const int least = a < 0 ? w : (w < 0 || a < w ? a : w);
-  if (least < 0 || least >= 7) return a < 0 ? go<K, 1, true>(p, plan, s) : go<K, 1>(p, plan, s);
+  if (least < 0 || least >= 7) {
+    if (a < 0) return go<K, 1, true>(p, plan, s);
+    return p.a.f32 ? go<K, 1>(p, plan, s) : go<K, 1, false, true>(p, plan, s);
+  }
   if (least == 6) return go<K, 2>(p, plan, s);
   return least == 5 ? go<K, 4>(p, plan, s) : go<K, 8>(p, plan, s);
 }
