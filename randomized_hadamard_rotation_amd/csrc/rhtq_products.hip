@@ -737,12 +737,9 @@ __global__ __launch_bounds__(64 * WR * WT, 2) void tile_kernel(ProductArgs p, in
     }
   };
   if (p.k_splits > 1) {
-    float* to = p.partial + blockIdx.y * p.tokens * p.rows;
-    results([&](int64_t t, int64_t r, f32x4 v) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (r + k < p.rows) to[t * p.rows + r + k] = v[k];
-    });
+    const int64_t line = (p.rows + 3) & ~(int64_t)3;                 // the last four of a line may hold some of no row
+    float* to = p.partial + blockIdx.y * p.tokens * line;
+    results([&](int64_t t, int64_t r, f32x4 v) { *reinterpret_cast<f32x4*>(to + t * line + r) = v; });
   } else if (p.out_dtype == RHTQ_IN_F32) {
     results([&](int64_t t, int64_t r, f32x4 v) { store_four<RHTQ_IN_F32>(p, t, r, v); });
   } else if (p.out_dtype == RHTQ_IN_BF16) {
@@ -906,11 +903,13 @@ __global__ __launch_bounds__(64 * kWaves) void stream_kernel(ProductArgs p) {
 }
 
 __global__ __launch_bounds__(256) void join_kernel(ProductArgs p) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, all = p.tokens * p.rows;
-  if (i >= all) return;
+  const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
+  if (r >= p.rows) return;
+  const int64_t line = (p.rows + 3) & ~(int64_t)3;
+  const float* from = p.partial + t * line + r;
   float v = 0.0f;
-  for (int k = 0; k < p.k_splits; ++k) v += p.partial[k * all + i];
-  store_one(p, i / p.rows, i % p.rows, v);
+  for (int k = 0; k < p.k_splits; ++k) v += from[k * p.tokens * line];
+  store_one(p, t, r, v);
 }
 
 // ---- which kernel -------------------------------------------------------------------------------------------------------------
@@ -939,7 +938,7 @@ Plan plan_of(int64_t tokens, int32_t n, int64_t rows, int32_t experts, bool grou
   if (large <= middle && large <= small) return {TILE256, 1};
   if (middle <= small) return {TILE128, 1};
   int64_t splits = 1024 / tiles(64);
-  const int64_t stages = n / 256 / 16, room = ((int64_t)32 << 20) / (4 * tokens * rows);
+  const int64_t stages = n / 256 / 16, room = ((int64_t)32 << 20) / (4 * tokens * ((rows + 3) / 4 * 4));
   if (splits > stages) splits = stages;
   if (splits > room) splits = room;
   return {TILE64, grouped || splits < 2 ? 1 : (int32_t)splits};
@@ -974,7 +973,7 @@ void go_tiles(const ProductArgs& p, hipStream_t s) {
   hipLaunchKernelGGL((tile_kernel<K, SUB, ONE, HALF, KS, FR, FT, WR, WT, WA>), dim3((unsigned)((int64_t)row_tiles * token_tiles), (unsigned)p.k_splits),
                      dim3(64 * WR * WT), 0, s, p, row_tiles, token_tiles);
   if (p.k_splits > 1)
-    hipLaunchKernelGGL(join_kernel, dim3((unsigned)((p.tokens * p.rows + 255) / 256)), dim3(256), 0, s, p);
+    hipLaunchKernelGGL(join_kernel, dim3((unsigned)((p.rows + 255) / 256), (unsigned)p.tokens), dim3(256), 0, s, p);
 }
 
 template <int K, int SUB, bool ONE = false, bool HALF = false>
@@ -986,7 +985,7 @@ hipError_t go(const ProductArgs& p, const Plan& plan, hipStream_t s) {
     case STREAM16: go_stream<K, SUB, ONE, 1>(p, s); break;
     case STREAM32: go_stream<K, SUB, ONE, 2>(p, s); break;
     case STREAM64: go_stream<K, SUB, ONE, 4>(p, s); break;
-    case TILE64: go_tiles<K, SUB, ONE, HALF, KS, 2 * WHOLE_ROWS, 2 / WHOLE_ROWS, 2 / WHOLE_ROWS, 2 * WHOLE_ROWS, SUB < 2 ? 4 : 1>(p, s); break;
+    case TILE64: go_tiles<K, SUB, ONE, HALF, KS, 2 * WHOLE_ROWS, 2 / WHOLE_ROWS, 2 / WHOLE_ROWS, 2 * WHOLE_ROWS, SUB < 2 ? 2 : 1>(p, s); break;
     case TILE128: go_tiles<K, SUB, ONE, HALF, KS256, 4 * WHOLE_ROWS, 4 / WHOLE_ROWS, 2 / WHOLE_ROWS, 2 * WHOLE_ROWS, SUB < 2 ? 3 : 1>(p, s); break;
     case TILE256:
       if constexpr (SUB < 2 && K != KNV) go_tiles<K, SUB, ONE, HALF, KS256, 8, 4, 2, 4, 2>(p, s);

@@ -72,7 +72,7 @@ int rhtq_products_version(void) { return RHTQ_PRODUCTS_VERSION; }
 int64_t rhtq_matmul_workspace(int64_t tokens, int32_t n, int64_t rows, int a_fmt) {
   if (tokens <= 0 || n <= 0 || rows <= 0 || tokens > kMostTokens || rows > kMostRows || n > kMostWidth || tokens * rows > kMostResults) return 0;
   const int64_t parts = rhtq::product_splits(tokens, n, rows, a_fmt);
-  return parts > 1 ? (4 * parts * tokens * rows + 15) / 16 * 16 : 0;
+  return parts > 1 ? 4 * parts * tokens * ((rows + 3) / 4 * 4) : 0;
 }
 
 int rhtq_matmul(const rhtq_rows_t* a, int64_t tokens, int32_t n, const rhtq_rows_t* w, int64_t rows, void* y_out, int out_dtype,

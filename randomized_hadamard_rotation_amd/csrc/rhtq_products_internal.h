@@ -24,7 +24,7 @@ struct ProductArgs {
   RowsArgs a;                 // activations: y's rows
   RowsArgs w;                 // weights: y's columns
   void* y;
-  float* partial;             // sums of the parts of k, [k_splits][tokens][rows]
+  float* partial;             // sums of the parts of k, [k_splits][tokens][rows up to the next multiple of 4]
   const int32_t* starts;      // grouped: [experts + 1], else null
   const int32_t* index;       // grouped: row of a for each row of y, or null
   int64_t tokens;             // rows of y
