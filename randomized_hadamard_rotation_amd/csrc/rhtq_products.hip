@@ -344,6 +344,11 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t all, int row_tiles
   rt = in / height;
 }
 
+// What bounds it: 8192 x 12288 x 4096 MXFP4, 221 us, 3.7 PFLOP/s of 6.9 that its instruction alone reaches on random codes -- a step of 256 x 256 is 1024
+// clocks of matrix instructions and 1024 of LDS (96 KB read, 32 KB written), which overlap in part.  INT4 in groups of 128 on both sides, 2048 x 4096 x
+// 12288, 118 us, 1.7 POP/s of 3.85: a tile of 16 x 16 x 128 takes 56 clocks of vector instructions (codes to bytes, sums to scaled floats), 32 of matrix
+// ones.  NVFP4, 2047 x 4096 x 11008, 161 us, 1.15 PFLOP/s of 1.9: 72 clocks (codes times scales to fp16) beside 64.
+//
 // FR x FT tiles of 16 weight rows x 16 tokens a wave, WR x WT waves.  A stage is KS steps (two where a row's 128 bytes fit: whole cache lines);
 // two stages' codes lie in LDS, one being worked on, the next on its way.  Scales come for a block of two stages at a time, so that a row's are
 // one request, a block ahead.  WA row tiles' codes are read from LDS ahead of their products.
@@ -923,10 +928,10 @@ struct Plan {
 
 // From sizes alone.  Up to 64 rows of y an expert (on average) the weights' bytes count: each is read once.  Beyond, the tile whose rounds over the chip
 // cost least: a round of 256 tiles of 256 x 256 counts 1, one of 512 tiles of 128 x 128 (two a CU) 0.65, one of 1024 tiles of 64 x 64 0.42.
-// 8192 x 12288 x 4096 MXFP4 took 255, 307 and 424 us in these forms (6, 7.8 and 10.1 by the rule), 2048 x 12288 x 4096 INT4 111, 91 and 121 (2, 1.95
-// and 2.5), 512 x 4096 x 4096 MXFP4 33, 17 and 13.5 (1, 0.65 and 0.42).  NVFP4's operands take too many registers for the largest.
+// 8192 x 12288 x 4096 MXFP4 took 214, 251 and 385 us in these forms (6, 7.8 and 10.1 by the rule), 2048 x 12288 x 4096 INT4 102, 85 and 119 (2, 1.95
+// and 2.5), 512 x 4096 x 4096 MXFP4 29, 16 and 12.7 (1, 0.65 and 0.42).  NVFP4's operands take too many registers for the largest.
 // Small tiles that leave half the chip's room empty share k among several workgroups, with 16 stages each at least and up to 32 MB of
-// partial sums: 333 x 4001 x 11008 MXFP8 48 instead of 56 us; 512 x 4096 x 4096 INT4, eight stages each, would take 31 instead of 20.
+// partial sums: 333 x 4001 x 11008 MXFP8 39 instead of 43 us; 512 x 4096 x 4096 INT4, eight stages each, would take 28 instead of 18.5.
 Plan plan_of(int64_t tokens, int32_t n, int64_t rows, int32_t experts, bool grouped, int a_fmt) {
   const int64_t each = (tokens + experts - 1) / experts;
   if (each <= 16) return {STREAM16, 1};
