@@ -63,6 +63,10 @@ KERNEL_SOURCES = ["randomized_hadamard_rotation_amd/csrc/rhtq_fast.hip",
                   "randomized_hadamard_rotation_amd/csrc/rhtq_serving_api.cpp",
                   "randomized_hadamard_rotation_amd/csrc/rhtq_serving_device.h",
                   "randomized_hadamard_rotation_amd/csrc/rhtq_serving_internal.h",
+                  "randomized_hadamard_rotation_amd/csrc/rhtq_norm.hip",
+                  "randomized_hadamard_rotation_amd/csrc/rhtq_products.hip",
+                  "randomized_hadamard_rotation_amd/csrc/rhtq_products_api.cpp",
+                  "randomized_hadamard_rotation_amd/csrc/rhtq_products_internal.h",
                   "randomized_hadamard_rotation_amd/build.py"]   # compiler flags shape the kernels too
 
 

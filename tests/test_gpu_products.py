@@ -539,3 +539,53 @@ def test_block_scales_of_the_whole_range(fmt, tokens):
     ra, rw = (ca, sa, None), (cw, sw, None)
     y = R.rhtq_matmul(to_rows(ra, fmt), to_rows(rw, "mxfp4"), out_dtype=torch.float32)
     expect(y, M.values(*ra, fmt), M.values(*rw, "mxfp4"), "f32")
+
+
+def random_on_gpu(shape, fmt, group, g):
+    """Rows of random codes made on the GPU, scales fp16 or E8M0, as RhtqRows."""
+    *lead, n = shape
+    wide = fmt in ("int8", "mxfp8")
+    codes = torch.randint(0, 256, (*lead, n if wide else n // 2), device="cuda", dtype=torch.uint8, generator=g)
+    if fmt == "mxfp4":
+        scales = torch.randint(120, 132, (*lead, n // 32), device="cuda", dtype=torch.uint8, generator=g)
+    else:
+        scales = torch.rand(*lead, n // (group or n), device="cuda", generator=g).mul_(0.1).add_(0.01).half()
+    return R.RhtqRows(codes.view(torch.int8) if fmt == "int8" else codes, scales, None, fmt, group)
+
+
+def values_of(rows, *at):
+    return M.values(*(t[at].cpu() for t in (rows.codes, rows.scales)), None, rows.fmt).cuda()
+
+
+@pytest.mark.parametrize("each", [1, 65])
+@pytest.mark.parametrize("a,w,group", [("mxfp4", "mxfp4", 0), ("int8", "int4", 128)])
+def test_weights_beyond_4_gib(each, a, w, group):
+    """Three experts of 2 GiB of codes each, few tokens and tiles: the first and the last rows of every expert."""
+    n, rows, experts = 4096, 1 << 20, 3
+    g = torch.Generator("cuda").manual_seed(3)
+    rw, ra = random_on_gpu((experts, rows, n), w, group, g), random_on_gpu((experts * each, n), a, 0, g)
+    starts = torch.arange(0, experts * each + 1, each, dtype=torch.int32, device="cuda")
+    y = R.rhtq_grouped_matmul(ra, rw, starts, out_dtype=torch.bfloat16)
+    for e in range(experts):
+        for part in (slice(0, 300), slice(rows - 300, rows)):
+            expect_on_gpu(y[e * each:(e + 1) * each, part], values_of(ra, slice(e * each, (e + 1) * each)), values_of(rw, e, part), "bf16")
+
+
+@pytest.mark.parametrize("tokens", [3, 70])
+def test_rows_taken_from_beyond_4_gib(tokens):
+    n, a_rows = 4096, (1 << 21) + 100
+    g = torch.Generator("cuda").manual_seed(4)
+    ra, rw = random_on_gpu((a_rows, n), "int4", 0, g), random_on_gpu((1, 40, n), "int4", 0, g)
+    index = torch.arange(a_rows - tokens, a_rows, dtype=torch.int32, device="cuda")
+    y = R.rhtq_grouped_matmul(ra, rw, torch.tensor([0, tokens], dtype=torch.int32, device="cuda"), index, out_dtype=torch.float32)
+    expect_on_gpu(y, values_of(ra, slice(a_rows - tokens, a_rows)), values_of(rw, 0), "f32")
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_results_beyond_4_gib(out):
+    n, tokens, rows = 32, 2200, (1 << 20) + 8
+    g = torch.Generator("cuda").manual_seed(5)
+    ra, rw = random_on_gpu((tokens, n), "mxfp4", 0, g), random_on_gpu((rows, n), "mxfp4", 0, g)
+    y = R.rhtq_matmul(ra, rw, out_dtype=OUT[out])
+    for part in (slice(0, 300), slice(rows - 300, rows)):
+        expect_on_gpu(y[tokens - 300:, part], values_of(ra, slice(tokens - 300, tokens)), values_of(rw, part), out)
