@@ -79,11 +79,11 @@ int rhtq_grouped_matmul(const rhtq_rows_t* a, int64_t a_rows, int64_t tokens, in
  *   codes_out, scales_out: y in `fmt` (INT4, NVFP4, MXFP4 as rhtq_forward, INT8, MXFP8 as above; a zero group: scale 0, E8M0 byte 0,
  *   codes 0).  tensor_scale (NVFP4) is read: a scale over all rows would need them twice.
  *   x, residual, residual_out  [tokens][n] bf16, fp16 or fp32, rows contiguous, 16-byte aligned; residual_out may be residual or x
- * n: a multiple of 32 up to 32768; block a power of two, 16 to n, dividing n; groups lie inside a block (INT4 and INT8 group 0, one a
- * row: any block) and, where they are not one a row, hold up to 32768 values.  eps is finite and not negative.  The mean, the norm and
- * the rotation are in fp32.  A row of h with a value that is not finite, or whose sum of squares is not in fp32, has NaN scales (INT4 and INT8
- * NaN, E8M0 0xFF, E4M3 0x7F), and so has a group of y with such a value; their codes are unspecified.  Where the mean in fp32 and eps are both
- * zero, y is zero.
+ * tokens up to 2^22 - 1; n: a multiple of 32 up to 32768; block a power of two, 16 to n, dividing n; groups lie inside a block (INT4 and
+ * INT8 group 0, one a row: any block) and, where they are not one a row, hold up to 32768 values.  eps is finite and not negative.  The
+ * mean, the norm and the rotation are in fp32.  A row of h with a value that is not finite, or whose sum of squares is not in fp32, has
+ * NaN scales (INT4 and INT8 NaN, E8M0 0xFF, E4M3 0x7F), and so has a group of y with such a value; their codes are unspecified.  Where the
+ * mean in fp32 and eps are both zero, y is zero.
  */
 int rhtq_norm_forward(const void* x, const void* residual, void* residual_out, int in_dtype, int64_t tokens, int32_t n, const void* weight,
                       float eps, const int8_t* signs, int32_t block, int fmt, int32_t group, int scale_dtype, void* codes_out,
